@@ -41,7 +41,7 @@ typedef enum {
   SMLA_ERR_DEVICE_CHECK = 5  /* an index / page id was out of range (device error word) */
 } smla_status_t;
 
-enum { SMLA_BF16 = 0, SMLA_E4M3 = 1 };
+enum { SMLA_BF16 = 0, SMLA_E4M3 = 1, SMLA_F32 = 2 };
 
 /* Ragged batch of B sequences over a paged cache (all pointers on the device).
  * Sequence b owns query tokens cu_q[b] .. cu_q[b+1]-1 and kv_len[b] cached
@@ -253,6 +253,100 @@ smla_status_t smla_sparse_decode_noalloc(const void* q, int32_t q_dtype, const u
                                          const uint32_t* topk_lengths, int32_t T, int32_t H,
                                          int32_t v_depth, float softmax_scale, const float* attn_sink,
                                          uint16_t* out, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Around the attention calls: rotary positions, the caches' write and read
+ * side, attention in the expanded form, and dense decode.  In all of them a
+ * token's position is the one smla_seqs_t gives it, and tokens behind the
+ * last sequence (t >= cu_q[B], as in a batch padded to a fixed T) are
+ * skipped: their outputs are left as they were.
+ * ------------------------------------------------------------------------ */
+
+enum { SMLA_ROPE_INTERLEAVED = 0, SMLA_ROPE_HALF = 1 };
+enum { SMLA_ROPE_PLAIN = 0, SMLA_ROPE_LINEAR = 1, SMLA_ROPE_YARN = 2 };
+
+/* A rotary embedding over columns [offset, offset + dim) of a row: pair i of
+ * the dim / 2 pairs is turned by pos * inv_freq[i] radians and multiplied by
+ * `amplitude`,
+ *   (p, q) -> amplitude * (p cos - q sin, q cos + p sin),
+ * where (p, q) are the part's columns (2i, 2i+1) (SMLA_ROPE_INTERLEAVED) or
+ * (i, i + dim/2) (SMLA_ROPE_HALF).  The angle is formed in 64-bit fixed
+ * point, so it is as exact at position 2^31 as at position 0.
+ * offset and dim are multiples of 8 and 16; dim = 0 turns nothing. */
+typedef struct {
+  const double* inv_freq;  /* device, f64 [dim/2], finite, 8-byte aligned */
+  int32_t offset;
+  int32_t dim;
+  int32_t layout;          /* SMLA_ROPE_INTERLEAVED or SMLA_ROPE_HALF */
+  float amplitude;
+} smla_rope_t;
+
+/* Host helper (no device work): the frequencies f_i = base^(-2i/dim) of a
+ * rotary embedding, scaled for contexts longer than the model was trained
+ * on, into inv_freq (host, f64 [dim/2]) and *amplitude.
+ *   SMLA_ROPE_PLAIN   as they are
+ *   SMLA_ROPE_LINEAR  every f_i / factor (position interpolation)
+ *   SMLA_ROPE_YARN    f_i kept where the pair makes more than beta_fast turns
+ *                     over original_len positions, f_i / factor where fewer
+ *                     than beta_slow, a linear ramp over i between;
+ *                     amplitude = 0.1 ln(factor) + 1
+ * dim: even, 2..1024; base > 1; factor >= 1; original_len >= 1 and
+ * beta_fast > beta_slow > 0 for YARN (ignored otherwise). */
+smla_status_t smla_rope_frequencies(int32_t dim, double base, int32_t scaling, double factor, int32_t original_len,
+                                    double beta_fast, double beta_slow, double* inv_freq, float* amplitude);
+
+/* Rotary positions of x [T, H, D] (T = seqs.T) into out [T, H, D]: the
+ * columns outside the rotated part are copied; everything is converted to
+ * out's type with one rounding (e4m3: to nearest even, values beyond +-448
+ * become +-448).
+ *   x    bf16 or f32, element (t, h, c) at x[t * x_token_stride + h * x_head_stride + c]
+ *   out  bf16, f32 or e4m3, likewise; either x itself (same pointer, type and
+ *        strides: rotated in place) or memory that x does not overlap
+ * D: a multiple of 8, 16..1024.  H: 1..65535.  Strides: in elements,
+ * multiples of 8.  Alignment: x and out 16 bytes (out e4m3: 8).
+ * Reads only cu_q and kv_len of seqs (page_table may be any valid pointer). */
+smla_status_t smla_rope(const void* x, int32_t x_dtype, int64_t x_token_stride, int64_t x_head_stride,
+                        smla_seqs_t seqs, int32_t H, int32_t D, smla_rope_t rope, void* out, int32_t out_dtype,
+                        int64_t out_token_stride, int64_t out_head_stride, cudaStream_t stream);
+
+/* Writes the batch's new rows into a paged cache (the MLA latents, D = 576,
+ * or the indexer keys, D = 128): for each token t of seqs
+ *   r = x[t];  r[0:norm_dim] = r[0:norm_dim] * rsqrt(mean(r[0:norm_dim]^2) + norm_eps) * norm_weight
+ *   r = rope(r) at pos(t)
+ *   pool[phys(pos(t))] = r in the cache's format, rows_out[t] = bf16(r)
+ * Formats: bf16 (scale_block_size 0), or e4m3 with scale_block_size 0 (unit
+ * scale, values beyond +-448 become +-448), >= D (one scale per row) or 32
+ * (D / 32 block scales per row), where scale = largest finite magnitude /
+ * 448 (1 when that is 0; at least the smallest normal f32), byte = e4m3(r /
+ * scale).  NaN stays NaN and infinities saturate.
+ *   x            bf16 [T, D], rows x_stride elements apart
+ *   norm_weight  bf16 [norm_dim], or NULL for no norm (norm_dim is then ignored)
+ *   rope         dim = 0 for none; its columns may overlap the normalised ones
+ *   pool         [phys_rows, D] (output)
+ *   scales       f32 [phys_rows, D / min(scale_block_size, D)] (output), NULL
+ *                when scale_block_size == 0
+ *   rows_out     bf16 [T, D], rows rows_stride elements apart, or NULL; not
+ *                overlapping x
+ * D: a multiple of 8 (of 32 for block scales), 16..1024; norm_dim a multiple
+ * of 8 up to D; x_stride and rows_stride multiples of 8, >= D.  Alignment:
+ * x, norm_weight, pool, rows_out 16 bytes; scales 4.  A token whose page lies
+ * outside the pool is reported (SMLA_ERR_DEVICE_CHECK) and not written.  No
+ * two tokens of a call may share a physical row. */
+smla_status_t smla_cache_append(const uint16_t* x, int64_t x_stride, smla_seqs_t seqs, int32_t D,
+                                const uint16_t* norm_weight, int32_t norm_dim, float norm_eps, smla_rope_t rope,
+                                void* pool, int32_t pool_dtype, int64_t phys_rows, float* scales,
+                                int32_t scale_block_size, uint16_t* rows_out, int64_t rows_stride,
+                                cudaStream_t stream);
+
+/* Reads cached rows back: rows[t] = bf16(pool[phys(pos(t))] * scale) for each
+ * token t of seqs.  With cu_q the running sum of kv_len (every q_len =
+ * kv_len) this is the whole cached context of the batch, sequence after
+ * sequence, as the expansion of a chunk's context needs it.  pool, scales,
+ * phys_rows, D, formats and alignment as smla_cache_append; rows bf16 [T, D],
+ * rows_stride elements apart. */
+smla_status_t smla_cache_gather(const void* pool, int32_t pool_dtype, int64_t phys_rows, const float* scales,
+                                int32_t scale_block_size, smla_seqs_t seqs, int32_t D, uint16_t* rows,
+                                int64_t rows_stride, cudaStream_t stream);
 
 /* Synchronises `stream`, then reads and clears the current device's error
  * word.  Returns SMLA_OK, SMLA_ERR_DEVICE_CHECK (out-of-range index or page

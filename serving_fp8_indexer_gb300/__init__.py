@@ -25,3 +25,12 @@ from ._lib import (  # noqa: F401
     version,
     load,
 )
+from ._latent import (  # noqa: F401
+    ROPE_HALF,
+    ROPE_INTERLEAVED,
+    Rope,
+    cache_append,
+    cache_gather,
+    rope,
+    rope_frequencies,
+)

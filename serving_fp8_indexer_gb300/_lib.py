@@ -23,11 +23,12 @@ STATUS_NAMES = {0: "SMLA_OK", 1: "SMLA_ERR_INVALID_ARG", 2: "SMLA_ERR_UNSUPPORTE
                 4: "SMLA_ERR_TIMEOUT", 5: "SMLA_ERR_DEVICE_CHECK"}
 SMLA_BF16 = 0
 SMLA_E4M3 = 1
+SMLA_F32 = 2
 
 EXPORTED = ("smla_indexer_scores", "smla_topk_workspace_size", "smla_topk", "smla_indexer_topk_workspace_size",
             "smla_indexer_topk", "smla_sparse_prefill",
             "smla_sparse_prefill_bf16_cache", "smla_dense_prefill", "smla_sparse_decode_workspace_size", "smla_sparse_decode",
-            "smla_sparse_decode_noalloc",
+            "smla_sparse_decode_noalloc", "smla_rope_frequencies", "smla_rope", "smla_cache_append", "smla_cache_gather",
             "smla_check_device_errors", "smla_selftest_wait_timeout", "smla_last_error", "smla_version")
 
 
@@ -41,6 +42,11 @@ class SeqsT(ctypes.Structure):
     _fields_ = [("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
                 ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("T", ctypes.c_int32)]
+
+
+class RopeT(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("offset", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float)]
 
 
 _lib = None
@@ -77,6 +83,11 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.smla_sparse_decode_noalloc.argtypes = [vp, i32, vp, i64, vp, i32, vp, i32, vp, i32, i32, i32, f32, vp,
                                                    vp, vp]
         lib.smla_sparse_prefill.argtypes = [vp, i32, vp, i64, vp, i32, vp, i32, vp, i32, i32, i32, f32, vp, vp, vp]
+        f64 = ctypes.c_double
+        lib.smla_rope_frequencies.argtypes = [i32, f64, i32, f64, i32, f64, f64, vp, vp]
+        lib.smla_rope.argtypes = [vp, i32, i64, i64, SeqsT, i32, i32, RopeT, vp, i32, i64, i64, vp]
+        lib.smla_cache_append.argtypes = [vp, i64, SeqsT, i32, vp, i32, f32, RopeT, vp, i32, i64, vp, i32, vp, i64, vp]
+        lib.smla_cache_gather.argtypes = [vp, i32, i64, vp, i32, SeqsT, i32, vp, i64, vp]
         lib.smla_check_device_errors.argtypes = [vp]
         lib.smla_last_error.argtypes = [ctypes.c_char_p, ctypes.c_size_t]
         lib.smla_last_error.restype = ctypes.c_size_t
@@ -84,7 +95,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         for name in ("smla_indexer_scores", "smla_topk", "smla_indexer_topk", "smla_sparse_prefill",
                      "smla_sparse_prefill_bf16_cache",
                      "smla_dense_prefill",
-                     "smla_sparse_decode", "smla_sparse_decode_noalloc", "smla_check_device_errors",
+                     "smla_sparse_decode", "smla_sparse_decode_noalloc", "smla_rope_frequencies", "smla_rope",
+                     "smla_cache_append", "smla_cache_gather", "smla_check_device_errors",
                      "smla_selftest_wait_timeout"):
             getattr(lib, name).restype = ctypes.c_int
         if path is None:

@@ -32,6 +32,8 @@ smla_status_t fail(smla_status_t st, const char* fmt, ...) {
   return st;
 }
 
+void clear_last_error() { g_last_error.clear(); }
+
 smla_status_t fail_cuda(cudaError_t e, const char* what) {
   return fail(SMLA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
@@ -80,7 +82,7 @@ bool encode_tma_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64
   return encode_tma_u8(map, base, 2, dims, strides, box, swizzle_bytes);
 }
 
-static smla_status_t device_err_ptr(unsigned** out) {
+smla_status_t device_err_ptr(unsigned** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fail_cuda(e, "cudaGetDevice");
@@ -121,10 +123,7 @@ __global__ void selftest_wait_kernel(unsigned* err, unsigned long long limit_ns)
   }
 }
 
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-static smla_status_t check_seqs(const smla_seqs_t& s) {
+smla_status_t check_seqs(const smla_seqs_t& s) {
   if (s.T < 0 || s.B < 0) return fail(SMLA_ERR_INVALID_ARG, "seqs: T=%d B=%d must be >= 0", s.T, s.B);
   if (s.T == 0) return SMLA_OK;
   if (s.B < 1) return fail(SMLA_ERR_INVALID_ARG, "seqs: B must be >= 1 when T > 0");

@@ -1,0 +1,184 @@
+// The C ABI of the operators around the attention calls (include/smla.h):
+// host-side argument validation and dispatch to their launchers.
+#include <cmath>
+
+#include "smla_internal.h"
+
+namespace smla {
+
+static smla_status_t check_rope(const smla_rope_t& r, int32_t D) {
+  if (r.dim == 0) return SMLA_OK;
+  if (r.layout != SMLA_ROPE_INTERLEAVED && r.layout != SMLA_ROPE_HALF)
+    return fail(SMLA_ERR_INVALID_ARG, "rope: layout=%d", r.layout);
+  if (r.dim < 0 || r.offset < 0 || r.offset > D || r.dim > D - r.offset)
+    return fail(SMLA_ERR_INVALID_ARG, "rope: columns [%d, +%d) outside a row of %d", r.offset, r.dim, D);
+  if (r.dim % 16 || r.offset % 8)
+    return fail(SMLA_ERR_UNSUPPORTED, "rope: dim=%d must be a multiple of 16, offset=%d of 8", r.dim, r.offset);
+  if (!r.inv_freq || (reinterpret_cast<uintptr_t>(r.inv_freq) & 7u))
+    return fail(SMLA_ERR_INVALID_ARG, "rope: inv_freq must be non-null and 8-byte aligned");
+  if (!std::isfinite(r.amplitude)) return fail(SMLA_ERR_INVALID_ARG, "rope: amplitude must be finite");
+  return SMLA_OK;
+}
+
+static smla_status_t check_row_width(int32_t D) {
+  if (D < 16 || D > 1024 || D % 8)
+    return fail(SMLA_ERR_UNSUPPORTED, "D=%d must be a multiple of 8 in [16, 1024]", D);
+  return SMLA_OK;
+}
+
+static smla_status_t check_cache(const void* pool, int32_t pool_dtype, int64_t phys_rows, const float* scales,
+                                 int32_t sbs, int32_t D, bool any) {
+  const smla_status_t st = check_row_width(D);
+  if (st != SMLA_OK) return st;
+  if (pool_dtype != SMLA_BF16 && pool_dtype != SMLA_E4M3)
+    return fail(SMLA_ERR_INVALID_ARG, "pool_dtype=%d must be bf16 or e4m3", pool_dtype);
+  if (!(sbs == 0 || sbs == 32 || sbs >= D))
+    return fail(SMLA_ERR_UNSUPPORTED, "scale_block_size=%d: supported 0, 32 or >= D", sbs);
+  if (pool_dtype == SMLA_BF16 && sbs != 0)
+    return fail(SMLA_ERR_INVALID_ARG, "a bf16 cache takes scale_block_size 0");
+  if (sbs == 32 && D % 32) return fail(SMLA_ERR_UNSUPPORTED, "block scales need D=%d to be a multiple of 32", D);
+  if (sbs != 0 && !scales) return fail(SMLA_ERR_INVALID_ARG, "scales is NULL with scale_block_size != 0");
+  if (!any) return SMLA_OK;
+  if (!pool) return fail(SMLA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(pool) || (scales && !aligned4(scales)))
+    return fail(SMLA_ERR_INVALID_ARG, "pool must be 16-byte aligned; scales 4-byte aligned");
+  if (phys_rows < 1 || phys_rows >= (int64_t(1) << 31))
+    return fail(SMLA_ERR_INVALID_ARG, "phys_rows=%lld out of range", static_cast<long long>(phys_rows));
+  return SMLA_OK;
+}
+
+static bool stride8(int64_t s) { return (s & 7) == 0; }
+
+}  // namespace smla
+
+using namespace smla;
+
+extern "C" {
+
+smla_status_t smla_rope_frequencies(int32_t dim, double base, int32_t scaling, double factor, int32_t original_len,
+                                    double beta_fast, double beta_slow, double* inv_freq, float* amplitude) {
+  clear_last_error();
+  if (dim < 2 || dim > 1024 || dim % 2) return fail(SMLA_ERR_INVALID_ARG, "dim=%d must be even, in [2, 1024]", dim);
+  if (!(base > 1.0) || !std::isfinite(base)) return fail(SMLA_ERR_INVALID_ARG, "base must be finite and > 1");
+  if (scaling != SMLA_ROPE_PLAIN && scaling != SMLA_ROPE_LINEAR && scaling != SMLA_ROPE_YARN)
+    return fail(SMLA_ERR_INVALID_ARG, "scaling=%d", scaling);
+  if (!inv_freq || !amplitude) return fail(SMLA_ERR_INVALID_ARG, "null pointer");
+  if (scaling != SMLA_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return fail(SMLA_ERR_INVALID_ARG, "factor must be finite and >= 1");
+  double low = 0, high = 0;
+  if (scaling == SMLA_ROPE_YARN) {
+    if (original_len < 1) return fail(SMLA_ERR_INVALID_ARG, "original_len=%d must be >= 1", original_len);
+    if (!(beta_slow > 0.0) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast))
+      return fail(SMLA_ERR_INVALID_ARG, "beta_fast > beta_slow > 0 is required");
+    // pair i makes original_len * base^(-2i/dim) / (2 pi) turns over the
+    // original length; solved for the i that makes `turns`
+    const auto pair_at = [&](double turns) {
+      return dim * std::log(original_len / (turns * 6.283185307179586)) / (2.0 * std::log(base));
+    };
+    low = std::fmax(std::floor(pair_at(beta_fast)), 0.0);
+    high = std::fmin(std::ceil(pair_at(beta_slow)), dim - 1.0);
+  }
+  for (int i = 0; i < dim / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / dim);
+    double ramp = 0.0;  // share of the interpolated frequency
+    if (scaling == SMLA_ROPE_LINEAR) ramp = 1.0;
+    if (scaling == SMLA_ROPE_YARN) ramp = std::fmin(1.0, std::fmax(0.0, (i - low) / std::fmax(high - low, 1e-3)));
+    inv_freq[i] = scaling == SMLA_ROPE_PLAIN ? f : f / factor * ramp + f * (1.0 - ramp);
+  }
+  *amplitude = scaling == SMLA_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  return SMLA_OK;
+}
+
+smla_status_t smla_rope(const void* x, int32_t x_dtype, int64_t x_token_stride, int64_t x_head_stride,
+                        smla_seqs_t seqs, int32_t H, int32_t D, smla_rope_t rope, void* out, int32_t out_dtype,
+                        int64_t out_token_stride, int64_t out_head_stride, cudaStream_t stream) {
+  clear_last_error();
+  smla_status_t st = check_seqs(seqs);
+  if (st != SMLA_OK) return st;
+  st = check_row_width(D);
+  if (st != SMLA_OK) return st;
+  if (H < 1 || H > 65535) return fail(SMLA_ERR_UNSUPPORTED, "H=%d must be in [1, 65535]", H);
+  if (x_dtype != SMLA_BF16 && x_dtype != SMLA_F32) return fail(SMLA_ERR_INVALID_ARG, "x_dtype=%d", x_dtype);
+  if (out_dtype != SMLA_BF16 && out_dtype != SMLA_F32 && out_dtype != SMLA_E4M3)
+    return fail(SMLA_ERR_INVALID_ARG, "out_dtype=%d", out_dtype);
+  st = check_rope(rope, D);
+  if (st != SMLA_OK) return st;
+  if (!stride8(x_token_stride) || !stride8(x_head_stride) || !stride8(out_token_stride) || !stride8(out_head_stride))
+    return fail(SMLA_ERR_INVALID_ARG, "strides must be multiples of 8 elements");
+  if (seqs.T == 0) return SMLA_OK;
+  if (!x || !out) return fail(SMLA_ERR_INVALID_ARG, "null pointer");
+  const uintptr_t out_mask = out_dtype == SMLA_E4M3 ? 7u : 15u;
+  if (!aligned16(x) || (reinterpret_cast<uintptr_t>(out) & out_mask))
+    return fail(SMLA_ERR_INVALID_ARG, "x and out must be 16-byte aligned (e4m3 out: 8)");
+  if (x == out && (x_dtype != out_dtype || x_token_stride != out_token_stride || x_head_stride != out_head_stride))
+    return fail(SMLA_ERR_INVALID_ARG, "in place, out must have x's type and strides");
+  unsigned* err = nullptr;
+  st = device_err_ptr(&err);
+  if (st != SMLA_OK) return st;
+  const RopeArgs a{x, x_dtype, x_token_stride, x_head_stride, H, D, rope, out, out_dtype, out_token_stride,
+                   out_head_stride};
+  return launch_rope(a, seqs, err, stream);
+}
+
+smla_status_t smla_cache_append(const uint16_t* x, int64_t x_stride, smla_seqs_t seqs, int32_t D,
+                                const uint16_t* norm_weight, int32_t norm_dim, float norm_eps, smla_rope_t rope,
+                                void* pool, int32_t pool_dtype, int64_t phys_rows, float* scales,
+                                int32_t scale_block_size, uint16_t* rows_out, int64_t rows_stride,
+                                cudaStream_t stream) {
+  clear_last_error();
+  smla_status_t st = check_seqs(seqs);
+  if (st != SMLA_OK) return st;
+  st = check_cache(pool, pool_dtype, phys_rows, scales, scale_block_size, D, seqs.T > 0);
+  if (st != SMLA_OK) return st;
+  st = check_rope(rope, D);
+  if (st != SMLA_OK) return st;
+  if (norm_weight) {
+    if (norm_dim < 8 || norm_dim > D || norm_dim % 8)
+      return fail(SMLA_ERR_UNSUPPORTED, "norm_dim=%d must be a multiple of 8 in [8, D]", norm_dim);
+    if (!(norm_eps >= 0.f) || !std::isfinite(norm_eps))
+      return fail(SMLA_ERR_INVALID_ARG, "norm_eps must be finite and >= 0");
+    if (!aligned16(norm_weight)) return fail(SMLA_ERR_INVALID_ARG, "norm_weight must be 16-byte aligned");
+  }
+  if (x_stride < D || !stride8(x_stride) || (rows_out && (rows_stride < D || !stride8(rows_stride))))
+    return fail(SMLA_ERR_INVALID_ARG, "x_stride and rows_stride must be multiples of 8, >= D");
+  if (seqs.T == 0) return SMLA_OK;
+  if (!x) return fail(SMLA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || (rows_out && !aligned16(rows_out)))
+    return fail(SMLA_ERR_INVALID_ARG, "x and rows_out must be 16-byte aligned");
+  unsigned* err = nullptr;
+  st = device_err_ptr(&err);
+  if (st != SMLA_OK) return st;
+  const CacheArgs a{x,         x_stride, D,    norm_weight, norm_dim, norm_eps, rope, pool, pool_dtype,
+                    phys_rows, scales,   scale_block_size,  rows_out, rows_stride};
+  return launch_cache_append(a, seqs, err, stream);
+}
+
+smla_status_t smla_cache_gather(const void* pool, int32_t pool_dtype, int64_t phys_rows, const float* scales,
+                                int32_t scale_block_size, smla_seqs_t seqs, int32_t D, uint16_t* rows,
+                                int64_t rows_stride, cudaStream_t stream) {
+  clear_last_error();
+  smla_status_t st = check_seqs(seqs);
+  if (st != SMLA_OK) return st;
+  st = check_cache(pool, pool_dtype, phys_rows, scales, scale_block_size, D, seqs.T > 0);
+  if (st != SMLA_OK) return st;
+  if (rows_stride < D || !stride8(rows_stride))
+    return fail(SMLA_ERR_INVALID_ARG, "rows_stride must be a multiple of 8, >= D");
+  if (seqs.T == 0) return SMLA_OK;
+  if (!rows) return fail(SMLA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(rows)) return fail(SMLA_ERR_INVALID_ARG, "rows must be 16-byte aligned");
+  unsigned* err = nullptr;
+  st = device_err_ptr(&err);
+  if (st != SMLA_OK) return st;
+  CacheArgs a{};
+  a.D = D;
+  a.pool = const_cast<void*>(pool);
+  a.pool_dtype = pool_dtype;
+  a.phys_rows = phys_rows;
+  a.scales = const_cast<float*>(scales);
+  a.sbs = scale_block_size;
+  a.rows = rows;
+  a.rows_stride = rows_stride;
+  return launch_cache_gather(a, seqs, err, stream);
+}
+
+}  // extern "C"

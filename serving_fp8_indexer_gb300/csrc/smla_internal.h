@@ -13,6 +13,13 @@ namespace smla {
 smla_status_t fail(smla_status_t st, const char* fmt, ...);
 smla_status_t fail_cuda(cudaError_t e, const char* what);
 
+// Host-side checks and lookups shared by the entry points.
+void clear_last_error();
+smla_status_t device_err_ptr(unsigned** out);
+smla_status_t check_seqs(const smla_seqs_t& s);
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // uint8 tensor map of the given rank: dims[0] innermost (elements = bytes),
 // strides[i] = byte stride of dimension i + 1, box per dimension, 64- or
 // 128-byte swizzle, zero fill out of bounds.  False when cuTensorMapEncodeTiled rejects it.
@@ -78,5 +85,39 @@ size_t noalloc_scratch_bytes();
 smla_status_t noalloc_scratch_for(size_t need, void** out);
 smla_status_t launch_decode_combine(const float* part_o, const float* part_lse, const float* sink, int T, int H,
                                     int nsplit, uint16_t* out, cudaStream_t stream);
+
+// Rotary positions of x [T, H, D] into out.
+struct RopeArgs {
+  const void* x;
+  int x_dtype;
+  int64_t x_ts, x_hs;  // token and head strides, elements
+  int H, D;
+  smla_rope_t rope;
+  void* out;
+  int out_dtype;
+  int64_t o_ts, o_hs;
+};
+smla_status_t launch_rope(const RopeArgs& a, const smla_seqs_t& seqs, unsigned* err, cudaStream_t stream);
+
+// Writing (x -> pool, optionally rows) and reading (pool -> rows) the cached
+// rows of a batch's tokens.
+struct CacheArgs {
+  const void* x;
+  int64_t x_stride;
+  int D;
+  const void* norm_weight;  // null: no norm
+  int norm_dim;
+  float norm_eps;
+  smla_rope_t rope;
+  void* pool;
+  int pool_dtype;
+  int64_t phys_rows;
+  float* scales;
+  int sbs;
+  void* rows;
+  int64_t rows_stride;
+};
+smla_status_t launch_cache_append(const CacheArgs& a, const smla_seqs_t& seqs, unsigned* err, cudaStream_t stream);
+smla_status_t launch_cache_gather(const CacheArgs& a, const smla_seqs_t& seqs, unsigned* err, cudaStream_t stream);
 
 }  // namespace smla

@@ -1,0 +1,117 @@
+"""Refusals of the operators around the attention calls, on the host: the
+library and the binding reject what the documentation does not allow before
+anything reaches a device."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from serving_fp8_indexer_gb300 import _lib, _latent
+from serving_fp8_indexer_gb300 import build as smla_build
+
+INVALID, UNSUPPORTED = 1, 2
+P = 0x10000  # an aligned fake device pointer: validation runs before any launch
+
+
+@pytest.fixture(scope="module")
+def lib():
+    smla_build.build()
+    return _lib.load()
+
+
+def _seqs(T=4, B=1, page_size=64):
+    return _lib.SeqsT(P, P, P, B, 1, page_size, T)
+
+
+def _msg(lib):
+    return _lib.last_error(lib)
+
+
+def _rope(inv=P, offset=0, dim=16, layout=0, amplitude=1.0):
+    return _lib.RopeT(inv, offset, dim, layout, amplitude)
+
+
+BAD_ROPES = [(dict(layout=2), INVALID), (dict(offset=-8), INVALID), (dict(dim=-16), INVALID), (dict(offset=56), INVALID),
+             (dict(offset=2147483640), INVALID), (dict(dim=24), UNSUPPORTED), (dict(offset=4), UNSUPPORTED),
+             (dict(inv=None), INVALID), (dict(inv=P + 4), INVALID), (dict(amplitude=math.nan), INVALID)]
+
+
+def test_frequencies_refusals(lib):
+    out, amp = (ctypes.c_double * 32)(), ctypes.c_float()
+
+    def call(dim=64, base=1e4, scaling=0, factor=2.0, length=4096, fast=32.0, slow=1.0, o=out, a=ctypes.byref(amp)):
+        return lib.smla_rope_frequencies(dim, base, scaling, factor, length, fast, slow, o, a)
+
+    assert call() == 0 and out[0] == 1.0 and amp.value == 1.0
+    for kw in (dict(dim=63), dict(dim=0), dict(dim=2000), dict(base=1.0), dict(base=math.nan), dict(base=math.inf),
+               dict(scaling=3), dict(o=None), dict(a=None), dict(scaling=1, factor=0.5), dict(scaling=2, factor=math.nan),
+               dict(scaling=2, length=0), dict(scaling=2, fast=1.0, slow=2.0), dict(scaling=2, slow=0.0)):
+        assert call(**kw) == INVALID, kw
+    with pytest.raises(ValueError):
+        _latent.rope_frequencies(64, scaling="other")
+
+
+def test_rope_refusals(lib):
+    def call(x=P, xd=0, xts=128, xhs=64, s=None, H=2, D=64, r=None, out=P + 0x10000, od=0, ots=128, ohs=64):
+        return lib.smla_rope(x, xd, xts, xhs, s or _seqs(), H, D, r or _rope(), out, od, ots, ohs, None)
+
+    for kw, st in ((dict(xd=1), INVALID), (dict(od=3), INVALID), (dict(D=12), UNSUPPORTED), (dict(D=8), UNSUPPORTED),
+                   (dict(D=2048), UNSUPPORTED), (dict(H=0), UNSUPPORTED), (dict(H=65536), UNSUPPORTED),
+                   (dict(xts=130), INVALID), (dict(ohs=4), INVALID), (dict(x=None), INVALID), (dict(out=None), INVALID),
+                   (dict(x=P + 8), INVALID), (dict(out=P + 8), INVALID), (dict(out=P + 4, od=1), INVALID),
+                   (dict(out=P, od=2), INVALID), (dict(out=P, ots=64), INVALID), (dict(s=_seqs(page_size=48)), UNSUPPORTED),
+                   (dict(s=_seqs(B=0)), INVALID)):
+        assert call(**kw) == st, kw
+    for kw, st in BAD_ROPES:
+        assert call(r=_rope(**kw)) == st and "rope" in _msg(lib), kw
+    assert call(s=_seqs(T=0), x=None, out=None) == 0
+
+
+def test_append_and_gather_refusals(lib):
+    def append(x=P, xs=64, s=None, D=64, w=None, nd=0, eps=1e-6, r=None, pool=P, pd=1, rows=64, sc=None, sbs=0, ro=None,
+               rs=64):
+        return lib.smla_cache_append(x, xs, s or _seqs(), D, w, nd, eps, r or _rope(), pool, pd, rows, sc, sbs, ro, rs,
+                                     None)
+
+    def gather(pool=P, pd=1, rows=64, sc=None, sbs=0, s=None, D=64, out=P, rs=64):
+        return lib.smla_cache_gather(pool, pd, rows, sc, sbs, s or _seqs(), D, out, rs, None)
+
+    both = ((dict(pd=2), INVALID), (dict(D=1032), UNSUPPORTED), (dict(D=20), UNSUPPORTED), (dict(sbs=16), UNSUPPORTED),
+            (dict(sbs=-1), UNSUPPORTED), (dict(sbs=32), INVALID), (dict(sbs=64, pd=0, sc=P), INVALID),
+            (dict(sbs=32, D=40, sc=P), UNSUPPORTED), (dict(pool=None), INVALID), (dict(pool=P + 8), INVALID),
+            (dict(sbs=64, sc=P + 2), INVALID), (dict(rows=0), INVALID), (dict(rows=1 << 31), INVALID),
+            (dict(s=_seqs(page_size=4)), UNSUPPORTED))
+    for kw, st in both:
+        assert append(**kw) == st and gather(**kw) == st, kw
+    for kw, st in ((dict(x=None), INVALID), (dict(x=P + 2), INVALID), (dict(xs=56), INVALID), (dict(xs=68), INVALID),
+                   (dict(ro=P, rs=63), INVALID), (dict(ro=P + 8), INVALID), (dict(w=P, nd=12), UNSUPPORTED),
+                   (dict(w=P, nd=72), UNSUPPORTED), (dict(w=P, nd=0), UNSUPPORTED), (dict(w=P, nd=64, eps=-1.0), INVALID),
+                   (dict(w=P, nd=64, eps=math.nan), INVALID), (dict(w=P + 8, nd=64), INVALID)):
+        assert append(**kw) == st, kw
+    for kw, st in BAD_ROPES:
+        assert append(r=_rope(**kw)) == st, kw
+    for kw, st in ((dict(out=None), INVALID), (dict(out=P + 8), INVALID), (dict(rs=56), INVALID), (dict(rs=65), INVALID)):
+        assert gather(**kw) == st, kw
+    assert append(s=_seqs(T=0), x=None, pool=None, rows=0) == 0
+    assert gather(s=_seqs(T=0), pool=None, out=None, rows=0) == 0
+
+
+def test_binding_refuses_host_tensors_and_wrong_layouts():
+    x = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        _latent._rows(x.half(), "x", (torch.bfloat16,), 3)
+    with pytest.raises(ValueError):
+        _latent._rows(x, "x", (torch.bfloat16,), 2)
+    with pytest.raises(ValueError):
+        _latent._rows(x.transpose(1, 2), "x", (torch.bfloat16,), 3)
+    # a dimension of one element has no stride of its own
+    assert _latent._rows(x[:1, :1], "x", (torch.bfloat16,), 3)[1] == [64, 64]
+    pool = torch.zeros((64, 64), dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        _latent._check_scales(torch.ones((64, 1)), pool, 0)
+    with pytest.raises(ValueError):
+        _latent._check_scales(torch.ones((64, 1)), pool, 32)
+    with pytest.raises(ValueError):
+        _latent._check_scales(None, pool, 64)
+    _latent._check_scales(torch.ones((64, 2)), pool, 32)
