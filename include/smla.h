@@ -348,6 +348,44 @@ smla_status_t smla_cache_gather(const void* pool, int32_t pool_dtype, int64_t ph
                                 int32_t scale_block_size, smla_seqs_t seqs, int32_t D, uint16_t* rows,
                                 int64_t rows_stride, cudaStream_t stream);
 
+/* Latent attention in the expanded form, for prefill: every head has keys and
+ * values of its own, up-projected from the latents, and all heads share the
+ * rotary part of the keys.  For token t of sequence b and head h, over the
+ * keys j = 0..pos(t) of b,
+ *   z_j = softmax_scale * (q[t,h,0:128] . k_nope[j,h] + q[t,h,128:192] . k_rope[j])
+ *   out[t,h] = bf16( sum_j p_j v[j,h] ),  p and the sink as for smla_sparse_prefill
+ *   lse[t,h] = ln( sum_j exp(z_j) [+ exp(sink_h)] )
+ * Sequence b owns query tokens cu_q[b] .. cu_q[b+1]-1 and key rows cu_kv[b]
+ * .. cu_kv[b+1]-1; its new tokens are the last of its keys, so token i sits
+ * at pos = kv_len - q_len + i.  A token that attends to nothing (no keys, or
+ * pos < 0) gets zeros, and lse -inf (the sink's logit with a sink).
+ *   q       bf16 [T, H, 192]; element (t, h, c) at q[t * q_token_stride + h * q_head_stride + c]
+ *   k_nope  bf16 [S, H, 128], v bf16 [S, H, 128]: likewise strided, so that they may be
+ *           the two halves of one up-projection's output
+ *   k_rope  bf16 [S, 64], rows k_rope_stride apart, rotated
+ *   out     bf16 [T, H, 128], dense;  lse f32 [T, H] or NULL
+ *   S       key rows in all (cu_kv[B] <= S)
+ * Key rows outside a sequence never reach its outputs, whatever they hold.
+ * Inside a sequence, a NaN or infinity in v at key j may also reach tokens of
+ * that sequence before j (within the 128-key block), which weigh it by 0.
+ * Strides: in elements, multiples of 8, at least the row's width.
+ * H: 1..65535.  softmax_scale: finite, > 0.  Alignment: q, k_nope, k_rope, v,
+ * out 16 bytes; the others 4.  workspace: caller-owned device scratch of at
+ * least smla_expanded_prefill_workspace_size(T, S, B, H) bytes on the
+ * current device (16-byte aligned; NULL when that is 0), used when the
+ * queries alone are too few to fill the GPU; contents on entry do not matter,
+ * unspecified on return; not shared by calls that may overlap.  The products
+ * run as tcgen05 kind::f16 (bf16) MMAs with f32 TMEM accumulation; P is
+ * rounded to bf16. */
+size_t smla_expanded_prefill_workspace_size(int32_t T, int32_t S, int32_t B, int32_t H);
+smla_status_t smla_expanded_prefill(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                                    const uint16_t* k_nope, int64_t k_token_stride, int64_t k_head_stride,
+                                    const uint16_t* k_rope, int64_t k_rope_stride, const uint16_t* v,
+                                    int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_q,
+                                    const int32_t* cu_kv, int32_t B, int32_t T, int32_t S, int32_t H,
+                                    float softmax_scale, const float* attn_sink, uint16_t* out, float* lse,
+                                    void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Synchronises `stream`, then reads and clears the current device's error
  * word.  Returns SMLA_OK, SMLA_ERR_DEVICE_CHECK (out-of-range index or page
  * id), SMLA_ERR_TIMEOUT (a pipeline wait gave up) or SMLA_ERR_CUDA. */

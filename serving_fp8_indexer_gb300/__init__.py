@@ -31,6 +31,8 @@ from ._latent import (  # noqa: F401
     Rope,
     cache_append,
     cache_gather,
+    expanded_prefill,
+    expanded_prefill_workspace_size,
     rope,
     rope_frequencies,
 )

@@ -150,3 +150,41 @@ def cache_gather(pool: torch.Tensor, scales: Optional[torch.Tensor], scale_block
                                int(scale_block_size), seqs.as_c(), int(rows.shape[1]), rp, rs, _stream(stream))
     _check(lib, st)
     return rows
+
+
+def expanded_prefill_workspace_size(T: int, S: int, B: int, H: int) -> int:
+    """Bytes of device scratch smla_expanded_prefill needs on the current device."""
+    return int(_lib.load().smla_expanded_prefill_workspace_size(int(T), int(S), int(B), int(H)))
+
+
+def expanded_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                     cu_kv: torch.Tensor, softmax_scale: float, out: torch.Tensor,
+                     workspace: Optional[torch.Tensor], attn_sink: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out bf16 [T, H, 128] = causal attention of q bf16 [T, H, 192] over keys
+    [k_nope [S, H, 128] | k_rope [S, 64]] and values v [S, H, 128] (bf16,
+    strided views with dense rows); cu_q, cu_kv int32 [B+1]; workspace a uint8
+    CUDA tensor of at least expanded_prefill_workspace_size() bytes (None when
+    that is 0); attn_sink f32 [H], lse f32 [T, H] (output)."""
+    lib = _lib.load()
+    bf = (torch.bfloat16,)
+    qp, (qt, qh) = _rows(q, "q", bf, 3)
+    kp, (kt, kh) = _rows(k_nope, "k_nope", bf, 3)
+    rp, (rt,) = _rows(k_rope, "k_rope", bf, 2)
+    vp, (vt, vh) = _rows(v, "v", bf, 3)
+    _here(q, k_nope, k_rope, v, cu_q, cu_kv, out, workspace, attn_sink, lse)
+    T, H, S, B = int(q.shape[0]), int(q.shape[1]), int(v.shape[0]), int(cu_q.shape[0]) - 1
+    if (tuple(q.shape) != (T, H, 192) or tuple(k_nope.shape) != (S, H, 128) or tuple(k_rope.shape) != (S, 64) or
+            tuple(v.shape) != (S, H, 128) or tuple(out.shape) != (T, H, 128) or tuple(cu_kv.shape) != (B + 1,) or
+            (attn_sink is not None and tuple(attn_sink.shape) != (H,)) or
+            (lse is not None and tuple(lse.shape) != (T, H))):
+        raise ValueError("q [T, H, 192], k_nope [S, H, 128], k_rope [S, 64], v [S, H, 128], out [T, H, 128], cu_q and "
+                         "cu_kv [B + 1], attn_sink [H], lse [T, H] do not fit each other")
+    st = lib.smla_expanded_prefill(qp, qt, qh, kp, kt, kh, rp, rt, vp, vt, vh, _ptr(cu_q, torch.int32, "cu_q", 1),
+                                   _ptr(cu_kv, torch.int32, "cu_kv", 1), B, T, S, H, float(softmax_scale),
+                                   _ptr(attn_sink, torch.float32, "attn_sink", 1),
+                                   _ptr(out, torch.bfloat16, "out", 3), _ptr(lse, torch.float32, "lse", 2),
+                                   _ptr(workspace, torch.uint8, "workspace", 1),
+                                   0 if workspace is None else int(workspace.numel()), _stream(stream))
+    _check(lib, st)
+    return out

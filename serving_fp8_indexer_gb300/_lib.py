@@ -29,6 +29,7 @@ EXPORTED = ("smla_indexer_scores", "smla_topk_workspace_size", "smla_topk", "sml
             "smla_indexer_topk", "smla_sparse_prefill",
             "smla_sparse_prefill_bf16_cache", "smla_dense_prefill", "smla_sparse_decode_workspace_size", "smla_sparse_decode",
             "smla_sparse_decode_noalloc", "smla_rope_frequencies", "smla_rope", "smla_cache_append", "smla_cache_gather",
+            "smla_expanded_prefill_workspace_size", "smla_expanded_prefill",
             "smla_check_device_errors", "smla_selftest_wait_timeout", "smla_last_error", "smla_version")
 
 
@@ -88,6 +89,10 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.smla_rope.argtypes = [vp, i32, i64, i64, SeqsT, i32, i32, RopeT, vp, i32, i64, i64, vp]
         lib.smla_cache_append.argtypes = [vp, i64, SeqsT, i32, vp, i32, f32, RopeT, vp, i32, i64, vp, i32, vp, i64, vp]
         lib.smla_cache_gather.argtypes = [vp, i32, i64, vp, i32, SeqsT, i32, vp, i64, vp]
+        lib.smla_expanded_prefill_workspace_size.argtypes = [i32, i32, i32, i32]
+        lib.smla_expanded_prefill_workspace_size.restype = sz
+        lib.smla_expanded_prefill.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, i32, i32, i32, i32,
+                                              f32, vp, vp, vp, vp, sz, vp]
         lib.smla_check_device_errors.argtypes = [vp]
         lib.smla_last_error.argtypes = [ctypes.c_char_p, ctypes.c_size_t]
         lib.smla_last_error.restype = ctypes.c_size_t
@@ -96,7 +101,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                      "smla_sparse_prefill_bf16_cache",
                      "smla_dense_prefill",
                      "smla_sparse_decode", "smla_sparse_decode_noalloc", "smla_rope_frequencies", "smla_rope",
-                     "smla_cache_append", "smla_cache_gather", "smla_check_device_errors",
+                     "smla_cache_append", "smla_cache_gather", "smla_expanded_prefill", "smla_check_device_errors",
                      "smla_selftest_wait_timeout"):
             getattr(lib, name).restype = ctypes.c_int
         if path is None:

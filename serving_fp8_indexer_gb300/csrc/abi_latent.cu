@@ -181,4 +181,50 @@ smla_status_t smla_cache_gather(const void* pool, int32_t pool_dtype, int64_t ph
   return launch_cache_gather(a, seqs, err, stream);
 }
 
+size_t smla_expanded_prefill_workspace_size(int32_t T, int32_t S, int32_t B, int32_t H) {
+  if (T <= 0 || S <= 0 || B <= 0 || H <= 0) return 0;
+  return expanded_workspace_bytes(T, H, expanded_splits(T, S, B, H));
+}
+
+smla_status_t smla_expanded_prefill(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                                    const uint16_t* k_nope, int64_t k_token_stride, int64_t k_head_stride,
+                                    const uint16_t* k_rope, int64_t k_rope_stride, const uint16_t* v,
+                                    int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_q,
+                                    const int32_t* cu_kv, int32_t B, int32_t T, int32_t S, int32_t H,
+                                    float softmax_scale, const float* attn_sink, uint16_t* out, float* lse,
+                                    void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  clear_last_error();
+  if (T < 0 || S < 0 || B < 0) return fail(SMLA_ERR_INVALID_ARG, "T=%d S=%d B=%d must be >= 0", T, S, B);
+  if (H < 1 || H > 65535) return fail(SMLA_ERR_UNSUPPORTED, "H=%d must be in [1, 65535]", H);
+  if (!(softmax_scale > 0.f) || softmax_scale < 1.0e-30f || softmax_scale > 1.0e30f)
+    return fail(SMLA_ERR_INVALID_ARG, "softmax_scale must be in [1e-30, 1e30]");
+  const auto stride_ok = [](int64_t s, int64_t width) { return s >= width && (s & 7) == 0 && s < (int64_t(1) << 38); };
+  if (!stride_ok(q_token_stride, 192) || !stride_ok(q_head_stride, 192) || !stride_ok(k_token_stride, 128) ||
+      !stride_ok(k_head_stride, 128) || !stride_ok(k_rope_stride, 64) || !stride_ok(v_token_stride, 128) ||
+      !stride_ok(v_head_stride, 128))
+    return fail(SMLA_ERR_INVALID_ARG, "strides must be multiples of 8 elements, at least the row's width");
+  if (T == 0) return SMLA_OK;
+  if (B < 1) return fail(SMLA_ERR_INVALID_ARG, "B must be >= 1 when T > 0");
+  if (!q || !cu_q || !cu_kv || !out || (S > 0 && (!k_nope || !k_rope || !v)))
+    return fail(SMLA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(q) || !aligned16(k_nope) || !aligned16(k_rope) || !aligned16(v) || !aligned16(out) ||
+      !aligned4(cu_q) || !aligned4(cu_kv) || !aligned4(attn_sink) || !aligned4(lse))
+    return fail(SMLA_ERR_INVALID_ARG,
+                "q, k_nope, k_rope, v, out must be 16-byte aligned; cu_q, cu_kv, attn_sink, lse 4-byte aligned");
+  if (static_cast<int64_t>(T) * H >= (int64_t(1) << 31)) return fail(SMLA_ERR_UNSUPPORTED, "T*H too large");
+  const int nsplit = expanded_splits(T, S, B, H);
+  const size_t need = expanded_workspace_bytes(T, H, nsplit);
+  if (workspace_bytes < need || (need && !workspace))
+    return fail(SMLA_ERR_INVALID_ARG, "workspace: %zu bytes given, %zu needed", workspace_bytes, need);
+  if (workspace && !aligned16(workspace)) return fail(SMLA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  unsigned* err = nullptr;
+  const smla_status_t st = device_err_ptr(&err);
+  if (st != SMLA_OK) return st;
+  const ExpandedArgs a{q,    q_token_stride, q_head_stride,  k_nope,        k_token_stride, k_head_stride, k_rope,
+                       k_rope_stride,        v,              v_token_stride, v_head_stride, cu_q,          cu_kv,
+                       B,    T,              S,              H,             softmax_scale,  attn_sink,     out,
+                       lse,  nsplit,         workspace};
+  return launch_expanded(a, err, stream);
+}
+
 }  // extern "C"

@@ -120,4 +120,29 @@ struct CacheArgs {
 smla_status_t launch_cache_append(const CacheArgs& a, const smla_seqs_t& seqs, unsigned* err, cudaStream_t stream);
 smla_status_t launch_cache_gather(const CacheArgs& a, const smla_seqs_t& seqs, unsigned* err, cudaStream_t stream);
 
+// Latent attention in the expanded form.  Strides in elements.
+struct ExpandedArgs {
+  const void* q;  // [T, H, 192]
+  int64_t q_ts, q_hs;
+  const void* k_nope;  // [S, H, 128]
+  int64_t k_ts, k_hs;
+  const void* k_rope;  // [S, 64]
+  int64_t r_ts;
+  const void* v;  // [S, H, 128]
+  int64_t v_ts, v_hs;
+  const int32_t* cu_q;
+  const int32_t* cu_kv;
+  int B, T, S, H;
+  float softmax_scale;
+  const float* sink;
+  uint16_t* out;
+  float* lse;
+  int nsplit;
+  void* workspace;
+};
+// Splits of the keys for these sizes, the workspace they need, the launch.
+int expanded_splits(int T, int S, int B, int H);
+size_t expanded_workspace_bytes(int T, int H, int nsplit);
+smla_status_t launch_expanded(const ExpandedArgs& a, unsigned* err, cudaStream_t stream);
+
 }  // namespace smla

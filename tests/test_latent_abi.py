@@ -115,3 +115,29 @@ def test_binding_refuses_host_tensors_and_wrong_layouts():
     with pytest.raises(ValueError):
         _latent._check_scales(None, pool, 64)
     _latent._check_scales(torch.ones((64, 2)), pool, 32)
+
+
+def test_expanded_refusals(lib):
+    def call(q=P, qt=384, qh=192, k=P, kt=512, kh=256, r=P, rt=64, v=P, vt=512, vh=256, cq=P, ck=P, B=1, T=4, S=8, H=2,
+             sc=0.1, sink=None, out=P, lse=None, ws=P, wsb=1 << 30):
+        return lib.smla_expanded_prefill(q, qt, qh, k, kt, kh, r, rt, v, vt, vh, cq, ck, B, T, S, H, sc, sink, out, lse,
+                                         ws, wsb, None)
+
+    for kw, st in ((dict(T=-1), INVALID), (dict(S=-1), INVALID), (dict(B=-1), INVALID), (dict(B=0), INVALID),
+                   (dict(H=0), UNSUPPORTED), (dict(H=65536), UNSUPPORTED), (dict(sc=0.0), INVALID),
+                   (dict(sc=-0.1), INVALID), (dict(sc=math.nan), INVALID), (dict(sc=math.inf), INVALID),
+                   (dict(qh=191), INVALID), (dict(qt=184), INVALID), (dict(kh=120), INVALID), (dict(kt=516), INVALID),
+                   (dict(rt=0), INVALID), (dict(vt=0), INVALID), (dict(vh=0), INVALID), (dict(vh=1 << 38), INVALID),
+                   (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(r=None), INVALID), (dict(v=None), INVALID),
+                   (dict(cq=None), INVALID), (dict(ck=None), INVALID), (dict(out=None), INVALID),
+                   (dict(q=P + 8), INVALID), (dict(v=P + 8), INVALID), (dict(out=P + 8), INVALID),
+                   (dict(sink=P + 2), INVALID), (dict(lse=P + 1), INVALID), (dict(cq=P + 2), INVALID),
+                   (dict(T=1 << 25, H=64), UNSUPPORTED)):
+        assert call(**kw) == st, kw
+    need = lib.smla_expanded_prefill_workspace_size(1, 8192, 1, 1)
+    assert need > 0
+    assert call(T=1, S=8192, H=1, wsb=need - 1) == INVALID and "workspace" in _msg(lib)
+    assert call(T=1, S=8192, H=1, ws=None, wsb=0) == INVALID
+    assert call(T=1, S=8192, H=1, ws=P + 8) == INVALID and "aligned" in _msg(lib)
+    assert call(T=0, B=0, q=None, k=None, r=None, v=None, cq=None, ck=None, out=None) == 0
+    assert lib.smla_expanded_prefill_workspace_size(0, 1, 1, 1) == 0
