@@ -19,9 +19,10 @@
 //
 // The keys are never concatenated: a K tile's three 64-column chunks come
 // from k_nope (two) and k_rope (one) by TMA, straight from the up-projection's
-// output.  Two K tiles and one V tile fit beside Q (224 KB); V is handed back
-// and refilled by 64-key halves, so that the next half's load is under way
-// while the other half and the next QK run.
+// output.  Beside Q (96 KB), 128 KB hold two V tiles and a ring of four K
+// chunks (a K tile is three): every chunk and tile is loaded at least 1280
+// cycles of tensor work before it is read.  (Two whole K tiles and one V tile
+// left V a third less, and PV waited for it.)
 //
 // A row's reference m is raised only when a block exceeds it by more than
 // 2^8 (P <= 256; bf16 P keeps its relative precision), so O is rescaled
@@ -29,7 +30,11 @@
 // rounding (2^-9 relative, random) is the only one beside the output's.
 //
 // Warps: 0-3 softmax of tile A, 4-7 of tile B (thread = row = TMEM lane, no
-// exchange between threads), 8 TMA, 9 MMA issue and TMEM, 10 the V tail.
+// exchange between threads), 8 TMA, 9 MMA issue and TMEM, 10 the V tail.  One
+// thread issues both tiles' MMAs, so that a tile's run of PV and QK completes
+// before the other's begins (a warp for each tile let the two runs share the
+// tensor cores and end together, and both softmaxes then ran with the tensor
+// cores idle: 12 % slower).
 // When one wave of (tile, head) items leaves SMs idle, the keys are split
 // over grid.z and a second kernel joins the partial results.
 #include <algorithm>
@@ -46,9 +51,8 @@ constexpr int kBN = 128;  // keys of a block
 constexpr int kNope = 128, kRope = 64, kDV = 128;
 constexpr int kChunk = kBM * 128;         // a 128-row x 64-column bf16 chunk, 128-byte swizzle
 constexpr int kQTile = 3 * kChunk;        // 128 x 192
-constexpr int kKTile = 3 * kChunk;
 constexpr int kVTile = 2 * kChunk;
-constexpr int kHalfV = 64;                // keys of a V half
+constexpr int kKSlots = 4, kVSlots = 2;
 constexpr int kSoftThreads = 256;
 constexpr int kThreads = 384;
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kTailWarp = 10;
@@ -69,6 +73,7 @@ struct Params {
   const float* sink;  // [H] or null
   uint16_t* out;      // [T, H, 128]
   float* lse;         // [T, H] or null
+  int slots, head_group;  // grid.x decomposition
   int nsplit;
   float* part_o;      // [nsplit, T, H, 128]
   float* part_lse;    // [nsplit, T, H], log2 units
@@ -77,10 +82,10 @@ struct Params {
 
 struct Smem {
   uint8_t q[2][kQTile];
-  uint8_t k[2][kKTile];
-  uint8_t v[kVTile];
-  unsigned long long bar_q, bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2];
-  unsigned long long bar_s[2], bar_p[2], bar_o[2];  // per tile
+  uint8_t k[kKSlots][kChunk];
+  uint8_t v[kVSlots][kVTile];
+  unsigned long long bar_q, bar_k_full[kKSlots], bar_k_empty[kKSlots], bar_v_full[kVSlots], bar_v_empty[kVSlots];
+  unsigned long long bar_s[2], bar_p[2][2], bar_o[2];  // per tile (bar_p: and half of the keys)
   unsigned long long bar_tail_go, bar_tail, bar_drain;
   uint32_t tmem_base;
   int b, tile;  // the CTA's sequence and 256-row tile; b < 0: none
@@ -136,10 +141,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   Smem& s = *reinterpret_cast<Smem*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int head = blockIdx.y;
+  // CTA -> (head group, slot, head of the group): a group's keys and values
+  // stay in L2 while all its tiles read them, and within a group the longest
+  // tiles start first.
+  const int per_group = p.slots * p.head_group;
+  const int group = blockIdx.x / per_group, rem = blockIdx.x - group * per_group;
+  const int g_heads = min(p.head_group, p.H - group * p.head_group);
+  const int slot = rem / g_heads, head = group * p.head_group + rem - slot * g_heads;
   if (warp == 0) {
-    // slot blockIdx.x -> (sequence, 256-row tile), each sequence's longest
-    // tile first
+    // slot -> (sequence, 256-row tile), each sequence's longest tile first
     int base = 0, fb = -1, ft = 0;
     for (int b0 = 0; b0 < p.B && fb < 0; b0 += 32) {
       const int b = b0 + lane;
@@ -150,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int up = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += up;
       }
-      const int at = static_cast<int>(blockIdx.x) - base - (inc - nt);
+      const int at = slot - base - (inc - nt);
       const unsigned hit = __ballot_sync(0xffffffffu, at >= 0 && at < nt);
       if (hit) {
         const int src = __ffs(hit) - 1;
@@ -169,18 +179,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Work w = work_of(p, s.b, s.tile);
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&s.bar_q), 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kKSlots; ++i) {
       mbar_init(smem_u32(&s.bar_k_full[i]), 1);
       mbar_init(smem_u32(&s.bar_k_empty[i]), 1);
+    }
+    for (int i = 0; i < kVSlots; ++i) {
       mbar_init(smem_u32(&s.bar_v_full[i]), 1);
       mbar_init(smem_u32(&s.bar_v_empty[i]), 1);
-      mbar_init(smem_u32(&s.bar_s[i]), 1);
-      mbar_init(smem_u32(&s.bar_p[i]), kBM);
-      mbar_init(smem_u32(&s.bar_o[i]), 1);
     }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(smem_u32(&s.bar_s[x]), 1);
+      mbar_init(smem_u32(&s.bar_p[x][0]), kBM);
+      mbar_init(smem_u32(&s.bar_p[x][1]), kBM);
+      mbar_init(smem_u32(&s.bar_o[x]), 1);
+    }
+    mbar_init(smem_u32(&s.bar_drain), 1);
     mbar_init(smem_u32(&s.bar_tail_go), 1);
     mbar_init(smem_u32(&s.bar_tail), 32);
-    mbar_init(smem_u32(&s.bar_drain), 1);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -206,9 +221,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + x * kBN, to = tmem + lanes + kTmemO + x * kDV;
     const int nk = i < w.rows ? min(w.pos0 + i + 1, w.kv) : 0;  // keys the row sees
-    const int n = w.n[x];
+    const int n = x ? w.n[1] : w.n[0];
     float m = -INFINITY;
-    float2 l2 = make_float2(0.f, 0.f);
+    float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // even and odd column pairs
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_s[x]), j & 1, p.err))) { ok = false; break; }
@@ -228,16 +243,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
+      for (int e = 0; e < 32; e += 2)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(v[q][e]));
-      const float z = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
+        for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], __uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1]));
+      const float z = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * p.c;
       const bool raise = z > m + kTau;
       if (__any_sync(0xffffffffu, raise)) {
         const float m_new = raise ? z : m;
         const float f = raise ? ex2_approx(m - m_new) : 1.f;  // 0 for the row's first keys
-        l2.x *= f;
-        l2.y *= f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          l2[k].x *= f;
+          l2[k].y *= f;
+        }
         m = m_new;
         if (j > 0) {
           // O holds blocks < j: wait for the last PV, scale the row
@@ -264,22 +282,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int q = hf * 2 + (e >> 4), a = (e & 15) * 2;
           const float2 y = fma2(make_float2(__uint_as_float(v[q][a]), __uint_as_float(v[q][a + 1])), c2, n2);
           const float2 w2 = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-          l2 = add2(l2, w2);
+          l2[e & 1] = add2(l2[e & 1], w2);
           const __nv_bfloat162 b2 = __floats2bfloat162_rn(w2.x, w2.y);
           pk[e] = *reinterpret_cast<const uint32_t*>(&b2);
         }
         tmem_st32(ts + 32 * hf, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&s.bar_p[x][hf]));  // PV starts on the first 64 keys
       }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(smem_u32(&s.bar_p[x]));
     }
     if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_o[x]), (n - 1) & 1, p.err));
     tc_fence_after();
     const int64_t t = w.t0 + i;
     const bool store = ok && i < w.rows && t >= 0 && t < p.T;
     const int64_t r = t * p.H + head;
-    const float l = l2.x + l2.y;
+    const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
     const bool any = !(l == 0.f);  // without weights O's row is not read: zeros
     float inv = 0.f;
     float* po = nullptr;
@@ -299,21 +317,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (store && p.lse) p.lse[r] = total == 0.f ? -INFINITY : kLn2 * (top + log2f(total));
     }
     if (n > 0) {
+      // O / l.  Partial results go out as they are; bf16 rows are first put
+      // into Q's place (every QK of the tile has been read by now), 16-byte
+      // pieces swizzled over the banks, so that a warp stores whole rows
+      // (stored from the registers, 32 rows 16 bytes at a time: 3300 cycles).
+      uint8_t* stage = s.q[x] + (row & ~31) * (kDV * 2);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t o[32];
         tmem_ld32(to + 32 * q, o);
         tmem_wait_ld_regs(o);
-        if (!store) continue;
         if (po) {
-          if (any)
+          if (store && any)
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               *reinterpret_cast<float4*>(po + 32 * q + e) =
                   make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
                               __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + r * kDV + 32 * q);
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             uint32_t u[4];
@@ -324,8 +345,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               const __nv_bfloat162 b2 = __floats2bfloat162_rn(a, b);
               u[k] = *reinterpret_cast<const uint32_t*>(&b2);
             }
-            dst[e / 8] = make_uint4(u[0], u[1], u[2], u[3]);
+            const int piece = q * 4 + e / 8;
+            *reinterpret_cast<uint4*>(stage + lane * (kDV * 2) + ((piece ^ (lane & 7)) << 4)) =
+                make_uint4(u[0], u[1], u[2], u[3]);
           }
+        }
+      }
+      if (!po) {
+        __syncwarp();
+        const unsigned keep = __ballot_sync(0xffffffffu, store);
+        const int64_t t_warp = t - lane;  // the warp's first token
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int rr = 2 * k + (lane >> 4), piece = lane & 15;
+          const uint4 u = *reinterpret_cast<const uint4*>(stage + rr * (kDV * 2) + ((piece ^ (rr & 7)) << 4));
+          if (keep >> rr & 1)
+            reinterpret_cast<uint4*>(p.out + ((t_warp + rr) * p.H + head) * kDV)[piece] = u;
         }
       }
     } else if (store && !po) {
@@ -340,38 +375,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < tiles; ++x)
         for (int c = 0; c < 3; ++c)
           tma_load_3d(smem_u32(s.q[x]) + c * kChunk, &tq, c * 128, head, w.t0 + x * kBM, smem_u32(&s.bar_q));
-      int nk = 0, nv = 0;  // K tiles and V halves requested
+      int nk = 0, nv = 0;  // K chunks and V tiles requested
       bool ok = true;
-      auto load_k = [&](int j) {
-        const int st = j & 1;
-        if (j >= 2) ok = ok && mbar_wait(smem_u32(&s.bar_k_empty[st]), ((j >> 1) - 1) & 1, p.err);
-        if (!ok) return;
+      // chunks [c0, c1) of K block j
+      auto load_k = [&](int j, int c0, int c1) {
         const int key = w.k0 + (w.j0 + j) * kBN;
-        const uint32_t bar = smem_u32(&s.bar_k_full[st]), dst = smem_u32(s.k[st]);
-        mbar_arrive_expect_tx(bar, kKTile);
-        tma_load_3d(dst, &tk, 0, head, key, bar);
-        tma_load_3d(dst + kChunk, &tk, 128, head, key, bar);
-        tma_load_2d(dst + 2 * kChunk, &tr, 0, key, bar);
-        ++nk;
-      };
-      auto load_v = [&](int j) {
-        for (int h = 0; h < 2; ++h) {
-          if (j > 0) ok = ok && mbar_wait(smem_u32(&s.bar_v_empty[h]), (j - 1) & 1, p.err);
+        for (int c = c0; c < c1; ++c) {
+          const int g = j * 3 + c, sl = g % kKSlots;
+          if (g >= kKSlots) ok = ok && mbar_wait(smem_u32(&s.bar_k_empty[sl]), (g / kKSlots - 1) & 1, p.err);
           if (!ok) return;
-          const int key = w.k0 + (w.j0 + j) * kBN + h * kHalfV;
-          const uint32_t bar = smem_u32(&s.bar_v_full[h]), dst = smem_u32(s.v) + h * kHalfV * 128;
-          mbar_arrive_expect_tx(bar, kVTile / 2);
-          tma_load_3d(dst, &tv, 0, head, key, bar);
-          tma_load_3d(dst + kChunk, &tv, 128, head, key, bar);
-          ++nv;
+          const uint32_t bar = smem_u32(&s.bar_k_full[sl]);
+          mbar_arrive_expect_tx(bar, kChunk);
+          if (c < 2)
+            tma_load_3d(smem_u32(s.k[sl]), &tk, c * 128, head, key, bar);
+          else
+            tma_load_2d(smem_u32(s.k[sl]), &tr, 0, key, bar);
+          ++nk;
         }
       };
-      load_k(0);
-      if (w.last > 1) load_k(1);
+      auto load_v = [&](int j) {
+        const int sl = j % kVSlots;
+        if (j >= kVSlots) ok = ok && mbar_wait(smem_u32(&s.bar_v_empty[sl]), (j / kVSlots - 1) & 1, p.err);
+        if (!ok) return;
+        const int key = w.k0 + (w.j0 + j) * kBN;
+        const uint32_t bar = smem_u32(&s.bar_v_full[sl]);
+        mbar_arrive_expect_tx(bar, kVTile);
+        tma_load_3d(smem_u32(s.v[sl]), &tv, 0, head, key, bar);
+        tma_load_3d(smem_u32(s.v[sl]) + kChunk, &tv, 128, head, key, bar);
+        ++nv;
+      };
+      // in the order in which their places come free: the next block's first
+      // chunk has a spare slot, V(j + 1) the other tile, the other chunks
+      // follow QK(j)
+      load_k(0, 0, 3);
       load_v(0);
-      for (int j = 1; j < w.last && ok; ++j) {
-        if (j + 1 < w.last) load_k(j + 1);
-        if (ok) load_v(j);
+      for (int j = 0; j < w.last && ok; ++j) {
+        if (j + 1 < w.last) {
+          load_k(j + 1, 0, 1);
+          if (ok) load_v(j + 1);
+          if (ok) load_k(j + 1, 1, 3);
+        }
       }
       // the last V is requested: from here on its barriers are in their last
       // phase, which the tail warp waits for
@@ -379,11 +422,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // nothing is still landing when the CTA ends (all have landed long ago
       // unless a wait gave up)
       mbar_wait(smem_u32(&s.bar_q), 0, p.err);
-      for (int st = 0; st < 2; ++st) {
-        const int loads = (nk + 1 - st) >> 1;
-        if (loads > 0) mbar_wait(smem_u32(&s.bar_k_full[st]), (loads - 1) & 1, p.err);
-        const int halves = (nv + 1 - st) >> 1;
-        if (halves > 0) mbar_wait(smem_u32(&s.bar_v_full[st]), (halves - 1) & 1, p.err);
+      for (int sl = 0; sl < kKSlots; ++sl) {
+        const int loads = (nk + kKSlots - 1 - sl) / kKSlots;
+        if (loads > 0) mbar_wait(smem_u32(&s.bar_k_full[sl]), (loads - 1) & 1, p.err);
+      }
+      for (int sl = 0; sl < kVSlots; ++sl) {
+        const int loads = (nv + kVSlots - 1 - sl) / kVSlots;
+        if (loads > 0) mbar_wait(smem_u32(&s.bar_v_full[sl]), (loads - 1) & 1, p.err);
       }
     }
     __syncwarp();
@@ -395,61 +440,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t IDESC_PV = idesc_bf16_f32(kBM, kDV, 0, 1);
       const uint64_t dq = make_sdesc(smem_u32(s.q[0]), 16, 1024, kSwizzle128B);
       const uint64_t dk = make_sdesc(smem_u32(s.k[0]), 16, 1024, kSwizzle128B);
-      const uint64_t dv = make_sdesc(smem_u32(s.v), kChunk, 1024, kSwizzle128B);
+      const uint64_t dv = make_sdesc(smem_u32(s.v[0]), kChunk, 1024, kSwizzle128B);
       bool ok = mbar_wait(smem_u32(&s.bar_q), 0, p.err);
-      auto qk = [&](int x, int j) {
-        const uint64_t a = dq + static_cast<uint64_t>((x * kQTile) >> 4);
-        const uint64_t b = dk + static_cast<uint64_t>(((j & 1) * kKTile) >> 4);
+      // S_x = Q_x K^T of block j; `first`: its chunks are waited for, `done`:
+      // they are handed back
+      auto qk = [&](int x, int j, bool first, bool done) {
 #pragma unroll
-        for (int c = 0; c < 3; ++c)
+        for (int c = 0; c < 3; ++c) {
+          const int g = j * 3 + c, sl = g % kKSlots;
+          if (first) ok = ok && mbar_wait(smem_u32(&s.bar_k_full[sl]), (g / kKSlots) & 1, p.err);
+          if (!ok) return;
+          const uint64_t a = dq + static_cast<uint64_t>((x * kQTile + c * kChunk) >> 4);
+          const uint64_t b = dk + static_cast<uint64_t>(sl * (kChunk >> 4));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t off = static_cast<uint64_t>((c * kChunk + kk * 32) >> 4);
-            mma_f16_ss(tmem + x * kBN, a + off, b + off, IDESC_QK, (c | kk) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ss(tmem + x * kBN, a + static_cast<uint64_t>(kk * 2), b + static_cast<uint64_t>(kk * 2), IDESC_QK,
+                       (c | kk) ? 1u : 0u);
+          if (done) mma_commit(smem_u32(&s.bar_k_empty[sl]));
+        }
         mma_commit(smem_u32(&s.bar_s[x]));
       };
-      auto wait_k = [&](int j) {
-        ok = ok && mbar_wait(smem_u32(&s.bar_k_full[j & 1]), (j >> 1) & 1, p.err);
-        return ok;
-      };
-      // PV of tile x, block j; `first`: the block's V is waited for; `done`:
-      // its halves are handed back
+      // O_x += P_x V of block j
       auto pv = [&](int x, int j, bool first, bool done) {
-        ok = ok && mbar_wait(smem_u32(&s.bar_p[x]), j & 1, p.err);
-        if (ok && first && has_tail && j == w.last - 1) ok = mbar_wait(smem_u32(&s.bar_tail), 0, p.err);
-        if (!ok) return;
-        tc_fence_after();
+        const int sl = j % kVSlots;
+        if (first) {
+          ok = ok && mbar_wait(smem_u32(&s.bar_v_full[sl]), (j / kVSlots) & 1, p.err);
+          if (ok && has_tail && j == w.last - 1) ok = mbar_wait(smem_u32(&s.bar_tail), 0, p.err);
+        }
+        const uint64_t b = dv + static_cast<uint64_t>(sl * (kVTile >> 4));
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (first) ok = ok && mbar_wait(smem_u32(&s.bar_v_full[h]), j & 1, p.err);
+          ok = ok && mbar_wait(smem_u32(&s.bar_p[x][h]), j & 1, p.err);
           if (!ok) return;
+          tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const int ks = h * 4 + kk;  // 16 keys: 8 columns of P, 16 rows of V
             mma_f16_ts(tmem + kTmemO + x * kDV, tmem + x * kBN + ks * 8,
-                       dv + static_cast<uint64_t>((ks * 16 * 128) >> 4), IDESC_PV, (j > 0 || ks > 0) ? 1u : 0u);
+                       b + static_cast<uint64_t>((ks * 16 * 128) >> 4), IDESC_PV, (j > 0 || ks > 0) ? 1u : 0u);
           }
-          if (done) mma_commit(smem_u32(&s.bar_v_empty[h]));
         }
+        if (done) mma_commit(smem_u32(&s.bar_v_empty[sl]));
         mma_commit(smem_u32(&s.bar_o[x]));
       };
-      if (ok && wait_k(0)) {
-        if (w.n[0] > 0) qk(0, 0);
-        if (w.n[1] > 0) qk(1, 0);
-        mma_commit(smem_u32(&s.bar_k_empty[0]));
-      }
+      if (ok && w.n[0] > 0) qk(0, 0, true, w.n[1] <= 0);
+      if (ok && w.n[1] > 0) qk(1, 0, w.n[0] <= 0, true);
       for (int j = 0; j < w.last && ok; ++j) {
         const bool a = j < w.n[0], b = j < w.n[1];
         const bool a1 = j + 1 < w.n[0], b1 = j + 1 < w.n[1];
         if (a) {
           pv(0, j, true, !b);
-          if (ok && a1 && wait_k(j + 1)) qk(0, j + 1);
+          if (ok && a1) qk(0, j + 1, true, !b1);
         }
         if (ok && b) {
           pv(1, j, !a, true);
-          if (ok && b1 && wait_k(j + 1)) qk(1, j + 1);
+          if (ok && b1) qk(1, j + 1, !a1, true);
         }
-        if (ok && j + 1 < w.last) mma_commit(smem_u32(&s.bar_k_empty[(j + 1) & 1]));
       }
       // every MMA has finished before TMEM is freed
       mma_commit(smem_u32(&s.bar_drain));
@@ -459,15 +505,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     setmaxnreg_dec<kOtherRegs>();
     if (warp == kTailWarp && has_tail) {
-      const int ph = (w.last - 1) & 1;
+      const int sl = (w.last - 1) % kVSlots, ph = (w.last - 1) / kVSlots & 1;
       const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_tail_go), 0, p.err) &&
-                                                  mbar_wait(smem_u32(&s.bar_v_full[0]), ph, p.err) &&
-                                                  mbar_wait(smem_u32(&s.bar_v_full[1]), ph, p.err));
+                                                  mbar_wait(smem_u32(&s.bar_v_full[sl]), ph, p.err));
       if (ok) {
         // rows [tail, 128) of both 64-column chunks, 128 bytes each
         for (int u = lane; u < (kBN - tail) * 16; u += 32) {
           const int r = tail + (u >> 4), pc = u & 15;
-          *reinterpret_cast<uint4*>(s.v + (pc >> 3) * kChunk + r * 128 + (pc & 7) * 16) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(s.v[sl] + (pc >> 3) * kChunk + r * 128 + (pc & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         mbar_arrive(smem_u32(&s.bar_tail));
@@ -549,7 +594,7 @@ smla_status_t launch_expanded(const ExpandedArgs& a, unsigned* err, cudaStream_t
   bool enc = map3(&tq, a.q, kNope + kRope, a.H, a.T, a.q_hs, a.q_ts, kBM);
   if (a.S > 0) {
     enc = enc && map3(&tk, a.k_nope, kNope, a.H, a.S, a.k_hs, a.k_ts, kBN) &&
-          map3(&tv, a.v, kDV, a.H, a.S, a.v_hs, a.v_ts, kHalfV);
+          map3(&tv, a.v, kDV, a.H, a.S, a.v_hs, a.v_ts, kBN);
     const uint64_t dims[2] = {kRope * 2, static_cast<uint64_t>(a.S)};
     const uint64_t strides[1] = {static_cast<uint64_t>(a.r_ts) * 2};
     const uint32_t box[2] = {128, kBN};
@@ -589,8 +634,15 @@ smla_status_t launch_expanded(const ExpandedArgs& a, unsigned* err, cudaStream_t
   if (fa.numRegs != kLaunchRegs)
     return fail(SMLA_ERR_UNSUPPORTED, "expanded kernel built with %d registers a thread, the register split needs %d",
                 fa.numRegs, kLaunchRegs);
-  const dim3 grid(static_cast<unsigned>(expanded_slots(a.T, a.B)), static_cast<unsigned>(a.H),
-                  static_cast<unsigned>(a.nsplit));
+  p.slots = static_cast<int>(expanded_slots(a.T, a.B));
+  // heads whose keys and values (512 bytes a row) take at most kGroupBytes,
+  // under half of L2
+  constexpr int64_t kGroupBytes = int64_t(48) << 20;
+  p.head_group = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(a.H, kGroupBytes / (int64_t(512) * std::max(a.S, 1)))));
+  const int64_t ctas = static_cast<int64_t>(p.slots) * a.H;
+  if (ctas > 0x7fffffff || static_cast<int64_t>(p.slots) * p.head_group > 0x7fffffff)
+    return fail(SMLA_ERR_UNSUPPORTED, "expanded prefill: too many tiles (T=%d, B=%d, H=%d)", a.T, a.B, a.H);
+  const dim3 grid(static_cast<unsigned>(ctas), 1, static_cast<unsigned>(a.nsplit));
   expanded_kernel<<<grid, kThreads, smem, stream>>>(tq, tk, tr, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "expanded launch");

@@ -370,6 +370,12 @@ SMLA_DEVICE_INLINE float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+// The largest of three (NaN only if all are).
+SMLA_DEVICE_INLINE float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // 2^x with the hardware approximation (MUFU), flushing subnormal results.
 SMLA_DEVICE_INLINE float ex2_approx(float x) {
   float r;
