@@ -386,6 +386,33 @@ smla_status_t smla_expanded_prefill(const uint16_t* q, int64_t q_token_stride, i
                                     float softmax_scale, const float* attn_sink, uint16_t* out, float* lse,
                                     void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* Dense MLA decode (latent attention, absorbed form) for few query tokens over
+ * the whole cache of their sequence: out[t,h] as for smla_dense_prefill, with
+ *   - the keys of a token divided among several CTAs when the tokens are too
+ *     few to fill the GPU, and the partial results merged by a second kernel;
+ *   - q, and the weights P, carried at bf16's accuracy whatever q's type
+ *     (smla_dense_prefill and the sparse calls round P to one e4m3 term for e4m3 q);
+ *   - e4m3 caches in every scale mode, or a bf16 cache.
+ *   q            [T, H, 576], bf16 or e4m3 (q_dtype)
+ *   latent_pool  [phys_rows, 576], e4m3 or bf16 (pool_dtype)
+ *   scales, scale_block_size, H, v_depth, softmax_scale, attn_sink, out: as for
+ *                smla_dense_prefill
+ *   max_kv_len   a bound on every kv_len, for the choice of the split; larger
+ *                lengths are served too, only less evenly
+ * Block scales (32) take e4m3 q; a bf16 cache takes bf16 q and
+ * scale_block_size 0 (SMLA_ERR_UNSUPPORTED otherwise).  Tokens behind the
+ * last sequence keep their outputs.  A token of a sequence without keys gets
+ * zeros.  workspace: caller-owned device scratch of at least
+ * smla_dense_decode_workspace_size(T, H, max_kv_len) bytes on the current
+ * device (16-byte aligned; NULL when that is 0); contents on entry do not
+ * matter, unspecified on return; not shared by calls that may overlap. */
+size_t smla_dense_decode_workspace_size(int32_t T, int32_t H, int32_t max_kv_len);
+smla_status_t smla_dense_decode(const void* q, int32_t q_dtype, const void* latent_pool, int32_t pool_dtype,
+                                int64_t phys_rows, const float* scales, int32_t scale_block_size, smla_seqs_t seqs,
+                                int32_t max_kv_len, int32_t H, int32_t v_depth, float softmax_scale,
+                                const float* attn_sink, uint16_t* out, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
 /* Synchronises `stream`, then reads and clears the current device's error
  * word.  Returns SMLA_OK, SMLA_ERR_DEVICE_CHECK (out-of-range index or page
  * id), SMLA_ERR_TIMEOUT (a pipeline wait gave up) or SMLA_ERR_CUDA. */

@@ -31,6 +31,8 @@ from ._latent import (  # noqa: F401
     Rope,
     cache_append,
     cache_gather,
+    dense_decode,
+    dense_decode_workspace_size,
     expanded_prefill,
     expanded_prefill_workspace_size,
     rope,

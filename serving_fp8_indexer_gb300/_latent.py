@@ -188,3 +188,35 @@ def expanded_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor
                                    0 if workspace is None else int(workspace.numel()), _stream(stream))
     _check(lib, st)
     return out
+
+
+def dense_decode_workspace_size(T: int, H: int, max_kv_len: int) -> int:
+    """Bytes of device scratch smla_dense_decode needs on the current device."""
+    return int(_lib.load().smla_dense_decode_workspace_size(int(T), int(H), int(max_kv_len)))
+
+
+def dense_decode(q: torch.Tensor, latent: torch.Tensor, scales: Optional[torch.Tensor], scale_block_size: int,
+                 seqs: Seqs, max_kv_len: int, softmax_scale: float, out: torch.Tensor,
+                 workspace: Optional[torch.Tensor], attn_sink: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """out bf16 [T, H, 512] = attention of each new token over its sequence's
+    whole cache.  q bf16 or uint8 (e4m3 bytes) [T, H, 576]; latent uint8 (e4m3
+    bytes) or bf16 [phys_rows, 576] with scales f32 [phys_rows, nscale] or
+    None; workspace a uint8 CUDA tensor of at least
+    dense_decode_workspace_size() bytes (None when that is 0)."""
+    lib = _lib.load()
+    qd, qp = _lib._q_arg(q)
+    _here(q, latent, scales, out, workspace, attn_sink, seqs.cu_q, seqs.kv_len, seqs.page_table)
+    T, H = int(q.shape[0]), int(q.shape[1])
+    if (T != seqs.T or tuple(q.shape) != (T, H, 576) or latent.shape[1] != 576 or tuple(out.shape[:2]) != (T, H) or
+            (attn_sink is not None and tuple(attn_sink.shape) != (H,))):
+        raise ValueError(f"q must be [T={seqs.T}, H, 576], latent [phys_rows, 576], out [T, H, 512], attn_sink [H]")
+    _check_scales(scales, latent, scale_block_size)
+    pp, pd = _pool(latent)
+    st = lib.smla_dense_decode(qp, qd, pp, pd, int(latent.shape[0]), _ptr(scales, torch.float32, "scales", 2),
+                               int(scale_block_size), seqs.as_c(), int(max_kv_len), H, int(out.shape[2]),
+                               float(softmax_scale), _ptr(attn_sink, torch.float32, "attn_sink", 1),
+                               _ptr(out, torch.bfloat16, "out", 3), _ptr(workspace, torch.uint8, "workspace", 1),
+                               0 if workspace is None else int(workspace.numel()), _stream(stream))
+    _check(lib, st)
+    return out

@@ -216,7 +216,7 @@ smla_status_t smla_topk(const float* scores, int64_t score_stride, smla_seqs_t s
 namespace smla {
 // Host-side checks shared by the attention entry points; T is the number of
 // query tokens, `keyed` says whether indices / topk_lengths are used.
-static smla_status_t check_attn(const void* q, int32_t q_dtype, const void* latent_pool, int64_t phys_rows,
+smla_status_t check_attn(const void* q, int32_t q_dtype, const void* latent_pool, int64_t phys_rows,
                                 const float* scales, int32_t scale_block_size, bool keyed, const uint32_t* indices,
                                 int32_t indices_stride, const uint32_t* topk_lengths, int32_t T, int32_t H,
                                 int32_t v_depth, float softmax_scale, const float* attn_sink, const void* out) {
@@ -392,7 +392,7 @@ static smla_status_t sparse_decode_impl(const void* q, int32_t q_dtype, const ui
              nullptr, T, H, softmax_scale, attn_sink, out, nsplit, nsplit > 1 ? part_o : nullptr, part_lse};
   st = launch_attention(a, err, stream);
   if (st != SMLA_OK || nsplit == 1) return st;
-  return launch_decode_combine(part_o, part_lse, attn_sink, T, H, nsplit, out, stream);
+  return launch_decode_combine(part_o, part_lse, attn_sink, T, H, nsplit, out, nullptr, stream);
 }
 
 }  // namespace smla

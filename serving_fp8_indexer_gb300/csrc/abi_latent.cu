@@ -227,4 +227,47 @@ smla_status_t smla_expanded_prefill(const uint16_t* q, int64_t q_token_stride, i
   return launch_expanded(a, err, stream);
 }
 
+size_t smla_dense_decode_workspace_size(int32_t T, int32_t H, int32_t max_kv_len) {
+  if (T <= 0 || H <= 0 || max_kv_len <= 0) return 0;
+  return decode_workspace_bytes(T, H, decode_splits(T, H, max_kv_len));
+}
+
+smla_status_t smla_dense_decode(const void* q, int32_t q_dtype, const void* latent_pool, int32_t pool_dtype,
+                                int64_t phys_rows, const float* scales, int32_t scale_block_size, smla_seqs_t seqs,
+                                int32_t max_kv_len, int32_t H, int32_t v_depth, float softmax_scale,
+                                const float* attn_sink, uint16_t* out, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream) {
+  clear_last_error();
+  smla_status_t st = check_seqs(seqs);
+  if (st != SMLA_OK) return st;
+  if (pool_dtype != SMLA_BF16 && pool_dtype != SMLA_E4M3)
+    return fail(SMLA_ERR_INVALID_ARG, "pool_dtype=%d must be bf16 or e4m3", pool_dtype);
+  if (pool_dtype == SMLA_BF16 && (q_dtype != SMLA_BF16 || scale_block_size != 0))
+    return fail(SMLA_ERR_UNSUPPORTED, "a bf16 cache takes bf16 q and scale_block_size 0");
+  if (max_kv_len < 1) return fail(SMLA_ERR_INVALID_ARG, "max_kv_len=%d must be >= 1", max_kv_len);
+  st = check_attn(q, q_dtype, latent_pool, phys_rows, scales, scale_block_size, false, nullptr, 0, nullptr, seqs.T, H,
+                  v_depth, softmax_scale, attn_sink, out);
+  if (st != SMLA_OK) return st;
+  const int T = seqs.T;
+  const int nsplit = T > 0 ? decode_splits(T, H, max_kv_len) : 1;
+  const size_t need = decode_workspace_bytes(T, H, nsplit);
+  if (workspace_bytes < need || (need && !workspace))
+    return fail(SMLA_ERR_INVALID_ARG, "workspace: %zu bytes given, %zu needed", workspace_bytes, need);
+  if (workspace && !aligned16(workspace)) return fail(SMLA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  if (T == 0) return SMLA_OK;
+  unsigned* err = nullptr;
+  st = device_err_ptr(&err);
+  if (st != SMLA_OK) return st;
+  // partial outputs [T, nsplit, H, 512] f32, then log2-sum-exps [T, nsplit, H] f32
+  float* part_o = nsplit > 1 ? static_cast<float*>(workspace) : nullptr;
+  const size_t o_bytes = (static_cast<size_t>(T) * nsplit * H * 512 * sizeof(float) + 255) & ~size_t(255);
+  float* part_lse = nsplit > 1 ? reinterpret_cast<float*>(static_cast<char*>(workspace) + o_bytes) : nullptr;
+  AttnArgs a{q, q_dtype, static_cast<const uint8_t*>(latent_pool), phys_rows, scales, scale_block_size, nullptr, 0,
+             nullptr, &seqs, T, H, softmax_scale, attn_sink, out, nsplit, part_o, part_lse,
+             pool_dtype == SMLA_BF16, 1};
+  st = launch_attention(a, err, stream);
+  if (st != SMLA_OK || nsplit == 1) return st;
+  return launch_decode_combine(part_o, part_lse, attn_sink, T, H, nsplit, out, seqs.cu_q + seqs.B, stream);
+}
+
 }  // extern "C"

@@ -369,6 +369,10 @@ __device__ __forceinline__ int seq_of(const Params& p, int t) {
 template <int KEYS>
 __device__ __forceinline__ int token_keys(const Params& p, int t, int& b) {
   if (KEYS == kCausal) {
+    if (t >= p.cu_q[p.B]) {  // behind the last sequence: nothing to compute, nothing to write
+      b = 0;
+      return -1;
+    }
     b = seq_of(p, t);
     const int q_len = p.cu_q[b + 1] - p.cu_q[b];
     const int n = p.kv_len[b] - q_len + (t - p.cu_q[b]) + 1;
@@ -397,7 +401,7 @@ __device__ __forceinline__ Item item_make(const Params& p, int w, int groups, in
   it.hv = min(kNH, p.H - it.h0);
   it.n = n;
   it.b = b;
-  const int nb = (n + kBK - 1) / kBK;
+  const int nb = (n + kBK - 1) / kBK;  // 0 for n = -1
   const int per = (nb + p.nsplit - 1) / p.nsplit;
   it.j0 = min(nb, it.s * per);
   it.nblk = min(nb, it.j0 + per) - it.j0;
@@ -424,7 +428,6 @@ __global__ void __launch_bounds__(threads_for(KVP), 1)
   constexpr int kCh = kChunks * EB;       // 64-byte chunks per cache row
   constexpr int kSlotBytes = EB * kKVBytes;
   constexpr int kRopeCh = kRope * EB;     // chunk of column 512 (P goes there)
-  static_assert(!(PP == 2 && KVP == 2), "P lo has a buffer only when rows are single-term");
   static_assert(KVP == 1 || NST == 1, "the blockwise quarter barriers complete once per block (one slot)");
   static_assert(offsetof(S, kv) % 1024 == 0 && offsetof(S, plo) % 1024 == 0,
                 "swizzled operand tiles need 1024-byte alignment");
@@ -587,8 +590,9 @@ __global__ void __launch_bounds__(threads_for(KVP), 1)
       if (nblk == 0) {
         // nothing to attend to: zeros (no softmax mass), or for a split an
         // empty partial (log-sum-exp -inf, which the combine skips); the QK
-        // warp skips the item
-        if (p.nsplit > 1) {
+        // warp skips the item.  A token outside the batch keeps its output.
+        if (n < 0) {
+        } else if (p.nsplit > 1) {
           if (threadIdx.x < I.hv) p.part_lse[part_row() + threadIdx.x] = -INFINITY;
         } else {
           for (int i = threadIdx.x; i < I.hv * kDV / 8; i += kSoftThreads)
@@ -1238,9 +1242,16 @@ smla_status_t launch_attention(const AttnArgs& a, unsigned* err, cudaStream_t st
   if (a.cache_bf16) {
     // bf16 cache: bf16 x bf16 MMAs, one gather slot (a 128-row block of
     // 1152-byte rows and the 64-head bf16 q fill shared memory)
-    if (!bf16 || sbs != 0 || p.keys != kIndexed)
-      return fail(SMLA_ERR_UNSUPPORTED, "a bf16 cache takes bf16 q, no scales and indexed keys");
-    return launch_k<1, 1, 1, 1, kUnit, kIndexed, 2>(tq, p, stream);
+    if (!bf16 || sbs != 0) return fail(SMLA_ERR_UNSUPPORTED, "a bf16 cache takes bf16 q and no scales");
+    return p.keys == kCausal ? launch_k<1, 1, 1, 1, kUnit, kCausal, 2>(tq, p, stream)
+                             : launch_k<1, 1, 1, 1, kUnit, kIndexed, 2>(tq, p, stream);
+  }
+  if (a.two_term_p && !bf16) {
+    // e4m3 q with P as hi + lo, as for bf16 q: the output keeps bf16's accuracy
+    if (p.keys != kCausal) return fail(SMLA_ERR_UNSUPPORTED, "two-term P with e4m3 q is built for dense keys");
+    if (sbs == 0) return launch_k<1, 1, 2, 2, kUnit, kCausal>(tq, p, stream);
+    if (sbs >= kD) return launch_k<1, 1, 2, 2, kRow, kCausal>(tq, p, stream);
+    return launch_k<1, 2, 2, 1, kBlock, kCausal>(tq, p, stream);
   }
   if (sbs == 0) return bf16 ? launch_t<2, 1, 2, 2, kUnit>(tq, p, stream) : launch_t<1, 1, 1, 2, kUnit>(tq, p, stream);
   if (sbs >= kD) return bf16 ? launch_t<2, 1, 2, 2, kRow>(tq, p, stream) : launch_t<1, 1, 1, 2, kRow>(tq, p, stream);

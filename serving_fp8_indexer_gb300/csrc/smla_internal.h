@@ -17,6 +17,10 @@ smla_status_t fail_cuda(cudaError_t e, const char* what);
 void clear_last_error();
 smla_status_t device_err_ptr(unsigned** out);
 smla_status_t check_seqs(const smla_seqs_t& s);
+smla_status_t check_attn(const void* q, int32_t q_dtype, const void* latent_pool, int64_t phys_rows,
+                         const float* scales, int32_t scale_block_size, bool keyed, const uint32_t* indices,
+                         int32_t indices_stride, const uint32_t* topk_lengths, int32_t T, int32_t H, int32_t v_depth,
+                         float softmax_scale, const float* attn_sink, const void* out);
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -71,11 +75,13 @@ struct AttnArgs {
   float* part_o;    // [T, nsplit, H, 512]
   float* part_lse;  // [T, nsplit, H]
   int cache_bf16;   // latent_pool holds bf16 [phys_rows, 576] (q bf16, no scales)
+  int two_term_p;   // P as hi + lo also for e4m3 q (dense keys)
 };
 smla_status_t launch_attention(const AttnArgs& a, unsigned* err, cudaStream_t stream);
 
 // Split-K decode: the split count for these sizes, the workspace it needs,
-// and the kernel that combines the partials into the bf16 output.
+// and the kernel that combines the partials into the bf16 output (`tokens`:
+// device count of the tokens that have partials, or null for all T).
 int decode_splits(int T, int H, int indices_stride);
 size_t decode_workspace_bytes(int T, int H, int nsplit);
 // Fixed scratch of smla_sparse_decode_noalloc (a static device array): its
@@ -84,7 +90,7 @@ size_t decode_workspace_bytes(int T, int H, int nsplit);
 size_t noalloc_scratch_bytes();
 smla_status_t noalloc_scratch_for(size_t need, void** out);
 smla_status_t launch_decode_combine(const float* part_o, const float* part_lse, const float* sink, int T, int H,
-                                    int nsplit, uint16_t* out, cudaStream_t stream);
+                                    int nsplit, uint16_t* out, const int32_t* tokens, cudaStream_t stream);
 
 // Rotary positions of x [T, H, D] into out.
 struct RopeArgs {

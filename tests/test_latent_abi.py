@@ -141,3 +141,24 @@ def test_expanded_refusals(lib):
     assert call(T=1, S=8192, H=1, ws=P + 8) == INVALID and "aligned" in _msg(lib)
     assert call(T=0, B=0, q=None, k=None, r=None, v=None, cq=None, ck=None, out=None) == 0
     assert lib.smla_expanded_prefill_workspace_size(0, 1, 1, 1) == 0
+
+
+def test_dense_decode_refusals(lib):
+    def call(q=P, qd=0, pool=P, pd=1, rows=64, sc=None, sbs=0, s=None, most=64, H=64, vd=512, scale=0.04, sink=None,
+             out=P, ws=P, wsb=1 << 30):
+        return lib.smla_dense_decode(q, qd, pool, pd, rows, sc, sbs, s or _seqs(), most, H, vd, scale, sink, out, ws, wsb,
+                                     None)
+
+    for kw, st in ((dict(qd=2), INVALID), (dict(pd=2), INVALID), (dict(pd=0, qd=1), UNSUPPORTED),
+                   (dict(pd=0, sbs=576, sc=P), UNSUPPORTED), (dict(sbs=32, sc=P), UNSUPPORTED), (dict(most=0), INVALID),
+                   (dict(H=24), UNSUPPORTED), (dict(vd=256), UNSUPPORTED), (dict(sbs=576), INVALID),
+                   (dict(scale=math.nan), INVALID), (dict(q=None), INVALID), (dict(pool=None), INVALID),
+                   (dict(out=None), INVALID), (dict(q=P + 8), INVALID), (dict(pool=P + 8), INVALID),
+                   (dict(sink=P + 2), INVALID), (dict(rows=0), INVALID), (dict(s=_seqs(B=0)), INVALID)):
+        assert call(**kw) == st, kw
+    need = lib.smla_dense_decode_workspace_size(4, 64, 8192)
+    assert need > 0 and lib.smla_dense_decode_workspace_size(0, 64, 8192) == 0
+    assert call(most=8192, wsb=need - 1) == INVALID and "workspace" in _msg(lib)
+    assert call(most=8192, ws=None, wsb=0) == INVALID
+    assert call(most=8192, ws=P + 8) == INVALID and "aligned" in _msg(lib)
+    assert call(s=_seqs(T=0), q=None, pool=None, rows=0, out=None) == 0
