@@ -1,0 +1,941 @@
+// Dense MLA decode over a paged e4m3 latent cache (unit or per-row scales):
+// attention of a few query tokens over every cached key of their sequence.
+//
+// Orientation and precision are those of the prefill attention kernel: keys
+// are the MMA M dimension and query rows the N dimension,
+//   S^T[128 keys x NR rows] = K . Q^T,   O^T[512 x NR] += V^T . P^T,
+// all on the FP8 pipe, with bf16 q and the weights P as two e4m3 terms (hi +
+// lo), so that the e4m3 cache rows are used as they lie in memory.  What is
+// different here:
+//
+// * Rows.  An item is up to NR rows (tokens x heads) of one sequence that
+//   share every key: up to NR / H consecutive tokens of a sequence when H <
+//   64, or 64 of one token's heads.  NR is 16, 32 or 64, so that a few heads
+//   do not pay for 64.  Rows of earlier tokens mask the last keys.
+// * Work.  The blocks of 128 keys of all items form one line, cut into equal
+//   parts, one per CTA, wherever the cuts fall: no SM waits for the longest
+//   sequence.  A part that is a whole item writes its output; the others
+//   write f32 partial results (at most two per CTA), which a second kernel
+//   joins per cut item.
+// * Loads.  Pages are contiguous, so a block is 10 TMA boxes (64-key pages)
+//   instead of 4608 16-byte gathers; nothing but the page table is read to
+//   address them.  Columns 0..511 lie in four 128-byte-swizzled chunks (each
+//   the K-major QK operand and, read MN-major, one 128-column tile of V), the
+//   rotary part in a 64-byte-swizzled one, which P^T reuses after QK.
+// * For NR < 64, P's hi and lo are one operand of 2 NR columns with an
+//   accumulator each (summed at the end): half the MMAs.  With NR = 64 there
+//   is no TMEM for that, and PV runs twice into one accumulator.
+//
+// Bound: HBM for few rows (a block of 73.7 KB is 3140 cycles of an SM's share
+// of 6.8 TB/s; its MMAs 1360 cycles at NR = 16, 1632 at 32), the tensor cores
+// at NR = 64 (2688 cycles), where the shared-memory reads of N = 64 operands
+// set their rate (48 cycles an MMA).
+//
+// Warps: 0-7 softmax and epilogue (thread = one key x NR/2 rows), 8 TMA, 9 QK,
+// 10 PV.
+#include <algorithm>
+#include <cstddef>
+#include <type_traits>
+
+#include "rope.cuh"
+
+namespace smla {
+namespace dd {
+
+constexpr int kD = 576, kDV = 512;
+constexpr int kBK = 128;                 // keys of a block
+constexpr int kChunk = kBK * 128;        // 128 columns of a block
+constexpr int kRopeOff = 4 * kChunk;     // columns 512..575: [128][64 bytes]
+constexpr int kSlot = kRopeOff + kBK * 64;
+constexpr int kNST = 2;                  // block slots
+constexpr int kSoftThreads = 256, kThreads = 384;
+constexpr int kTmaWarp = 8, kQkWarp = 9, kPvWarp = 10;
+constexpr uint32_t kTmemCols = 512, kTmemS = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTau = 8.f, kPOffset = 4.f;  // lazy rescale; the largest weight is 2^4 .. 2^8 (two-term e4m3's best range)
+constexpr int kOrdMin = static_cast<int>(0x80000000u);
+
+struct Cut;
+struct Params {
+  SeqsDev seqs;
+  int64_t phys_rows;
+  const float* scales;  // [phys_rows] or null
+  int T, H;
+  int tok_per_item;     // tokens of an item (H < 64), else 1
+  int groups;           // 64-head groups of a token (H > 64), else 1
+  float softmax_scale;
+  const float* sink;
+  uint16_t* out;
+  // Partial results: CTA c's slot 2c holds the item its part continues, slot
+  // 2c + 1 the one that begins in it and goes on.
+  float* part_o;        // [2 * grid][NR][512], each normalised by its own sum
+  float* part_lse;      // [2 * grid][NR], log2 units
+  Cut* cuts;            // [grid]
+  unsigned* err;
+};
+// What CTA c's part begins with: an item cut at its first block, and whether
+// that is the item's first cut (whose CTA the join goes by).
+struct Cut {
+  int first_cta;  // CTA where the item begins; -1: not an item's first cut
+  int last_cta;
+  int row0, rows, h0;  // output rows [row0, row0 + rows), head of the first
+};
+
+template <int NR, int QP>
+struct Smem {
+  uint8_t q[QP * NR * kD];  // [4][QP * NR rows][128] then [QP * NR][64]: hi rows, then lo rows
+  uint8_t kv[kNST][kSlot];
+  uint8_t plo[NR == 64 ? kBK * 64 : 16];
+  alignas(16) float cs[NR];    // softmax_scale * log2(e) / 2^e per row
+  alignas(16) float negm[NR];  // minus the reference, log2 units
+  float delta[NR], fac[NR];
+  int mx[NR];
+  int nk[NR];                  // keys each row sees
+  unsigned long long bar_qraw, bar_q, bar_full[kNST], bar_empty[kNST][2];
+  unsigned long long bar_s[2], bar_s_free[2], bar_p[2][2], bar_pv[2], bar_drain[2];
+  uint32_t tmem_base;
+};
+
+// ------------------------------------------------------------- the work line
+// Items in order: sequence after sequence, its token groups, their head
+// groups; each `nblk` blocks of 128 keys (at least one, so that tokens
+// without keys are visited and get their zeros).
+struct SeqWork {
+  int q0, q_len, kv, nblk, items;
+};
+__device__ __forceinline__ SeqWork seq_work(const Params& p, int b) {
+  SeqWork w;
+  w.q0 = max(0, p.seqs.cu_q[b]);
+  w.q_len = max(0, min(p.T, p.seqs.cu_q[b + 1]) - w.q0);
+  w.kv = max(0, p.seqs.kv_len[b]);
+  const int most = p.seqs.max_pages << p.seqs.page_shift;
+  if (w.kv > most) {
+    atomicOr(p.err, kErrShape);
+    w.kv = most;
+  }
+  w.nblk = max(1, (w.kv + kBK - 1) / kBK);
+  w.items = (w.q_len + p.tok_per_item - 1) / p.tok_per_item * p.groups;
+  return w;
+}
+
+// All blocks, by the whole warp.
+__device__ __forceinline__ int64_t total_blocks(const Params& p, int lane) {
+  int64_t n = 0;
+  for (int b = lane; b < p.seqs.B; b += 32) {
+    const SeqWork w = seq_work(p, b);
+    n += static_cast<int64_t>(w.items) * w.nblk;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
+}
+
+// Sequence that holds block x of the line (x below the total), and the line's
+// position of its first block; by the whole warp.
+__device__ __forceinline__ int find_block(const Params& p, int64_t x, int lane, int64_t& first) {
+  int64_t base = 0;
+  for (int b0 = 0; b0 < p.seqs.B; b0 += 32) {
+    int64_t n = 0;
+    if (b0 + lane < p.seqs.B) {
+      const SeqWork w = seq_work(p, b0 + lane);
+      n = static_cast<int64_t>(w.items) * w.nblk;
+    }
+    int64_t inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    const bool here = x >= base + inc - n && x < base + inc;
+    const unsigned hit = __ballot_sync(0xffffffffu, here);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      first = base + __shfl_sync(0xffffffffu, inc - n, src);
+      return b0 + src;
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  first = base;
+  return -1;
+}
+
+// A CTA's walk along its part of the line.
+struct Cursor {
+  int b, item, blk;  // next: sequence, item of the sequence, block of the item
+  int64_t left;      // blocks left
+};
+// One item's blocks within the part.
+struct Seg {
+  int t0, ntok, h0, rows;  // first token, tokens, first head, rows
+  int b, pos1;             // sequence; keys that token t0 sees
+  int j0, nb;              // blocks [j0, j0 + nb)
+  bool whole;              // all of the item's blocks
+};
+__device__ __forceinline__ bool next_seg(const Params& p, Cursor& c, Seg& s) {
+  if (c.left <= 0) return false;
+  SeqWork w = seq_work(p, c.b);
+  while (c.item >= w.items) {  // past the sequence's items
+    if (++c.b >= p.seqs.B) return false;
+    c.item = 0;
+    w = seq_work(p, c.b);
+  }
+  const int tg = c.item / p.groups, hg = c.item - tg * p.groups;
+  s.b = c.b;
+  s.t0 = w.q0 + tg * p.tok_per_item;
+  s.ntok = min(p.tok_per_item, w.q_len - tg * p.tok_per_item);
+  s.h0 = hg * 64;
+  s.rows = p.groups > 1 ? 64 : s.ntok * p.H;
+  s.pos1 = w.kv - w.q_len + tg * p.tok_per_item + 1;
+  s.j0 = c.blk;
+  s.nb = static_cast<int>(min(static_cast<int64_t>(w.nblk - c.blk), c.left));
+  s.whole = s.nb == w.nblk;
+  c.left -= s.nb;
+  c.blk += s.nb;
+  if (c.blk >= w.nblk) {
+    c.blk = 0;
+    ++c.item;
+  }
+  return true;
+}
+__device__ __forceinline__ int seg_keys(const Seg& s) { return max(0, s.pos1 + s.ntok - 1); }  // the last token's keys
+
+__device__ __forceinline__ int ord_int(float f) {
+  const int b = __float_as_int(f);
+  return b >= 0 ? b : b ^ 0x7fffffff;
+}
+__device__ __forceinline__ float ord_float(int o) { return __int_as_float(o >= 0 ? o : o ^ 0x7fffffff); }
+// byte offset of 16-byte piece c of row r in a 128- (64-) byte-swizzled chunk
+__device__ __forceinline__ uint32_t sw128(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
+__device__ __forceinline__ uint32_t sw64(int r, int c) { return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
+
+// N (8, 16 or 32) TMEM columns of the thread's lane, waited for.
+template <int N>
+__device__ __forceinline__ void tmem_issue_ld(uint32_t a, uint32_t (&v)[N]) {
+  static_assert(N == 8 || N == 16 || N == 32, "");
+  if constexpr (N == 32) {
+    tmem_ld32(a, v);
+  } else if constexpr (N == 16) {
+    tmem_ld16(a, v);
+  } else {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(a));
+  }
+}
+// Ties v's uses to after the wait before it.
+template <int N>
+__device__ __forceinline__ void after_wait(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Two floats -> e4m3 hi and lo pairs, through f16 (|x| <= 448): hi = e4m3(x),
+// lo = e4m3(x - hi), the difference exact in f16.
+__device__ __forceinline__ void split2(float a, float b, uint16_t& hi, uint16_t& lo) {
+  const uint32_t h = f32x2_to_f16x2(a, b);
+  hi = f16x2_to_e4m3x2(h);
+  lo = f16x2_to_e4m3x2(hsub2(h, e4m3x2_to_f16x2(hi)));
+}
+
+template <int NR, int QP, bool ROWSCALE>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tqr,
+                  const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tr, const Params p) {
+  using S = Smem<NR, QP>;
+  constexpr int kQN = QP * NR;                 // QK's N
+  constexpr int kQChunk = kQN * 128;           // a 128-column chunk of Q
+  constexpr int kPasses = NR == 64 ? 2 : 1;    // PV passes (hi, lo)
+  constexpr int kPN = NR == 64 ? 64 : 2 * NR;  // PV's N
+  constexpr int NC = NR / 2;                   // rows of a softmax thread
+  static_assert(offsetof(S, kv) % 1024 == 0 && offsetof(S, plo) % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+  static_assert(4 * kPN <= static_cast<int>(kTmemS) && 2 * kQN <= static_cast<int>(kTmemCols - kTmemS), "TMEM budget");
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (smem_u32(smem_raw) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(p.err, kErrShape);
+    return;
+  }
+  S& s = *reinterpret_cast<S*>(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // this CTA's part of the line
+  Cursor start;
+  {
+    const int64_t total = total_blocks(p, lane);
+    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t x0 = per * blockIdx.x;
+    int64_t first = 0;
+    start.b = x0 < total ? find_block(p, x0, lane, first) : -1;
+    Cut cut{-1, 0, 0, 0, 0};
+    if (start.b >= 0) {
+      const SeqWork w = seq_work(p, start.b);
+      start.item = static_cast<int>((x0 - first) / w.nblk);
+      start.blk = static_cast<int>((x0 - first) - static_cast<int64_t>(start.item) * w.nblk);
+      start.left = min(per, total - x0);
+      if (start.blk > 0) {
+        const int64_t w0 = x0 - start.blk;  // the item's first block
+        Cursor c = start;
+        Seg g;
+        next_seg(p, c, g);
+        if (w0 / per + 1 == blockIdx.x)
+          cut = {static_cast<int>(w0 / per), static_cast<int>((w0 + w.nblk - 1) / per), g.t0 * p.H + g.h0, g.rows, g.h0};
+      }
+    }
+    if (threadIdx.x == 0 && p.cuts) p.cuts[blockIdx.x] = cut;
+    if (start.b < 0) return;
+  }
+
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&s.bar_qraw), 1);
+    mbar_init(smem_u32(&s.bar_q), kSoftThreads);
+    for (int i = 0; i < kNST; ++i) {
+      mbar_init(smem_u32(&s.bar_full[i]), 1);
+      mbar_init(smem_u32(&s.bar_empty[i][0]), 1);
+      mbar_init(smem_u32(&s.bar_empty[i][1]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.bar_s[i]), 1);
+      mbar_init(smem_u32(&s.bar_s_free[i]), kSoftThreads);
+      mbar_init(smem_u32(&s.bar_p[i][0]), kSoftThreads / 2);
+      mbar_init(smem_u32(&s.bar_p[i][1]), kSoftThreads / 2);
+      mbar_init(smem_u32(&s.bar_pv[i]), 1);
+      mbar_init(smem_u32(&s.bar_drain[i]), 1);
+    }
+    fence_mbar_init();
+  }
+  if (threadIdx.x < NR) s.mx[threadIdx.x] = kOrdMin;
+  if (warp == kQkWarp) {
+    tmem_alloc(smem_u32(&s.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+
+  if (warp < 8) {
+    // ===================================================== softmax, epilogue
+    const int r = threadIdx.x & 127;    // key lane
+    const int hb = (warp >> 2) * NC;    // rows [hb, hb + NC)
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    int q_in = 0;  // q loads waited for
+    // PV of block i.  The block before the last one's PV is not always waited
+    // for, and a wait that lags its barrier by two phases returns at once:
+    // two barriers in turn, of which PV(i - 2) has completed wherever block i's
+    // S has been seen (its keys lie in PV(i - 2)'s slot).
+    auto wait_pv = [&](int i) { return mbar_wait(smem_u32(&s.bar_pv[i & 1]), (i >> 1) & 1, p.err); };
+    // q of a segment: bf16 rows are split in place into e4m3 hi + lo (a
+    // power of two per row puts the largest |q| in [128, 256)); rows past the
+    // segment's are cleared
+    auto convert_q = [&](const Seg& g) -> bool {
+      if (!named_bar_and(1, kSoftThreads, mbar_wait(smem_u32(&s.bar_qraw), q_in++ & 1, p.err))) return false;
+      if (QP == 2) {
+        constexpr int kPer = NR / 32 > 0 ? NR / 32 : 1;  // rows an octet of lanes handles
+        const int r8 = threadIdx.x & 7;
+        uint4 v[kPer][9];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int row = 32 * k + (threadIdx.x >> 3);
+#pragma unroll
+          for (int c = 0; c < 9; ++c)  // raw chunk c: 64 columns, [NR][128 bytes]
+            v[k][c] = row < g.rows ? *reinterpret_cast<const uint4*>(s.q + c * (NR * 128) + sw128(row, r8))
+                                   : make_uint4(0, 0, 0, 0);
+        }
+        named_bar_sync(1, kSoftThreads);  // every byte is read before any is overwritten
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int row = 32 * k + (threadIdx.x >> 3);
+          float amax = 0.f;
+#pragma unroll
+          for (int c = 0; c < 9; ++c) {
+            const uint32_t w[4] = {v[k][c].x, v[k][c].y, v[k][c].z, v[k][c].w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              amax = max3(amax, fabsf(__uint_as_float(w[u] << 16)), fabsf(__uint_as_float(w[u] & 0xffff0000u)));
+          }
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          int e = 0;
+          if (amax > 0.f) {
+            int ex;
+            frexpf(amax, &ex);
+            e = 8 - ex;
+          }
+          const float sigma = ldexpf(1.f, e);
+          if (row < NR) {
+#pragma unroll
+            for (int c = 0; c < 9; ++c) {
+              const uint32_t w[4] = {v[k][c].x, v[k][c].y, v[k][c].z, v[k][c].w};
+              uint16_t hi[4], lo[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                split2(__uint_as_float(w[u] << 16) * sigma, __uint_as_float(w[u] & 0xffff0000u) * sigma, hi[u], lo[u]);
+              const uint2 h2 = make_uint2(hi[0] | static_cast<uint32_t>(hi[1]) << 16, hi[2] | static_cast<uint32_t>(hi[3]) << 16);
+              const uint2 l2 = make_uint2(lo[0] | static_cast<uint32_t>(lo[1]) << 16, lo[2] | static_cast<uint32_t>(lo[3]) << 16);
+              // columns 64 c + 8 r8 .. +7
+              if (c < 8) {
+                const int piece = (c & 1) * 4 + (r8 >> 1);
+                uint8_t* dst = s.q + (c >> 1) * kQChunk + (r8 & 1) * 8;
+                *reinterpret_cast<uint2*>(dst + sw128(row, piece)) = h2;
+                *reinterpret_cast<uint2*>(dst + sw128(NR + row, piece)) = l2;
+              } else {
+                uint8_t* dst = s.q + 4 * kQChunk + (r8 & 1) * 8;
+                *reinterpret_cast<uint2*>(dst + sw64(row, r8 >> 1)) = h2;
+                *reinterpret_cast<uint2*>(dst + sw64(NR + row, r8 >> 1)) = l2;
+              }
+            }
+            if (r8 == 0) s.cs[row] = p.softmax_scale * kLog2e / sigma;
+          }
+        }
+      } else {
+        for (int i = threadIdx.x; i < (NR - g.rows) * 36; i += kSoftThreads) {
+          const int row = g.rows + i / 36, pc = i % 36;
+          uint8_t* dst = pc < 32 ? s.q + (pc >> 3) * kQChunk + row * 128 + (pc & 7) * 16
+                                 : s.q + 4 * kQChunk + row * 64 + (pc & 3) * 16;
+          *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+        }
+        if (threadIdx.x < NR) s.cs[threadIdx.x] = p.softmax_scale * kLog2e;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(smem_u32(&s.bar_q));
+      return true;
+    };
+    // scale of the thread's key of block j (1 outside the keys)
+    auto key_scale = [&](const Seg& g, int j) -> float {
+      if (!ROWSCALE) return 1.f;
+      const int key = (g.j0 + j) * kBK + r;
+      if (key >= seg_keys(g)) return 1.f;
+      const int pid = p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)];
+      const int64_t row = (static_cast<int64_t>(pid) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
+      return pid < 0 || row >= p.phys_rows ? 1.f : p.scales[row];  // (a bad page is reported by the TMA warp)
+    };
+    Cursor cur = start;
+    Seg g;
+    bool ok = next_seg(p, cur, g) && convert_q(g);
+    int gb = 0;  // blocks of the segments before
+    float sr_next = ok ? key_scale(g, 0) : 1.f;
+    bool more = ok;
+    while (ok && more) {
+      const int n_item = seg_keys(g);
+      if (threadIdx.x < NR) {
+        s.negm[threadIdx.x] = 0.f;  // the first block sets the reference
+        const int tok = p.groups > 1 ? 0 : threadIdx.x / p.H;
+        s.nk[threadIdx.x] = threadIdx.x < g.rows ? g.pos1 + tok : 0;
+      }
+      named_bar_sync(1, kSoftThreads);
+      float lv[NC];
+#pragma unroll
+      for (int h = 0; h < NC; ++h) lv[h] = 0.f;
+      Cursor cn = cur;
+      Seg gn;
+      const bool has_next = next_seg(p, cn, gn);
+      for (int j = 0; j < g.nb; ++j) {
+        const int i = gb + j, slot = i % kNST, buf = i & 1;
+        const float sr = sr_next;
+        if (j + 1 < g.nb)
+          sr_next = key_scale(g, j + 1);
+        else if (has_next)
+          sr_next = key_scale(gn, 0);
+        if (!named_bar_and(1, kSoftThreads, mbar_wait(smem_u32(&s.bar_s[buf]), (i >> 1) & 1, p.err))) { ok = false; break; }
+        tc_fence_after();
+        float y[NC];
+        {
+          const uint32_t a = tmem + lanes + kTmemS + buf * kQN + hb;
+          uint32_t v0[NC], v1[NC];
+          tmem_issue_ld(a, v0);
+          if (QP == 2) tmem_issue_ld(a + NR, v1);
+          tmem_wait_ld();
+          after_wait(v0);
+          if (QP == 2) after_wait(v1);
+#pragma unroll
+          for (int h = 0; h < NC; ++h) y[h] = QP == 2 ? __uint_as_float(v0[h]) + __uint_as_float(v1[h]) : __uint_as_float(v0[h]);
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&s.bar_s_free[buf]));
+        const float lg = ROWSCALE ? __log2f(sr) : 0.f;
+        float ymax = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < NC; ++h) y[h] = fmaf(y[h], ROWSCALE ? sr * s.cs[hb + h] : s.cs[hb + h], s.negm[hb + h]);
+        const int key = (g.j0 + j) * kBK + r;
+        const bool edge = (g.j0 + j + 1) * kBK > g.pos1;  // some row's keys end in this block (or before it)
+        if (edge) {
+#pragma unroll
+          for (int h = 0; h < NC; ++h)
+            if (key >= s.nk[hb + h]) y[h] = -INFINITY;
+        }
+#pragma unroll
+        for (int h = 0; h < NC; ++h) ymax = fmaxf(ymax, y[h]);
+        if (named_bar_or(1, kSoftThreads, j == 0 || ymax + lg > kTau)) {
+          // Rows whose largest exceeds their reference by 2^8 (all of them in
+          // the first block) get a new one, and their sums and O^T columns
+          // are rescaled.
+          int mine = kOrdMin;
+#pragma unroll
+          for (int h = 0; h < NC; ++h) {
+            const int m = __reduce_max_sync(0xffffffffu, ord_int(y[h] + lg));
+            if (lane == h) mine = m;
+          }
+          if (lane < NC) atomicMax(&s.mx[hb + lane], mine);
+          named_bar_sync(1, kSoftThreads);
+          if ((warp & 3) == 0 && lane < NC) {
+            const int hh = hb + lane;
+            const float t = ord_float(s.mx[hh]);
+            s.mx[hh] = kOrdMin;
+            float d = 0.f, f = 1.f;
+            if ((j == 0 || t > kTau) && t > -INFINITY) {  // (a row without keys here keeps 0)
+              d = t - kPOffset;
+              if (j > 0) f = exp2f(-d);
+              s.negm[hh] -= d;
+            }
+            s.delta[hh] = d;
+            s.fac[hh] = f;
+          }
+          named_bar_sync(1, kSoftThreads);
+#pragma unroll
+          for (int h = 0; h < NC; ++h) y[h] -= s.delta[hb + h];
+          if (j > 0) {
+#pragma unroll
+            for (int h = 0; h < NC; ++h) lv[h] *= s.fac[hb + h];
+            if (!named_bar_and(1, kSoftThreads, wait_pv(i - 1))) { ok = false; break; }
+            tc_fence_after();
+            constexpr int kParts = kPN / NR;  // hi (and lo) accumulators
+#pragma unroll 1
+            for (int part = 0; part < 4 * kParts; ++part) {
+              const uint32_t a = tmem + lanes + (part / kParts) * kPN + (part % kParts) * NR + hb;
+#pragma unroll
+              for (int c = 0; c < NC; c += 8) {
+                uint32_t v[8];
+                tmem_issue_ld(a + c, v);
+                tmem_wait_ld();
+                after_wait(v);
+#pragma unroll
+                for (int h = 0; h < 8; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * s.fac[hb + c + h]);
+                tmem_st8(a + c, v);
+              }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            named_bar_sync(1, kSoftThreads);  // all lanes are rescaled before any P is published
+          }
+        }
+        // ---- P^T row r, this thread's rows, as hi + lo; row sums
+        uint8_t* p_row = s.kv[slot] + kRopeOff;
+        uint16_t hi[NC / 2], lo[NC / 2];
+#pragma unroll
+        for (int k = 0; k < NC / 2; ++k) {
+          const float a = ex2_approx(ROWSCALE ? y[2 * k] + lg : y[2 * k]);
+          const float b = ex2_approx(ROWSCALE ? y[2 * k + 1] + lg : y[2 * k + 1]);
+          // (the sum takes the weight itself: a / sr would lose it where the
+          // scale is 0 or tiny)
+          lv[2 * k] += ROWSCALE ? ex2_approx(y[2 * k]) : a;
+          lv[2 * k + 1] += ROWSCALE ? ex2_approx(y[2 * k + 1]) : b;
+          split2(a, b, hi[k], lo[k]);
+        }
+        auto pack = [](const uint16_t* h) { return static_cast<uint32_t>(h[0]) | static_cast<uint32_t>(h[1]) << 16; };
+        if constexpr (NR == 64) {
+          // 32 bytes of hi in the slot's rope chunk (read by QK, now dead);
+          // lo's own buffer is free once the previous PV is done with it
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<uint4*>(p_row + sw64(r, (hb >> 4) + c)) =
+                make_uint4(pack(hi + 8 * c), pack(hi + 8 * c + 2), pack(hi + 8 * c + 4), pack(hi + 8 * c + 6));
+          if (i > 0) wait_pv(i - 1);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<uint4*>(s.plo + sw64(r, (hb >> 4) + c)) =
+                make_uint4(pack(lo + 8 * c), pack(lo + 8 * c + 2), pack(lo + 8 * c + 4), pack(lo + 8 * c + 6));
+        } else if constexpr (NR == 32) {
+          *reinterpret_cast<uint4*>(p_row + sw64(r, hb >> 4)) = make_uint4(pack(hi), pack(hi + 2), pack(hi + 4), pack(hi + 6));
+          *reinterpret_cast<uint4*>(p_row + sw64(r, 2 + (hb >> 4))) =
+              make_uint4(pack(lo), pack(lo + 2), pack(lo + 4), pack(lo + 6));
+        } else {
+          *reinterpret_cast<uint2*>(p_row + sw64(r, 0) + hb) = make_uint2(pack(hi), pack(hi + 2));
+          *reinterpret_cast<uint2*>(p_row + sw64(r, 1) + hb) = make_uint2(pack(lo), pack(lo + 2));
+        }
+        if (edge && key >= n_item) {
+          // nobody's key: whatever lies there must not meet a weight of 0
+          for (int c = (warp >> 2); c < 32; c += 2)
+            *reinterpret_cast<uint4*>(s.kv[slot] + (c >> 3) * kChunk + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&s.bar_p[i & 1][(warp & 3) >> 1]));
+      }
+      if (!ok) break;
+      gb += g.nb;
+      // ---- row sums over the key lanes
+      float* linv = s.fac;
+      if (threadIdx.x < NR) linv[threadIdx.x] = 0.f;
+      named_bar_sync(1, kSoftThreads);
+      // halving exchanges: lane l ends with the sum of row hb + l % NC
+#pragma unroll
+      for (int step = NC / 2; step >= 1; step >>= 1) {
+        const bool upper = (lane & step) != 0;
+#pragma unroll
+        for (int h = 0; h < step; ++h) {
+          const float send = upper ? lv[h] : lv[h + step];
+          const float keep = upper ? lv[h + step] : lv[h];
+          lv[h] = keep + __shfl_xor_sync(0xffffffffu, send, step);
+        }
+      }
+#pragma unroll
+      for (int o = NC; o < 32; o <<= 1) lv[0] += __shfl_xor_sync(0xffffffffu, lv[0], o);
+      if (lane < NC) atomicAdd(&linv[hb + lane], lv[0]);
+      named_bar_sync(1, kSoftThreads);
+      // the next segment's q while this one's last PV runs
+      float l_row = 0.f, ref_row = 0.f;
+      if (threadIdx.x < NR) {
+        l_row = linv[threadIdx.x];
+        ref_row = s.negm[threadIdx.x];
+      }
+      if (has_next && !convert_q(gn)) { ok = false; break; }
+      const bool done = named_bar_and(1, kSoftThreads, wait_pv(gb - 1));
+      const int part = static_cast<int>(blockIdx.x) * 2 + (g.j0 == 0 ? 1 : 0);
+      if (threadIdx.x < NR) {
+        float l = l_row;
+        if (g.whole) {
+          if (p.sink && threadIdx.x < g.rows) {
+            const int head = p.groups > 1 ? g.h0 + threadIdx.x : threadIdx.x % p.H;
+            l += exp2f(fmaf(p.sink[head], kLog2e, ref_row));
+          }
+        } else if (threadIdx.x < g.rows) {
+          p.part_lse[static_cast<int64_t>(part) * NR + threadIdx.x] = l == 0.f ? -INFINITY : log2f(l) - ref_row;
+        }
+        linv[threadIdx.x] = l_row == 0.f ? 0.f : 1.f / l;
+      }
+      named_bar_sync(1, kSoftThreads);
+      if (done) {
+        tc_fence_after();
+        const int64_t row0 = static_cast<int64_t>(g.t0) * p.H + g.h0;
+        const bool odd = lane & 1;
+#pragma unroll 1
+        for (int tile = 0; tile < 4; ++tile) {
+          float o[NC];
+          const uint32_t a = tmem + lanes + tile * kPN + hb;
+#pragma unroll
+          for (int c = 0; c < NC; c += 8) {
+            uint32_t v0[8], v1[8];
+            tmem_issue_ld(a + c, v0);
+            if (kPN > NR) tmem_issue_ld(a + NR + c, v1);
+            tmem_wait_ld();
+            after_wait(v0);
+            if (kPN > NR) {
+              after_wait(v1);
+#pragma unroll
+              for (int h = 0; h < 8; ++h) o[c + h] = __uint_as_float(v0[h]) + __uint_as_float(v1[h]);
+            } else {
+#pragma unroll
+              for (int h = 0; h < 8; ++h) o[c + h] = __uint_as_float(v0[h]);
+            }
+          }
+          if (!g.whole) {
+            float* po = p.part_o + (static_cast<int64_t>(part) * NR + hb) * kDV + tile * 128 + r;
+#pragma unroll
+            for (int h = 0; h < NC; ++h)
+              if (hb + h < g.rows) po[h * kDV] = o[h] * linv[hb + h];
+          } else {
+            // lane pairs swap one value per two rows, so that each stores two
+            // neighbouring columns of one row
+            uint32_t* o2 = reinterpret_cast<uint32_t*>(p.out + row0 * kDV + tile * 128 + (r & ~1));
+#pragma unroll
+            for (int h = 0; h < NC; h += 2) {
+              const float va = o[h] * linv[hb + h], vb = o[h + 1] * linv[hb + h + 1];
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? va : vb, 1);
+              const __nv_bfloat162 pr = odd ? __floats2bfloat162_rn(got, vb) : __floats2bfloat162_rn(va, got);
+              const int row = hb + h + (odd ? 1 : 0);
+              if (row < g.rows) o2[static_cast<int64_t>(row) * (kDV / 2)] = *reinterpret_cast<const uint32_t*>(&pr);
+            }
+          }
+        }
+      } else {
+        ok = false;
+      }
+      tc_fence_before();
+      named_bar_sync(1, kSoftThreads);  // O^T and linv are read before the next segment writes them
+      more = has_next;
+      cur = cn;
+      g = gn;
+    }
+  } else if (warp == kTmaWarp) {
+    // ============================================================= key blocks
+    Cursor cur = start;
+    Seg g;
+    int i = 0;
+    bool ok = true;
+    const int box = min(1 << p.seqs.page_shift, kBK / 2);  // keys of a TMA box
+    while (ok && next_seg(p, cur, g)) {
+      const int n_item = seg_keys(g);
+      for (int j = 0; ok && j < g.nb; ++j) {
+        const int slot = i % kNST, key0 = (g.j0 + j) * kBK;
+        const int nbox = min(kBK, max(0, n_item - key0) + box - 1) / box;  // boxes with keys in them
+        const uint32_t bar = smem_u32(&s.bar_full[slot]);
+        const uint32_t dst = smem_u32(s.kv[slot]);
+        const uint32_t par = ((i / kNST) & 1) ^ 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_empty[slot][0]), par, p.err))) { ok = false; break; }
+        if (lane == 0) {
+          if (nbox > 0)
+            mbar_arrive_expect_tx(bar, nbox * box * kD);
+          else
+            mbar_arrive(bar);
+        }
+        __syncwarp();
+        // five boxes (four 128-byte columns, one of 64) of each page part, a
+        // lane each; the second half of the keys once PV has given it back
+        const int half_boxes = (kBK / 2) / box;
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && nbox > half_boxes &&
+              !__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_empty[slot][1]), par, p.err))) {
+            ok = false;
+            break;
+          }
+          const int k1 = min(nbox, (h + 1) * half_boxes);
+          for (int u = h * half_boxes * 5 + lane; u < k1 * 5; u += 32) {
+            const int k = u / 5, c = u - k * 5, key = key0 + k * box;
+            const int pid =
+                p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)];
+            int64_t row = (static_cast<int64_t>(pid) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
+            if (pid < 0 || row >= p.phys_rows) {
+              atomicOr(p.err, kErrPage);
+              row = 0;
+            }
+            if (c < 4)
+              tma_load_2d(dst + c * kChunk + k * box * 128, &tk, c * 128, static_cast<int>(row), bar);
+            else
+              tma_load_2d(dst + kRopeOff + k * box * 64, &tr, 512, static_cast<int>(row), bar);
+          }
+          __syncwarp();
+        }
+        ++i;
+      }
+    }
+    // nothing is still landing when the CTA ends
+    for (int sl = 0; sl < kNST; ++sl) {
+      const int loads = (i + kNST - 1 - sl) / kNST;
+      if (loads > 0) mbar_wait(smem_u32(&s.bar_full[sl]), (loads - 1) & 1, p.err);
+    }
+  } else if (warp == kQkWarp) {
+    // ============================================================== q and QK
+    Cursor cur = start;
+    Seg g;
+    const bool leader = elect_one();
+    constexpr uint32_t IDESC = idesc_e4m3_f32(kBK, kQN, 0, 0);
+    const uint64_t ka = make_sdesc(smem_u32(s.kv[0]), 16, 1024, kSwizzle128B);
+    const uint64_t kr = make_sdesc(smem_u32(s.kv[0]) + kRopeOff, 16, 512, kSwizzle64B);
+    const uint64_t qa = make_sdesc(smem_u32(s.q), 16, 1024, kSwizzle128B);
+    const uint64_t qr = make_sdesc(smem_u32(s.q) + 4 * kQChunk, 16, 512, kSwizzle64B);
+    int i = 0, nq = 0;
+    bool ok = true;
+    while (ok && next_seg(p, cur, g)) {
+      // the segment's q rows: every QK before has completed (waited for below)
+      if (leader) {
+        const int row = g.t0 * p.H + g.h0;
+        const uint32_t bar = smem_u32(&s.bar_qraw), dst = smem_u32(s.q);
+        mbar_arrive_expect_tx(bar, NR * kD * QP);
+        if (QP == 2) {
+          for (int c = 0; c < 9; ++c) tma_load_2d(dst + c * (NR * 128), &tq, c * 128, row, bar);
+        } else {
+          for (int c = 0; c < 4; ++c) tma_load_2d(dst + c * kQChunk, &tq, c * 128, row, bar);
+          tma_load_2d(dst + 4 * kQChunk, &tqr, 512, row, bar);
+        }
+      }
+      __syncwarp();
+      ++nq;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_q), (nq - 1) & 1, p.err));
+      for (int j = 0; ok && j < g.nb; ++j, ++i) {
+        const int slot = i % kNST, buf = i & 1;
+        const bool w = (i < 2 || mbar_wait(smem_u32(&s.bar_s_free[buf]), ((i >> 1) - 1) & 1, p.err)) &&
+                       mbar_wait(smem_u32(&s.bar_full[slot]), (i / kNST) & 1, p.err);
+        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+        tc_fence_after();
+        if (leader) {
+          const uint64_t so = static_cast<uint64_t>(slot * (kSlot >> 4));
+          const uint32_t d = tmem + kTmemS + buf * kQN;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f8f6f4_ss(d, ka + so + static_cast<uint64_t>((c * kChunk + kk * 32) >> 4),
+                            qa + static_cast<uint64_t>((c * kQChunk + kk * 32) >> 4), IDESC, (c | kk) ? 1u : 0u);
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk)
+            mma_f8f6f4_ss(d, kr + so + static_cast<uint64_t>((kk * 32) >> 4), qr + static_cast<uint64_t>((kk * 32) >> 4),
+                          IDESC, 1u);
+          mma_commit(smem_u32(&s.bar_s[buf]));
+        }
+        __syncwarp();
+      }
+      // q's place is free once the segment's last QK has completed
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_s[(i - 1) & 1]), ((i - 1) >> 1) & 1, p.err));
+    }
+    if (leader) mma_commit(smem_u32(&s.bar_drain[0]));
+    __syncwarp();
+    mbar_wait(smem_u32(&s.bar_drain[0]), 0, p.err);
+    if (nq > 0) mbar_wait(smem_u32(&s.bar_qraw), (nq - 1) & 1, p.err);
+  } else if (warp == kPvWarp) {
+    // ==================================================================== PV
+    Cursor cur = start;
+    Seg g;
+    const bool leader = elect_one();
+    constexpr uint32_t IDESC = idesc_e4m3_f32(128, kPN, 1, 1);
+    const uint64_t va = make_sdesc(smem_u32(s.kv[0]), kChunk, 1024, kSwizzle128B);
+    const uint64_t ph = make_sdesc(smem_u32(s.kv[0]) + kRopeOff, kBK * 64, 512, kSwizzle64B);
+    const uint64_t pl = make_sdesc(smem_u32(s.plo), kBK * 64, 512, kSwizzle64B);
+    int i = 0;
+    bool ok = true;
+    while (ok && next_seg(p, cur, g)) {
+      for (int j = 0; ok && j < g.nb; ++j, ++i) {
+        const int slot = i % kNST;
+        const uint64_t so = static_cast<uint64_t>(slot * (kSlot >> 4));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_p[i & 1][h]), (i >> 1) & 1, p.err))) { ok = false; break; }
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int ps = 0; ps < kPasses; ++ps)
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int tile = 0; tile < 4; ++tile) {
+                  const int key = h * 64 + kk * 32;
+                  mma_f8f6f4_ss(tmem + tile * kPN, va + so + static_cast<uint64_t>((tile * kChunk + key * 128) >> 4),
+                                (ps == 0 ? ph + so : pl) + static_cast<uint64_t>((key * 64) >> 4), IDESC,
+                                (j > 0 || (ps | kk | h)) ? 1u : 0u);
+                }
+            mma_commit(smem_u32(&s.bar_empty[slot][h]));
+            if (h == 1) mma_commit(smem_u32(&s.bar_pv[i & 1]));
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (leader) mma_commit(smem_u32(&s.bar_drain[1]));
+    __syncwarp();
+    mbar_wait(smem_u32(&s.bar_drain[1]), 0, p.err);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kQkWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the parts of one cut item, a row (token, head) per CTA half:
+//   out = sum_c 2^(L_c - M) O_c / (sum_c 2^(L_c - M) + 2^(sink - M)).
+constexpr int kJoinRows = 2;
+template <int NR>
+__global__ void __launch_bounds__(128 * kJoinRows) join_kernel(const Params p) {
+  const Cut cut = p.cuts[blockIdx.x + 1];
+  if (cut.first_cta < 0) return;
+  const int row = blockIdx.y * kJoinRows + threadIdx.x / 128, col = threadIdx.x % 128;
+  if (row >= cut.rows) return;
+  const int head = p.groups > 1 ? cut.h0 + row : row % p.H;
+  const float sk = p.sink ? p.sink[head] * kLog2e : -INFINITY;
+  const auto slot = [&](int c) { return static_cast<int64_t>(2 * c + (c == cut.first_cta ? 1 : 0)) * NR + row; };
+  float top = sk;
+  for (int c = cut.first_cta; c <= cut.last_cta; ++c) top = fmaxf(top, p.part_lse[slot(c)]);
+  const float m = top == -INFINITY ? 0.f : top;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = exp2f(sk - m);
+#pragma unroll 4
+  for (int c = cut.first_cta; c <= cut.last_cta; ++c) {
+    const float w = exp2f(p.part_lse[slot(c)] - m);  // 0 for a part without keys, whose O is 0
+    const float4 o = __ldcs(reinterpret_cast<const float4*>(p.part_o + slot(c) * kDV) + col);
+    l += w;
+    acc.x = fmaf(w, o.x, acc.x);
+    acc.y = fmaf(w, o.y, acc.y);
+    acc.z = fmaf(w, o.z, acc.z);
+    acc.w = fmaf(w, o.w, acc.w);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(cut.row0 + row) * kDV)[col] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+template <int NR, int QP, bool ROWSCALE>
+static smla_status_t launch(const DenseDecodeArgs& a, Params p, int grid, cudaStream_t stream) {
+  CUtensorMap tq, tqr, tk, tr;
+  const uint64_t q_rows = static_cast<uint64_t>(a.T) * a.H;
+  const uint32_t box = std::min(a.seqs->page_size, kBK / 2);
+  bool enc = encode_tma_2d_u8(&tk, a.latent, kD, a.phys_rows, 128, box, 128) &&
+             encode_tma_2d_u8(&tr, a.latent, kD, a.phys_rows, 64, box, 64) &&
+             encode_tma_2d_u8(&tq, a.q, kD * QP, q_rows, 128, NR, 128);
+  tqr = tq;
+  if (QP == 1) enc = enc && encode_tma_2d_u8(&tqr, a.q, kD, q_rows, 64, NR, 64);
+  if (!enc) return fail(SMLA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the dense-decode tensor maps");
+  constexpr size_t smem = sizeof(Smem<NR, QP>);
+  static_assert(smem <= 232448, "shared memory exceeds a CTA's 227 KB");
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<NR, QP, ROWSCALE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return fail_cuda(e, "dense decode smem attribute");
+  decode_kernel<NR, QP, ROWSCALE><<<grid, kThreads, smem, stream>>>(tq, tqr, tk, tr, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return fail_cuda(e, "dense decode launch");
+  if (grid > 1) {
+    join_kernel<NR><<<dim3(grid - 1, NR / kJoinRows), 128 * kJoinRows, 0, stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return fail_cuda(e, "dense decode join launch");
+  }
+  return SMLA_OK;
+}
+
+// Tokens that share an item: as many as a sequence has on average, while their
+// rows fit 64 (16 rows cost 1360 cycles of MMAs a block, 64 rows 2688).
+static int tokens_per_item(int T, int B, int H) {
+  if (H >= 48) return 1;
+  int n = 1;
+  while (n * H < 64 && n * B < T) n *= 2;
+  return n;
+}
+static int rows_per_item(int T, int B, int H) { return H >= 48 ? 64 : tokens_per_item(T, B, H) * H; }
+static int decode_grid(int T, int H, int max_kv_len) {
+  const int64_t blocks = static_cast<int64_t>(T) * std::max(1, H / 64) * ((max_kv_len + kBK - 1) / kBK);
+  return static_cast<int>(std::min<int64_t>(device_sm_count(), std::max<int64_t>(blocks, 1)));
+}
+
+}  // namespace dd
+
+size_t dense_decode_workspace_bytes(int T, int H, int max_kv_len) {
+  using namespace dd;
+  const size_t grid = decode_grid(T, H, max_kv_len), nr = rows_per_item(T, 1, H);  // (the most rows any batch of T gives)
+  if (grid <= 1) return 0;
+  return 2 * grid * nr * (kDV + 1) * sizeof(float) + ((grid * sizeof(Cut) + 255) & ~size_t(255)) + 256;
+}
+
+smla_status_t launch_dense_decode(const DenseDecodeArgs& a, unsigned* err, cudaStream_t stream) {
+  using namespace dd;
+  const int B = a.seqs->B, nr = rows_per_item(a.T, B, a.H), grid = decode_grid(a.T, a.H, a.max_kv_len);
+  Params p{};
+  p.seqs = seqs_dev(*a.seqs);
+  p.phys_rows = a.phys_rows;
+  p.scales = a.scales;
+  p.T = a.T;
+  p.H = a.H;
+  p.tok_per_item = tokens_per_item(a.T, B, a.H);
+  p.groups = std::max(1, a.H / 64);
+  p.softmax_scale = a.softmax_scale;
+  p.sink = a.sink;
+  p.out = a.out;
+  p.err = err;
+  if (grid > 1) {
+    p.part_o = static_cast<float*>(a.workspace);
+    p.part_lse = p.part_o + static_cast<size_t>(2) * grid * nr * kDV;
+    p.cuts = reinterpret_cast<Cut*>(p.part_lse + static_cast<size_t>(2) * grid * nr);
+  }
+  const bool bf16 = a.q_dtype == SMLA_BF16, rows = a.scales != nullptr;
+  const auto go = [&](auto nr_c) {
+    constexpr int NR = decltype(nr_c)::value;
+    if (bf16) return rows ? launch<NR, 2, true>(a, p, grid, stream) : launch<NR, 2, false>(a, p, grid, stream);
+    return rows ? launch<NR, 1, true>(a, p, grid, stream) : launch<NR, 1, false>(a, p, grid, stream);
+  };
+  if (nr == 64) return go(std::integral_constant<int, 64>{});
+  if (nr == 32) return go(std::integral_constant<int, 32>{});
+  return go(std::integral_constant<int, 16>{});
+}
+
+}  // namespace smla

@@ -151,4 +151,21 @@ int expanded_splits(int T, int S, int B, int H);
 size_t expanded_workspace_bytes(int T, int H, int nsplit);
 smla_status_t launch_expanded(const ExpandedArgs& a, unsigned* err, cudaStream_t stream);
 
+// Dense decode over an e4m3 cache with unit or per-row scales.
+struct DenseDecodeArgs {
+  const void* q;
+  int q_dtype;
+  const uint8_t* latent;
+  int64_t phys_rows;
+  const float* scales;  // null: unit
+  const smla_seqs_t* seqs;
+  int T, H, max_kv_len;
+  float softmax_scale;
+  const float* sink;
+  uint16_t* out;
+  void* workspace;
+};
+size_t dense_decode_workspace_bytes(int T, int H, int max_kv_len);
+smla_status_t launch_dense_decode(const DenseDecodeArgs& a, unsigned* err, cudaStream_t stream);
+
 }  // namespace smla

@@ -116,7 +116,8 @@ def _close(got, ref, tol):
 
 MODES = [("bf16", "unit"), ("bf16", "row"), ("e4m3", "unit"), ("e4m3", "row"), ("e4m3", "block"), ("bf16", "bf16")]
 SHAPES = [([1], [1], 16, 64), ([1, 1, 1], [127, 128, 129], 64, 64), ([2, 0, 3, 1], [700, 5, 3, 2049], 128, 16),
-          ([4, 4], [4100, 77], 16, 8), ([1], [20011], 32, 256), ([3, 2], [300, 1000], 48, 64)]
+          ([4, 4], [4100, 77], 16, 8), ([1], [20011], 32, 256), ([3, 2], [300, 1000], 48, 64),
+          ([2, 1, 4, 1], [30001, 5, 9000, 12345], 64, 64), ([1, 1], [60000, 777], 16, 128)]
 
 
 @pytest.mark.parametrize("qd,mode", MODES)
