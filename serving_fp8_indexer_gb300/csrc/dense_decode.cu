@@ -118,51 +118,33 @@ __device__ __forceinline__ SeqWork seq_work(const Params& p, int b) {
   return w;
 }
 
-// All blocks, by the whole warp.
-__device__ __forceinline__ int64_t total_blocks(const Params& p, int lane) {
-  int64_t n = 0;
-  for (int b = lane; b < p.seqs.B; b += 32) {
-    const SeqWork w = seq_work(p, b);
-    n += static_cast<int64_t>(w.items) * w.nblk;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n;
-}
+// All blocks (below 2^31: the launcher checks the bound), by the whole warp.
+__device__ __forceinline__ int warp_sum(int n) { return __reduce_add_sync(0xffffffffu, n); }
 
-// Sequence that holds block x of the line (x below the total), and the line's
-// position of its first block; by the whole warp.
-__device__ __forceinline__ int find_block(const Params& p, int64_t x, int lane, int64_t& first) {
-  int64_t base = 0;
-  for (int b0 = 0; b0 < p.seqs.B; b0 += 32) {
-    int64_t n = 0;
-    if (b0 + lane < p.seqs.B) {
-      const SeqWork w = seq_work(p, b0 + lane);
-      n = static_cast<int64_t>(w.items) * w.nblk;
-    }
-    int64_t inc = n;
+// Sequence that holds block x of the line, and the line's position of its
+// first block; by the whole warp, lane l holding sequence b0 + l's blocks n.
+// -1 when x lies behind these; `base` then moves past them.
+__device__ __forceinline__ int find_among(int x, int n, int lane, int& base) {
+  int inc = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += up;
-    }
-    const bool here = x >= base + inc - n && x < base + inc;
-    const unsigned hit = __ballot_sync(0xffffffffu, here);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      first = base + __shfl_sync(0xffffffffu, inc - n, src);
-      return b0 + src;
-    }
-    base += __shfl_sync(0xffffffffu, inc, 31);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
   }
-  first = base;
+  const unsigned hit = __ballot_sync(0xffffffffu, x >= base + inc - n && x < base + inc);
+  if (hit) {
+    const int src = __ffs(hit) - 1;
+    base += __shfl_sync(0xffffffffu, inc - n, src);
+    return src;
+  }
+  base += __shfl_sync(0xffffffffu, inc, 31);
   return -1;
 }
 
 // A CTA's walk along its part of the line.
 struct Cursor {
   int b, item, blk;  // next: sequence, item of the sequence, block of the item
-  int64_t left;      // blocks left
+  int left;          // blocks left
 };
 // One item's blocks within the part.
 struct Seg {
@@ -187,7 +169,7 @@ __device__ __forceinline__ bool next_seg(const Params& p, Cursor& c, Seg& s) {
   s.rows = p.groups > 1 ? 64 : s.ntok * p.H;
   s.pos1 = w.kv - w.q_len + tg * p.tok_per_item + 1;
   s.j0 = c.blk;
-  s.nb = static_cast<int>(min(static_cast<int64_t>(w.nblk - c.blk), c.left));
+  s.nb = min(w.nblk - c.blk, c.left);
   s.whole = s.nb == w.nblk;
   c.left -= s.nb;
   c.blk += s.nb;
@@ -262,33 +244,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   S& s = *reinterpret_cast<S*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // this CTA's part of the line
-  Cursor start;
-  {
-    const int64_t total = total_blocks(p, lane);
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t x0 = per * blockIdx.x;
-    int64_t first = 0;
-    start.b = x0 < total ? find_block(p, x0, lane, first) : -1;
-    Cut cut{-1, 0, 0, 0, 0};
-    if (start.b >= 0) {
-      const SeqWork w = seq_work(p, start.b);
-      start.item = static_cast<int>((x0 - first) / w.nblk);
-      start.blk = static_cast<int>((x0 - first) - static_cast<int64_t>(start.item) * w.nblk);
-      start.left = min(per, total - x0);
-      if (start.blk > 0) {
-        const int64_t w0 = x0 - start.blk;  // the item's first block
-        Cursor c = start;
-        Seg g;
-        next_seg(p, c, g);
-        if (w0 / per + 1 == blockIdx.x)
-          cut = {static_cast<int>(w0 / per), static_cast<int>((w0 + w.nblk - 1) / per), g.t0 * p.H + g.h0, g.rows, g.h0};
-      }
-    }
-    if (threadIdx.x == 0 && p.cuts) p.cuts[blockIdx.x] = cut;
-    if (start.b < 0) return;
-  }
-
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&s.bar_qraw), 1);
     mbar_init(smem_u32(&s.bar_q), kSoftThreads);
@@ -312,12 +267,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(&s.tmem_base), kTmemCols);
     tmem_relinquish();
   }
+  // (the descriptors' and the line's cold reads overlap)
+  if (threadIdx.x == kTmaWarp * 32) {
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tr);
+    if (QP == 1) tma_prefetch_desc(&tqr);
+  }
+  // this CTA's part of the line
+  Cursor start{-1, 0, 0, 0};
+  {
+    const int B = p.seqs.B;
+    int n0 = 0, total = 0;  // n0: the lane's blocks among the first 32 sequences
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      int n = 0;
+      if (b0 + lane < B) {
+        const SeqWork w = seq_work(p, b0 + lane);
+        n = w.items * w.nblk;
+      }
+      if (b0 == 0) n0 = n;
+      total += warp_sum(n);
+    }
+    const int grid = gridDim.x, cta = blockIdx.x;
+    const int per = (total + grid - 1) / grid;
+    const int x0 = total - per * cta > 0 ? per * cta : total;  // (per * cta stays below 2^31: cta < grid)
+    Cut cut{-1, 0, 0, 0, 0};
+    if (x0 < total) {
+      int base = 0;
+      start.b = find_among(x0, n0, lane, base);
+      for (int b0 = 32; start.b < 0 && b0 < B; b0 += 32) {
+        int n = 0;
+        if (b0 + lane < B) {
+          const SeqWork w = seq_work(p, b0 + lane);
+          n = w.items * w.nblk;
+        }
+        const int at = find_among(x0, n, lane, base);
+        if (at >= 0) start.b = b0 + at;
+      }
+      const SeqWork w = seq_work(p, max(start.b, 0));
+      start.item = (x0 - base) / w.nblk;
+      start.blk = x0 - base - start.item * w.nblk;
+      start.left = min(per, total - x0);
+      if (start.b >= 0 && start.blk > 0) {
+        const int w0 = x0 - start.blk;  // the item's first block
+        if (w0 / per + 1 == cta) {
+          Cursor c = start;
+          Seg g;
+          next_seg(p, c, g);
+          cut = {w0 / per, (w0 + w.nblk - 1) / per, g.t0 * p.H + g.h0, g.rows, g.h0};
+        }
+      }
+    }
+    if (threadIdx.x == 0 && p.cuts) p.cuts[cta] = cut;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
 
-  if (warp < 8) {
+  if (start.b < 0) {
+    // nothing left of the line for this CTA
+  } else if (warp < 8) {
     // ===================================================== softmax, epilogue
     const int r = threadIdx.x & 127;    // key lane
     const int hb = (warp >> 2) * NC;    // rows [hb, hb + NC)
@@ -359,13 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          int e = 0;
-          if (amax > 0.f) {
-            int ex;
-            frexpf(amax, &ex);
-            e = 8 - ex;
-          }
-          const float sigma = ldexpf(1.f, e);
+          // 2^e that puts amax into [128, 256), from its exponent bits; capped
+          // (an all-zero or subnormal row keeps a finite factor)
+          const int e = min(7 + 127 - static_cast<int>(__float_as_uint(amax) >> 23), 120);
+          const float sigma = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
           if (row < NR) {
 #pragma unroll
             for (int c = 0; c < 9; ++c) {
@@ -404,20 +411,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(smem_u32(&s.bar_q));
       return true;
     };
-    // scale of the thread's key of block j (1 outside the keys)
-    auto key_scale = [&](const Seg& g, int j) -> float {
-      if (!ROWSCALE) return 1.f;
+    // Page of the thread's key of block j (-1 outside the keys), and its scale
+    // (1 there, and on a bad page, which the TMA warp reports).  The page is
+    // read two blocks ahead and the scale one, so that neither read is waited
+    // for inside a segment.
+    auto key_page = [&](const Seg& g, int j) -> int {
       const int key = (g.j0 + j) * kBK + r;
-      if (key >= seg_keys(g)) return 1.f;
-      const int pid = p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)];
+      return ROWSCALE && key < seg_keys(g)
+                 ? p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)]
+                 : -1;
+    };
+    auto key_scale = [&](const Seg& g, int j, int pid) -> float {
+      const int key = (g.j0 + j) * kBK + r;
       const int64_t row = (static_cast<int64_t>(pid) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
-      return pid < 0 || row >= p.phys_rows ? 1.f : p.scales[row];  // (a bad page is reported by the TMA warp)
+      return !ROWSCALE || pid < 0 || row >= p.phys_rows ? 1.f : p.scales[row];
     };
     Cursor cur = start;
     Seg g;
-    bool ok = next_seg(p, cur, g) && convert_q(g);
+    bool ok = next_seg(p, cur, g);
+    float sr_next = key_scale(g, 0, key_page(g, 0));
+    int pid_next = g.nb > 1 ? key_page(g, 1) : -1;
+    ok = ok && convert_q(g);
     int gb = 0;  // blocks of the segments before
-    float sr_next = ok ? key_scale(g, 0) : 1.f;
     bool more = ok;
     while (ok && more) {
       const int n_item = seg_keys(g);
@@ -436,10 +451,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < g.nb; ++j) {
         const int i = gb + j, slot = i % kNST, buf = i & 1;
         const float sr = sr_next;
-        if (j + 1 < g.nb)
-          sr_next = key_scale(g, j + 1);
-        else if (has_next)
-          sr_next = key_scale(gn, 0);
+        if (j + 1 < g.nb) {
+          sr_next = key_scale(g, j + 1, pid_next);
+          if (j + 2 < g.nb) pid_next = key_page(g, j + 2);
+        } else if (has_next) {
+          sr_next = key_scale(gn, 0, key_page(gn, 0));
+          if (gn.nb > 1) pid_next = key_page(gn, 1);
+        }
         if (!named_bar_and(1, kSoftThreads, mbar_wait(smem_u32(&s.bar_s[buf]), (i >> 1) & 1, p.err))) { ok = false; break; }
         tc_fence_after();
         float y[NC];
@@ -662,55 +680,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kTmaWarp) {
     // ============================================================= key blocks
+    // A block's keys come in parts of a page, up to 64 keys each: five boxes a
+    // part (four 128-byte columns, one of 64), all issued by one lane with the
+    // part's page handed to it (boxes spread over the lanes are issued one
+    // lane at a time, at 200 cycles a box).  Lane k reads part k's page, one
+    // block ahead.
+    const bool leader = elect_one();
+    const int box = min(1 << p.seqs.page_shift, kBK / 2);
+    const int half_parts = (kBK / 2) / box;
+    const auto parts_of = [&](const Seg& g, int j) {  // parts with keys in them
+      return (min(kBK, max(0, seg_keys(g) - (g.j0 + j) * kBK)) + box - 1) / box;
+    };
+    const auto read_page = [&](const Seg& g, int j) {
+      const int key = (g.j0 + j) * kBK + lane * box;
+      return lane < parts_of(g, j)
+                 ? p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)]
+                 : 0;
+    };
     Cursor cur = start;
-    Seg g;
+    Seg g, gn;
     int i = 0;
-    bool ok = true;
-    const int box = min(1 << p.seqs.page_shift, kBK / 2);  // keys of a TMA box
-    while (ok && next_seg(p, cur, g)) {
-      const int n_item = seg_keys(g);
+    bool ok = true, more = next_seg(p, cur, g);
+    int pid = read_page(g, 0), pid_n = 0;
+    while (ok && more) {
+      more = next_seg(p, cur, gn);
       for (int j = 0; ok && j < g.nb; ++j) {
-        const int slot = i % kNST, key0 = (g.j0 + j) * kBK;
-        const int nbox = min(kBK, max(0, n_item - key0) + box - 1) / box;  // boxes with keys in them
+        if (j + 1 < g.nb)
+          pid_n = read_page(g, j + 1);
+        else if (more)
+          pid_n = read_page(gn, 0);
+        const int slot = i % kNST, key0 = (g.j0 + j) * kBK, parts = parts_of(g, j);
         const uint32_t bar = smem_u32(&s.bar_full[slot]);
         const uint32_t dst = smem_u32(s.kv[slot]);
         const uint32_t par = ((i / kNST) & 1) ^ 1;
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_empty[slot][0]), par, p.err))) { ok = false; break; }
-        if (lane == 0) {
-          if (nbox > 0)
-            mbar_arrive_expect_tx(bar, nbox * box * kD);
+        if (leader) {
+          if (parts > 0)
+            mbar_arrive_expect_tx(bar, parts * box * kD);
           else
             mbar_arrive(bar);
         }
-        __syncwarp();
-        // five boxes (four 128-byte columns, one of 64) of each page part, a
-        // lane each; the second half of the keys once PV has given it back
-        const int half_boxes = (kBK / 2) / box;
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1 && nbox > half_boxes &&
+        // the second half of the keys once PV has given it back
+        for (int k = 0; k < parts; ++k) {
+          if (k == half_parts &&
               !__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_empty[slot][1]), par, p.err))) {
             ok = false;
             break;
           }
-          const int k1 = min(nbox, (h + 1) * half_boxes);
-          for (int u = h * half_boxes * 5 + lane; u < k1 * 5; u += 32) {
-            const int k = u / 5, c = u - k * 5, key = key0 + k * box;
-            const int pid =
-                p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)];
-            int64_t row = (static_cast<int64_t>(pid) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
-            if (pid < 0 || row >= p.phys_rows) {
-              atomicOr(p.err, kErrPage);
-              row = 0;
-            }
-            if (c < 4)
-              tma_load_2d(dst + c * kChunk + k * box * 128, &tk, c * 128, static_cast<int>(row), bar);
-            else
-              tma_load_2d(dst + kRopeOff + k * box * 64, &tr, 512, static_cast<int>(row), bar);
+          const int pg = __shfl_sync(0xffffffffu, pid, k), key = key0 + k * box;
+          int64_t row64 = (static_cast<int64_t>(pg) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
+          if (pg < 0 || row64 >= p.phys_rows) {
+            if (leader) atomicOr(p.err, kErrPage);
+            row64 = 0;
+          }
+          const int row = static_cast<int>(row64);
+          if (leader) {
+            const uint32_t d = dst + k * box * 128;
+            tma_load_2d(d, &tk, 0, row, bar);
+            tma_load_2d(d + kChunk, &tk, 128, row, bar);
+            tma_load_2d(d + 2 * kChunk, &tk, 256, row, bar);
+            tma_load_2d(d + 3 * kChunk, &tk, 384, row, bar);
+            tma_load_2d(dst + kRopeOff + k * box * 64, &tr, 512, row, bar);
           }
           __syncwarp();
         }
         ++i;
+        pid = pid_n;
       }
+      g = gn;
     }
     // nothing is still landing when the CTA ends
     for (int sl = 0; sl < kNST; ++sl) {
@@ -736,8 +773,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bar = smem_u32(&s.bar_qraw), dst = smem_u32(s.q);
         mbar_arrive_expect_tx(bar, NR * kD * QP);
         if (QP == 2) {
+#pragma unroll
           for (int c = 0; c < 9; ++c) tma_load_2d(dst + c * (NR * 128), &tq, c * 128, row, bar);
         } else {
+#pragma unroll
           for (int c = 0; c < 4; ++c) tma_load_2d(dst + c * kQChunk, &tq, c * 128, row, bar);
           tma_load_2d(dst + 4 * kQChunk, &tqr, 512, row, bar);
         }
@@ -823,25 +862,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kQkWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the parts of one cut item, a row (token, head) per CTA half:
+// Joins the parts of one cut item, a row (token, head) per CTA:
 //   out = sum_c 2^(L_c - M) O_c / (sum_c 2^(L_c - M) + 2^(sink - M)).
-constexpr int kJoinRows = 2;
+// Four groups of 128 threads (a float4 of the row each) take every fourth
+// part, so that a long item's parts are read side by side.
+constexpr int kJoinGroups = 4;
 template <int NR>
-__global__ void __launch_bounds__(128 * kJoinRows) join_kernel(const Params p) {
+__global__ void __launch_bounds__(128 * kJoinGroups) join_kernel(const Params p) {
   const Cut cut = p.cuts[blockIdx.x + 1];
-  if (cut.first_cta < 0) return;
-  const int row = blockIdx.y * kJoinRows + threadIdx.x / 128, col = threadIdx.x % 128;
-  if (row >= cut.rows) return;
+  const int row = blockIdx.y;
+  if (cut.first_cta < 0 || row >= cut.rows) return;
+  __shared__ float4 s_acc[kJoinGroups - 1][128];
+  __shared__ float s_top[kJoinGroups * 4], s_l[kJoinGroups - 1];
+  const int grp = threadIdx.x / 128, col = threadIdx.x % 128, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int head = p.groups > 1 ? cut.h0 + row : row % p.H;
   const float sk = p.sink ? p.sink[head] * kLog2e : -INFINITY;
   const auto slot = [&](int c) { return static_cast<int64_t>(2 * c + (c == cut.first_cta ? 1 : 0)) * NR + row; };
   float top = sk;
-  for (int c = cut.first_cta; c <= cut.last_cta; ++c) top = fmaxf(top, p.part_lse[slot(c)]);
+  for (int c = cut.first_cta + threadIdx.x; c <= cut.last_cta; c += 128 * kJoinGroups) top = fmaxf(top, p.part_lse[slot(c)]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+  for (int w = 0; w < kJoinGroups * 4; ++w) top = fmaxf(top, s_top[w]);
   const float m = top == -INFINITY ? 0.f : top;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = exp2f(sk - m);
+  float l = grp == 0 ? exp2f(sk - m) : 0.f;
 #pragma unroll 4
-  for (int c = cut.first_cta; c <= cut.last_cta; ++c) {
+  for (int c = cut.first_cta + grp; c <= cut.last_cta; c += kJoinGroups) {
     const float w = exp2f(p.part_lse[slot(c)] - m);  // 0 for a part without keys, whose O is 0
     const float4 o = __ldcs(reinterpret_cast<const float4*>(p.part_o + slot(c) * kDV) + col);
     l += w;
@@ -849,6 +897,21 @@ __global__ void __launch_bounds__(128 * kJoinRows) join_kernel(const Params p) {
     acc.y = fmaf(w, o.y, acc.y);
     acc.z = fmaf(w, o.z, acc.z);
     acc.w = fmaf(w, o.w, acc.w);
+  }
+  if (grp > 0) {
+    s_acc[grp - 1][col] = acc;
+    if (col == 0) s_l[grp - 1] = l;
+  }
+  __syncthreads();
+  if (grp > 0) return;
+#pragma unroll
+  for (int k = 0; k < kJoinGroups - 1; ++k) {
+    const float4 o = s_acc[k][col];
+    l += s_l[k];
+    acc.x += o.x;
+    acc.y += o.y;
+    acc.z += o.z;
+    acc.w += o.w;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
@@ -877,7 +940,7 @@ static smla_status_t launch(const DenseDecodeArgs& a, Params p, int grid, cudaSt
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "dense decode launch");
   if (grid > 1) {
-    join_kernel<NR><<<dim3(grid - 1, NR / kJoinRows), 128 * kJoinRows, 0, stream>>>(p);
+    join_kernel<NR><<<dim3(grid - 1, NR), 128 * kJoinGroups, 0, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return fail_cuda(e, "dense decode join launch");
   }
@@ -909,6 +972,11 @@ size_t dense_decode_workspace_bytes(int T, int H, int max_kv_len) {
 
 smla_status_t launch_dense_decode(const DenseDecodeArgs& a, unsigned* err, cudaStream_t stream) {
   using namespace dd;
+  const int64_t line = static_cast<int64_t>(a.T) * std::max(1, a.H / 64) *
+                       ((static_cast<int64_t>(a.seqs->max_pages) * a.seqs->page_size + kBK - 1) / kBK + 1);
+  if (line >= (int64_t(1) << 30))
+    return fail(SMLA_ERR_UNSUPPORTED, "dense decode: T=%d tokens of up to %d pages of %d keys are too much for one call",
+                a.T, a.seqs->max_pages, a.seqs->page_size);
   const int B = a.seqs->B, nr = rows_per_item(a.T, B, a.H), grid = decode_grid(a.T, a.H, a.max_kv_len);
   Params p{};
   p.seqs = seqs_dev(*a.seqs);
