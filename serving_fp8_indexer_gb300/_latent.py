@@ -14,52 +14,87 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import SMLA_BF16, SMLA_E4M3, SMLA_F32, RopeT, Seqs, _check, _ptr, _stream
+from ._lib import SMLA_BF16, SMLA_E4M3, SMLA_F32, RopeT, Seqs, SeqsT, _check, _stream
 
 ROPE_INTERLEAVED, ROPE_HALF = 0, 1
 _SCALINGS = {"plain": 0, "linear": 1, "yarn": 2}
 _DTYPES = {torch.bfloat16: SMLA_BF16, torch.uint8: SMLA_E4M3, torch.float32: SMLA_F32}
 
 
-def _here(*tensors: Optional[torch.Tensor]):
-    """The kernels launch on the current device: every tensor must be there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
-            raise ValueError(f"tensors must be on the current CUDA device (cuda:{dev}), got {t.device}")
+# These calls take a few microseconds on the GPU, so the checks below keep to
+# the cheapest queries of a tensor, and the message is put together only when
+# one fails.
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _rows(t: torch.Tensor, name: str, dtypes, ndim: int):
-    """Pointer and the leading strides (in elements) of a tensor whose last
-    dimension is dense.  A dimension of one element has no stride to speak
-    of: its row's width stands in."""
+def _refuse(t, name, dtypes, dev, ndim):
+    """The reason a tensor was not accepted, raised."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current CUDA device (cuda:{dev}), got {t.device}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _flat(t, name, dtype, dev, ndim):
+    """Pointer of a contiguous tensor of this type on the current device (the
+    kernels launch there); None for None."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.dim() == ndim and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, (dtype,), dev, ndim)
+
+
+def _rows(t, name, dtypes, dev, ndim):
+    """Pointer, shape and leading strides (in elements) of a tensor whose last
+    dimension is dense.  A dimension of one element has no stride to speak of:
+    its row's width stands in."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.get_device() != dev or t.dim() != ndim:
+        _refuse(t, name, dtypes, dev, ndim)
+    shape, strides = t.shape, t.stride()
+    width = shape[-1]
+    if width > 1 and strides[-1] != 1:
         raise ValueError(f"{name}'s last dimension must be dense")
-    strides = [t.stride(d) if t.shape[d] > 1 else t.shape[-1] for d in range(ndim - 1)]
-    return (t.data_ptr() if t.numel() else None), strides
+    if 1 in shape:
+        strides = tuple(st if n > 1 else width for st, n in zip(strides, shape))
+    return t.data_ptr(), shape, strides
 
 
-def _pool(pool: torch.Tensor):
-    if pool.dtype not in (torch.uint8, torch.bfloat16):
-        raise TypeError(f"pool must be torch.uint8 (e4m3 bytes) or torch.bfloat16, got {pool.dtype}")
-    return _ptr(pool, pool.dtype, "pool", 2), SMLA_BF16 if pool.dtype == torch.bfloat16 else SMLA_E4M3
+def _seqs(s: Seqs, dev: int) -> SeqsT:
+    i32 = torch.int32
+    return SeqsT(_flat(s.cu_q, "cu_q", i32, dev, 1), _flat(s.kv_len, "kv_len", i32, dev, 1),
+                 _flat(s.page_table, "page_table", i32, dev, 2), s.B, s.max_pages, s.page_size, s.T)
 
 
-def _check_scales(scales: Optional[torch.Tensor], pool: torch.Tensor, sbs: int):
+def _on(stream, dev: int) -> int:
+    return _raw_stream(dev) if stream is None else _stream(stream)
+
+
+def _pool(pool, dev: int):
+    """(pointer, type code, rows, row width) of a cache pool."""
+    bf16 = pool.dtype is torch.bfloat16
+    ptr = _flat(pool, "pool", torch.bfloat16 if bf16 else torch.uint8, dev, 2)
+    rows, width = pool.shape
+    return ptr, SMLA_BF16 if bf16 else SMLA_E4M3, rows, width
+
+
+def _scales(scales, rows: int, D: int, sbs: int, dev: int):
+    """Pointer of a pool's scales [rows, ceil(D / sbs)]; None without."""
     if sbs == 0:
         if scales is not None:
             raise ValueError("scales must be None with scale_block_size 0")
-        return
-    D = int(pool.shape[1])
-    want = (int(pool.shape[0]), 1 if sbs >= D else D // max(sbs, 1))
-    if scales is None or tuple(scales.shape) != want:
+        return None
+    ptr = _flat(scales, "scales", torch.float32, dev, 2)
+    want = (rows, 1 if sbs >= D else D // max(sbs, 1))
+    if scales is None or scales.shape != want:
         raise ValueError(f"scales must be {want}, got {None if scales is None else tuple(scales.shape)}")
+    return ptr
 
 
 class Rope:
@@ -70,8 +105,9 @@ class Rope:
     def __init__(self, inv_freq: torch.Tensor, offset: int, layout: int = ROPE_INTERLEAVED, amplitude: float = 1.0):
         self.inv_freq, self.offset, self.layout, self.amplitude = inv_freq, int(offset), int(layout), float(amplitude)
 
-    def as_c(self) -> RopeT:
-        return RopeT(_ptr(self.inv_freq, torch.float64, "inv_freq", 1), self.offset, 2 * self.inv_freq.shape[0],
+    def as_c(self, dev: Optional[int] = None) -> RopeT:
+        dev = _device() if dev is None else dev
+        return RopeT(_flat(self.inv_freq, "inv_freq", torch.float64, dev, 1), self.offset, 2 * self.inv_freq.shape[0],
                      self.layout, self.amplitude)
 
 
@@ -95,15 +131,15 @@ def rope(x: torch.Tensor, seqs: Seqs, rope: Rope, out: torch.Tensor, stream=None
     position.  x bf16 or f32 [T, H, D]; out bf16, f32 or uint8 (e4m3 bytes)
     [T, H, D], x itself for an in-place rotation.  Both may be strided views
     with dense rows."""
-    lib = _lib.load()
-    xp, xs = _rows(x, "x", (torch.bfloat16, torch.float32), 3)
-    op, os_ = _rows(out, "out", (torch.bfloat16, torch.float32, torch.uint8), 3)
-    _here(x, out, rope.inv_freq, seqs.cu_q, seqs.kv_len, seqs.page_table)
-    if x.shape != out.shape or int(x.shape[0]) != seqs.T:
-        raise ValueError(f"x {tuple(x.shape)} and out {tuple(out.shape)} must both be [T={seqs.T}, H, D]")
-    st = lib.smla_rope(xp, _DTYPES[x.dtype], xs[0], xs[1], seqs.as_c(), int(x.shape[1]), int(x.shape[2]),
-                       rope.as_c(), op, _DTYPES[out.dtype], os_[0], os_[1], _stream(stream))
-    _check(lib, st)
+    lib, dev = _lib._lib or _lib.load(), _device()
+    xp, shape, xs = _rows(x, "x", (torch.bfloat16, torch.float32), dev, 3)
+    op, out_shape, os_ = _rows(out, "out", (torch.bfloat16, torch.float32, torch.uint8), dev, 3)
+    if shape != out_shape or shape[0] != seqs.T:
+        raise ValueError(f"x {tuple(shape)} and out {tuple(out_shape)} must both be [T={seqs.T}, H, D]")
+    st = lib.smla_rope(xp, _DTYPES[x.dtype], xs[0], xs[1], _seqs(seqs, dev), shape[1], shape[2], rope.as_c(dev), op,
+                       _DTYPES[out.dtype], os_[0], os_[1], _on(stream, dev))
+    if st:
+        _check(lib, st)
     return out
 
 
@@ -115,40 +151,39 @@ def cache_append(x: torch.Tensor, seqs: Seqs, pool: torch.Tensor, scales: Option
     RMS-normalised over the first norm_weight.shape[0] columns when a weight
     is given, rotated, quantised (scales f32 [phys_rows, nscale] written too);
     rows_out bf16 [T, D] also receives the finished rows."""
-    lib = _lib.load()
-    xp, (xs,) = _rows(x, "x", (torch.bfloat16,), 2)
-    rp, (rs,) = _rows(rows_out, "rows_out", (torch.bfloat16,), 2) if rows_out is not None else (None, (x.shape[1],))
-    _here(x, pool, scales, rope.inv_freq if rope else None, norm_weight, rows_out, seqs.cu_q, seqs.kv_len,
-          seqs.page_table)
-    if int(x.shape[0]) != seqs.T or x.shape[1] != pool.shape[1]:
-        raise ValueError(f"x {tuple(x.shape)} must be [T={seqs.T}, D={int(pool.shape[1])}]")
-    if rows_out is not None and rows_out.shape != x.shape:
-        raise ValueError("rows_out must have x's shape")
-    _check_scales(scales, pool, scale_block_size)
-    pp, pd = _pool(pool)
-    st = lib.smla_cache_append(xp, xs, seqs.as_c(), int(x.shape[1]),
-                               _ptr(norm_weight, torch.bfloat16, "norm_weight", 1),
-                               0 if norm_weight is None else int(norm_weight.shape[0]), float(norm_eps),
-                               rope.as_c() if rope else RopeT(), pp, pd, int(pool.shape[0]),
-                               _ptr(scales, torch.float32, "scales", 2), int(scale_block_size), rp, rs,
-                               _stream(stream))
-    _check(lib, st)
+    lib, dev = _lib._lib or _lib.load(), _device()
+    xp, (T, D), xs = _rows(x, "x", (torch.bfloat16,), dev, 2)
+    rp, rs = None, D
+    if rows_out is not None:
+        rp, rows_shape, rs = _rows(rows_out, "rows_out", (torch.bfloat16,), dev, 2)
+        rs = rs[0]
+        if rows_shape != x.shape:
+            raise ValueError("rows_out must have x's shape")
+    pp, pd, phys_rows, width = _pool(pool, dev)
+    if T != seqs.T or D != width:
+        raise ValueError(f"x {tuple(x.shape)} must be [T={seqs.T}, D={width}]")
+    sp = _scales(scales, phys_rows, D, scale_block_size, dev)
+    st = lib.smla_cache_append(xp, xs[0], _seqs(seqs, dev), D, _flat(norm_weight, "norm_weight", torch.bfloat16, dev, 1),
+                               0 if norm_weight is None else norm_weight.shape[0], norm_eps,
+                               rope.as_c(dev) if rope is not None else RopeT(), pp, pd, phys_rows, sp, scale_block_size,
+                               rp, rs, _on(stream, dev))
+    if st:
+        _check(lib, st)
 
 
 def cache_gather(pool: torch.Tensor, scales: Optional[torch.Tensor], scale_block_size: int, seqs: Seqs,
                  rows: torch.Tensor, stream=None) -> torch.Tensor:
     """rows[t] bf16 = the cached row of seqs' token t, dequantised.  A Seqs
     whose cu_q is the running sum of kv_len reads the whole context."""
-    lib = _lib.load()
-    rp, (rs,) = _rows(rows, "rows", (torch.bfloat16,), 2)
-    _here(pool, scales, rows, seqs.cu_q, seqs.kv_len, seqs.page_table)
-    if int(rows.shape[0]) != seqs.T or rows.shape[1] != pool.shape[1]:
-        raise ValueError(f"rows {tuple(rows.shape)} must be [T={seqs.T}, D={int(pool.shape[1])}]")
-    _check_scales(scales, pool, scale_block_size)
-    pp, pd = _pool(pool)
-    st = lib.smla_cache_gather(pp, pd, int(pool.shape[0]), _ptr(scales, torch.float32, "scales", 2),
-                               int(scale_block_size), seqs.as_c(), int(rows.shape[1]), rp, rs, _stream(stream))
-    _check(lib, st)
+    lib, dev = _lib._lib or _lib.load(), _device()
+    rp, (T, D), rs = _rows(rows, "rows", (torch.bfloat16,), dev, 2)
+    pp, pd, phys_rows, width = _pool(pool, dev)
+    if T != seqs.T or D != width:
+        raise ValueError(f"rows {tuple(rows.shape)} must be [T={seqs.T}, D={width}]")
+    sp = _scales(scales, phys_rows, D, scale_block_size, dev)
+    st = lib.smla_cache_gather(pp, pd, phys_rows, sp, scale_block_size, _seqs(seqs, dev), D, rp, rs[0], _on(stream, dev))
+    if st:
+        _check(lib, st)
     return rows
 
 
@@ -166,27 +201,26 @@ def expanded_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor
     strided views with dense rows); cu_q, cu_kv int32 [B+1]; workspace a uint8
     CUDA tensor of at least expanded_prefill_workspace_size() bytes (None when
     that is 0); attn_sink f32 [H], lse f32 [T, H] (output)."""
-    lib = _lib.load()
-    bf = (torch.bfloat16,)
-    qp, (qt, qh) = _rows(q, "q", bf, 3)
-    kp, (kt, kh) = _rows(k_nope, "k_nope", bf, 3)
-    rp, (rt,) = _rows(k_rope, "k_rope", bf, 2)
-    vp, (vt, vh) = _rows(v, "v", bf, 3)
-    _here(q, k_nope, k_rope, v, cu_q, cu_kv, out, workspace, attn_sink, lse)
-    T, H, S, B = int(q.shape[0]), int(q.shape[1]), int(v.shape[0]), int(cu_q.shape[0]) - 1
-    if (tuple(q.shape) != (T, H, 192) or tuple(k_nope.shape) != (S, H, 128) or tuple(k_rope.shape) != (S, 64) or
-            tuple(v.shape) != (S, H, 128) or tuple(out.shape) != (T, H, 128) or tuple(cu_kv.shape) != (B + 1,) or
-            (attn_sink is not None and tuple(attn_sink.shape) != (H,)) or
-            (lse is not None and tuple(lse.shape) != (T, H))):
+    lib, dev = _lib._lib or _lib.load(), _device()
+    bf, f32, i32 = (torch.bfloat16,), torch.float32, torch.int32
+    qp, q_shape, qs = _rows(q, "q", bf, dev, 3)
+    kp, k_shape, ks = _rows(k_nope, "k_nope", bf, dev, 3)
+    rp, r_shape, rs = _rows(k_rope, "k_rope", bf, dev, 2)
+    vp, v_shape, vs = _rows(v, "v", bf, dev, 3)
+    T, H, S, B = q_shape[0], q_shape[1], v_shape[0], cu_q.shape[0] - 1
+    if (q_shape[2] != 192 or k_shape != (S, H, 128) or r_shape != (S, 64) or v_shape != (S, H, 128) or
+            out.shape != (T, H, 128) or cu_kv.shape != (B + 1,) or
+            (attn_sink is not None and attn_sink.shape != (H,)) or (lse is not None and lse.shape != (T, H))):
         raise ValueError("q [T, H, 192], k_nope [S, H, 128], k_rope [S, 64], v [S, H, 128], out [T, H, 128], cu_q and "
                          "cu_kv [B + 1], attn_sink [H], lse [T, H] do not fit each other")
-    st = lib.smla_expanded_prefill(qp, qt, qh, kp, kt, kh, rp, rt, vp, vt, vh, _ptr(cu_q, torch.int32, "cu_q", 1),
-                                   _ptr(cu_kv, torch.int32, "cu_kv", 1), B, T, S, H, float(softmax_scale),
-                                   _ptr(attn_sink, torch.float32, "attn_sink", 1),
-                                   _ptr(out, torch.bfloat16, "out", 3), _ptr(lse, torch.float32, "lse", 2),
-                                   _ptr(workspace, torch.uint8, "workspace", 1),
-                                   0 if workspace is None else int(workspace.numel()), _stream(stream))
-    _check(lib, st)
+    st = lib.smla_expanded_prefill(qp, qs[0], qs[1], kp, ks[0], ks[1], rp, rs[0], vp, vs[0], vs[1],
+                                   _flat(cu_q, "cu_q", i32, dev, 1), _flat(cu_kv, "cu_kv", i32, dev, 1), B, T, S, H,
+                                   softmax_scale, _flat(attn_sink, "attn_sink", f32, dev, 1),
+                                   _flat(out, "out", torch.bfloat16, dev, 3), _flat(lse, "lse", f32, dev, 2),
+                                   _flat(workspace, "workspace", torch.uint8, dev, 1),
+                                   0 if workspace is None else workspace.numel(), _on(stream, dev))
+    if st:
+        _check(lib, st)
     return out
 
 
@@ -204,19 +238,21 @@ def dense_decode(q: torch.Tensor, latent: torch.Tensor, scales: Optional[torch.T
     bytes) or bf16 [phys_rows, 576] with scales f32 [phys_rows, nscale] or
     None; workspace a uint8 CUDA tensor of at least
     dense_decode_workspace_size() bytes (None when that is 0)."""
-    lib = _lib.load()
-    qd, qp = _lib._q_arg(q)
-    _here(q, latent, scales, out, workspace, attn_sink, seqs.cu_q, seqs.kv_len, seqs.page_table)
-    T, H = int(q.shape[0]), int(q.shape[1])
-    if (T != seqs.T or tuple(q.shape) != (T, H, 576) or latent.shape[1] != 576 or tuple(out.shape[:2]) != (T, H) or
-            (attn_sink is not None and tuple(attn_sink.shape) != (H,))):
+    lib, dev = _lib._lib or _lib.load(), _device()
+    bf16 = q.dtype is torch.bfloat16
+    qp = _flat(q, "q", torch.bfloat16 if bf16 else torch.uint8, dev, 3)
+    pp, pd, phys_rows, width = _pool(latent, dev)
+    T, H, D = q.shape
+    if (T != seqs.T or D != 576 or width != 576 or out.shape[:2] != (T, H) or
+            (attn_sink is not None and attn_sink.shape != (H,))):
         raise ValueError(f"q must be [T={seqs.T}, H, 576], latent [phys_rows, 576], out [T, H, 512], attn_sink [H]")
-    _check_scales(scales, latent, scale_block_size)
-    pp, pd = _pool(latent)
-    st = lib.smla_dense_decode(qp, qd, pp, pd, int(latent.shape[0]), _ptr(scales, torch.float32, "scales", 2),
-                               int(scale_block_size), seqs.as_c(), int(max_kv_len), H, int(out.shape[2]),
-                               float(softmax_scale), _ptr(attn_sink, torch.float32, "attn_sink", 1),
-                               _ptr(out, torch.bfloat16, "out", 3), _ptr(workspace, torch.uint8, "workspace", 1),
-                               0 if workspace is None else int(workspace.numel()), _stream(stream))
-    _check(lib, st)
+    sp = _scales(scales, phys_rows, D, scale_block_size, dev)
+    st = lib.smla_dense_decode(qp, SMLA_BF16 if bf16 else SMLA_E4M3, pp, pd, phys_rows, sp, scale_block_size,
+                               _seqs(seqs, dev), max_kv_len, H, out.shape[2], softmax_scale,
+                               _flat(attn_sink, "attn_sink", torch.float32, dev, 1),
+                               _flat(out, "out", torch.bfloat16, dev, 3),
+                               _flat(workspace, "workspace", torch.uint8, dev, 1),
+                               0 if workspace is None else workspace.numel(), _on(stream, dev))
+    if st:
+        _check(lib, st)
     return out

@@ -110,6 +110,27 @@ int device_sm_count() {
   return g_sm_count[dev];
 }
 
+smla_status_t prepare_kernel(const void* fn, size_t smem, int regs, std::atomic<unsigned long long>& done,
+                             const char* what) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail_cuda(e, "cudaGetDevice");
+  if (dev < 0 || dev >= kMaxDevices) return fail(SMLA_ERR_UNSUPPORTED, "device ordinal %d >= %d", dev, kMaxDevices);
+  if (done.load(std::memory_order_acquire) >> dev & 1) return SMLA_OK;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return fail_cuda(e, what);
+  if (regs > 0) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, fn);
+    if (e != cudaSuccess) return fail_cuda(e, what);
+    if (fa.numRegs != regs)
+      return fail(SMLA_ERR_UNSUPPORTED, "%s: built with %d registers a thread, its register split needs %d", what,
+                  fa.numRegs, regs);
+  }
+  done.fetch_or(1ull << dev, std::memory_order_release);
+  return SMLA_OK;
+}
+
 // One warp: lane 0 initialises an mbarrier expecting one arrival that never
 // comes and waits on its first phase with the given limit (the stage
 // kernels' bounded wait); the wait gives up, records kErrTimeout and the

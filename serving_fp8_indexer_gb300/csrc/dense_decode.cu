@@ -933,11 +933,12 @@ static smla_status_t launch(const DenseDecodeArgs& a, Params p, int grid, cudaSt
   if (!enc) return fail(SMLA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the dense-decode tensor maps");
   constexpr size_t smem = sizeof(Smem<NR, QP>);
   static_assert(smem <= 232448, "shared memory exceeds a CTA's 227 KB");
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<NR, QP, ROWSCALE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return fail_cuda(e, "dense decode smem attribute");
+  static std::atomic<unsigned long long> ready{0};
+  const smla_status_t st = prepare_kernel(reinterpret_cast<const void*>(decode_kernel<NR, QP, ROWSCALE>), smem, 0, ready,
+                                          "dense decode kernel");
+  if (st != SMLA_OK) return st;
   decode_kernel<NR, QP, ROWSCALE><<<grid, kThreads, smem, stream>>>(tq, tqr, tk, tr, p);
-  e = cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "dense decode launch");
   if (grid > 1) {
     join_kernel<NR><<<dim3(grid - 1, NR), 128 * kJoinGroups, 0, stream>>>(p);

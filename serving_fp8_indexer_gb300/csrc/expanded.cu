@@ -624,16 +624,10 @@ smla_status_t launch_expanded(const ExpandedArgs& a, unsigned* err, cudaStream_t
   const size_t smem = sizeof(Smem);
   static_assert(sizeof(Smem) <= 232448, "shared memory exceeds a CTA's 227 KB");
   static_assert(offsetof(Smem, k) % 1024 == 0 && offsetof(Smem, v) % 1024 == 0, "swizzled tiles need 1024-byte alignment");
-  cudaError_t e = cudaFuncSetAttribute(expanded_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return fail_cuda(e, "expanded smem attribute");
-  // the register split draws on the launch allocation
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, expanded_kernel);
-  if (e != cudaSuccess) return fail_cuda(e, "expanded attributes");
-  if (fa.numRegs != kLaunchRegs)
-    return fail(SMLA_ERR_UNSUPPORTED, "expanded kernel built with %d registers a thread, the register split needs %d",
-                fa.numRegs, kLaunchRegs);
+  static std::atomic<unsigned long long> ready{0};
+  const smla_status_t st = prepare_kernel(reinterpret_cast<const void*>(expanded_kernel), smem, kLaunchRegs, ready,
+                                          "expanded kernel");
+  if (st != SMLA_OK) return st;
   p.slots = static_cast<int>(expanded_slots(a.T, a.B));
   // heads whose keys and values (512 bytes a row) take at most kGroupBytes,
   // under half of L2
@@ -644,7 +638,7 @@ smla_status_t launch_expanded(const ExpandedArgs& a, unsigned* err, cudaStream_t
     return fail(SMLA_ERR_UNSUPPORTED, "expanded prefill: too many tiles (T=%d, B=%d, H=%d)", a.T, a.B, a.H);
   const dim3 grid(static_cast<unsigned>(ctas), 1, static_cast<unsigned>(a.nsplit));
   expanded_kernel<<<grid, kThreads, smem, stream>>>(tq, tk, tr, tv, p);
-  e = cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "expanded launch");
   if (a.nsplit > 1) {
     const int64_t rows = static_cast<int64_t>(a.T) * a.H;

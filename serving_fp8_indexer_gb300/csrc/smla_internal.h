@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/smla.h"
@@ -37,6 +38,13 @@ bool encode_tma_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64
 
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
+
+// What a kernel needs before its launches on a device, done on the first one:
+// its dynamic shared memory granted, and its register count checked where its
+// register split (setmaxnreg) draws on it (0: no split).  `done`: one bit per
+// device, the caller's, per kernel.
+smla_status_t prepare_kernel(const void* fn, size_t smem, int regs, std::atomic<unsigned long long>& done,
+                             const char* what);
 
 smla_status_t launch_indexer(const uint8_t* q, const float* q_scale, const uint8_t* k_pool, const float* k_scale,
                              int64_t phys_rows, const smla_seqs_t& seqs, int h_idx, float* scores,

@@ -99,22 +99,33 @@ def test_append_and_gather_refusals(lib):
 
 def test_binding_refuses_host_tensors_and_wrong_layouts():
     x = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    bf = (torch.bfloat16,)
     with pytest.raises(TypeError):
-        _latent._rows(x.half(), "x", (torch.bfloat16,), 3)
+        _latent._rows(x.half(), "x", bf, -1, 3)
+    with pytest.raises(TypeError):
+        _latent._rows([1.0], "x", bf, -1, 3)
+    with pytest.raises(ValueError, match="device"):
+        _latent._rows(x, "x", bf, 0, 3)  # on the host
     with pytest.raises(ValueError):
-        _latent._rows(x, "x", (torch.bfloat16,), 2)
+        _latent._rows(x, "x", bf, -1, 2)
+    with pytest.raises(ValueError, match="dense"):
+        _latent._rows(x.transpose(1, 2), "x", bf, -1, 3)
+    with pytest.raises(ValueError, match="device"):
+        _latent._flat(x, "x", torch.bfloat16, 0, 3)
+    with pytest.raises(TypeError):
+        _latent._flat(x, "x", torch.float32, -1, 3)
+    # a dimension of one element has no stride of its own (host tensors count
+    # as device -1 in these helpers)
+    assert _latent._rows(x[:1, :1], "x", bf, -1, 3)[2] == (64, 64, 1)
+    assert _latent._rows(x[..., :8], "x", bf, -1, 3)[2] == (128, 64, 1)
     with pytest.raises(ValueError):
-        _latent._rows(x.transpose(1, 2), "x", (torch.bfloat16,), 3)
-    # a dimension of one element has no stride of its own
-    assert _latent._rows(x[:1, :1], "x", (torch.bfloat16,), 3)[1] == [64, 64]
-    pool = torch.zeros((64, 64), dtype=torch.uint8)
+        _latent._scales(torch.ones((64, 1)), 64, 64, 0, -1)
     with pytest.raises(ValueError):
-        _latent._check_scales(torch.ones((64, 1)), pool, 0)
+        _latent._scales(torch.ones((64, 1)), 64, 64, 32, -1)
     with pytest.raises(ValueError):
-        _latent._check_scales(torch.ones((64, 1)), pool, 32)
-    with pytest.raises(ValueError):
-        _latent._check_scales(None, pool, 64)
-    _latent._check_scales(torch.ones((64, 2)), pool, 32)
+        _latent._scales(None, 64, 64, 64, -1)
+    assert _latent._scales(torch.ones((64, 2)), 64, 64, 32, -1) is not None
+    assert _latent._scales(None, 64, 64, 0, -1) is None
 
 
 def test_expanded_refusals(lib):
