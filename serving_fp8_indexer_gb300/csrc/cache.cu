@@ -13,15 +13,15 @@
 //
 // Both are bound by HBM, and by latency for a decode step's few rows.
 #include <algorithm>
+#include <type_traits>
 
 #include "rope.cuh"
 
 namespace smla {
 namespace ca {
 
-constexpr int kMaxD = 1024;
-constexpr int kSlots = kMaxD / 8 / 32;  // 8-element chunks a lane may hold
 constexpr int kWarps = 4;
+
 constexpr float kE4m3Max = 448.f;
 
 struct AppendParams {
@@ -56,10 +56,15 @@ __device__ __forceinline__ float scale_of(float amax) {
   return amax > 0.f ? fmaxf(amax / kE4m3Max, 1.17549435e-38f) : 1.f;
 }
 
-template <int MODE>
+// kSlots: 8-element chunks a lane holds.
+template <int MODE, int kSlots>
 __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendParams p) {
+  // the rotary angles' cos and sin, for each warp its token's
+  extern __shared__ float2 s_cs[];
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int pairs = (p.c1 - p.c0) * 4;
+  float2* cs = s_cs + (threadIdx.x >> 5) * pairs;
   if (t >= p.T) return;
   const __nv_bfloat16* x = p.x + t * p.x_stride;
   // the row's loads go out before the chain of index loads
@@ -73,6 +78,8 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendParams 
   if (b < 0) return;  // behind the last sequence: nothing is written
   const int pos = token_pos(p.seqs, b, t);
   const int64_t row = key_phys_row(p.seqs, b, pos, p.phys_rows, p.err);
+  for (int i = lane; i < pairs; i += 32) rope_cos_sin(p.inv_freq[i], pos, p.amplitude, cs[i].x, cs[i].y);
+  __syncwarp();
   float v[kSlots][8];
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) unpack_bf16x8(raw[i], v[i]);
@@ -108,11 +115,10 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendParams 
     if (!p.half) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float cs, sn;
-        rope_cos_sin(p.inv_freq[(c - p.c0) * 4 + k], pos, p.amplitude, cs, sn);
+        const float2 r = cs[(c - p.c0) * 4 + k];
         const float a = v[i][2 * k], q = v[i][2 * k + 1];
-        v[i][2 * k] = a * cs - q * sn;
-        v[i][2 * k + 1] = q * cs + a * sn;
+        v[i][2 * k] = a * r.x - q * r.y;
+        v[i][2 * k + 1] = q * r.x + a * r.y;
       }
     } else {
       // the other half's chunk is another lane's, perhaps in another slot:
@@ -125,9 +131,8 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendParams 
       const int f0 = ((first ? c : pc) - p.c0) * 8;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        float cs, sn;
-        rope_cos_sin(p.inv_freq[f0 + k], pos, p.amplitude, cs, sn);
-        v[i][k] = first ? v[i][k] * cs - o[k] * sn : v[i][k] * cs + o[k] * sn;
+        const float2 r = cs[f0 + k];
+        v[i][k] = first ? v[i][k] * r.x - o[k] * r.y : v[i][k] * r.x + o[k] * r.y;
       }
     }
   }
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendParams 
     }
     return;
   }
-  float scale = 1.f;
+  float scale = 1.f, inv = 1.f;
   if (MODE == kRow) {
     float amax = 0.f;
 #pragma unroll
@@ -158,6 +163,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendParams 
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     scale = scale_of(amax);
+    inv = 1.f / scale;
     if (lane == 0) p.scales[row] = scale;
   }
   uint8_t* dst = static_cast<uint8_t*>(p.pool) + row * (p.chunks * 8);
@@ -172,12 +178,13 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendParams 
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       scale = scale_of(amax);
+      inv = 1.f / scale;
       if (c < p.chunks && (c & 3) == 0) p.scales[row * (p.chunks >> 2) + (c >> 2)] = scale;
     }
     if (c < p.chunks) {
       float q[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[k] = MODE == kUnit ? v[i][k] : v[i][k] / scale;
+      for (int k = 0; k < 8; ++k) q[k] = MODE == kUnit ? v[i][k] : v[i][k] * inv;  // 2^-24 from the quotient, before a 2^-4 rounding
       *reinterpret_cast<uint2*>(dst + c * 8) = pack_e4m3x8(q);
     }
   }
@@ -201,42 +208,64 @@ struct GatherParams {
 
 constexpr int kMaxGatherRows = 32;
 
-// A CTA takes up to 32 consecutive tokens: a warp finds their physical rows,
-// then the rows' chunks are spread flat over the threads, so that a row width
-// that is no multiple of 32 chunks leaves no lane idle.
+// A CTA takes up to 32 consecutive tokens: a warp finds the first one's
+// sequence, then each lane steps to its own token's (few steps, mostly none)
+// and reads its page, one chain of reads for all rows.  Then the rows' chunks
+// are spread flat over the threads, so that a row width that is no multiple of
+// 32 chunks leaves no lane idle; a thread's loads go out before its stores.
 template <int MODE>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherParams p) {
   __shared__ int64_t s_row[kMaxGatherRows];
   const int t0 = blockIdx.x * p.rows_per_cta;
   const int nr = min(p.rows_per_cta, p.T - t0);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < nr; r += kGatherThreads / 32) {
-    const int t = t0 + r;
-    const int b = warp_seq_of(p.seqs.cu_q, p.seqs.B, t, lane);
-    if (lane == 0) s_row[r] = b < 0 ? -1 : key_phys_row(p.seqs, b, token_pos(p.seqs, b, t), p.phys_rows, p.err);
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, t = t0 + lane;
+    int b = warp_seq_of(p.seqs.cu_q, p.seqs.B, t0, lane);
+    if (lane < nr) {
+      if (b < 0) b = p.seqs.cu_q[0] > t0 ? 0 : p.seqs.B;  // before the first sequence, or behind the last
+      while (b < p.seqs.B && p.seqs.cu_q[b + 1] <= t) ++b;
+      s_row[lane] = b >= p.seqs.B || p.seqs.cu_q[b] > t
+                        ? -1
+                        : key_phys_row(p.seqs, b, token_pos(p.seqs, b, t), p.phys_rows, p.err);
+    }
   }
   __syncthreads();
   const int n = nr * p.chunks;
-#pragma unroll 3
-  for (int i = threadIdx.x; i < n; i += kGatherThreads) {
-    const int r = __umulhi(i, p.magic);
-    const int c = i - r * p.chunks;
-    const int64_t row = s_row[r];
-    if (row < 0) continue;
-    __nv_bfloat16* dst = p.rows + (t0 + r) * p.rows_stride + c * 8;
-    if (MODE == kBf16) {
-      *reinterpret_cast<uint4*>(dst) =
-          *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.pool) + row * (p.chunks * 8) + c * 8);
-    } else {
-      float v[8];
-      unpack_e4m3x8(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.pool) + row * (p.chunks * 8) + c * 8),
-                    v);
-      if (MODE != kUnit) {
-        const float s = MODE == kRow ? p.scales[row] : p.scales[row * (p.chunks >> 2) + (c >> 2)];
+  constexpr int kBatch = 5;  // loads of a thread in flight (a full CTA of 576-wide rows has nine)
+  for (int i0 = threadIdx.x; i0 < n; i0 += kBatch * kGatherThreads) {
+    uint4 raw[kBatch];
+    float sc[kBatch];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= s;
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kGatherThreads, r = __umulhi(i, p.magic), c = i - r * p.chunks;
+      const int64_t row = i < n ? s_row[r] : -1;
+      raw[k] = make_uint4(0, 0, 0, 0);
+      sc[k] = 1.f;
+      if (row < 0) continue;
+      const int64_t at = row * (p.chunks * 8) + c * 8;
+      if (MODE == kBf16) {
+        raw[k] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.pool) + at));
+      } else {
+        const uint2 u = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.pool) + at));
+        raw[k].x = u.x;
+        raw[k].y = u.y;
+        if (MODE != kUnit) sc[k] = MODE == kRow ? p.scales[row] : p.scales[row * (p.chunks >> 2) + (c >> 2)];
       }
-      *reinterpret_cast<uint4*>(dst) = pack_bf16x8(v);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kGatherThreads, r = __umulhi(i, p.magic), c = i - r * p.chunks;
+      if (i >= n || s_row[r] < 0) continue;
+      uint4 o = raw[k];
+      if (MODE != kBf16) {
+        float v[8];
+        unpack_e4m3x8(make_uint2(raw[k].x, raw[k].y), v);
+        if (MODE != kUnit)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] *= sc[k];
+        o = pack_bf16x8(v);
+      }
+      *reinterpret_cast<uint4*>(p.rows + (t0 + r) * p.rows_stride + c * 8) = o;
     }
   }
 }
@@ -271,11 +300,22 @@ smla_status_t launch_cache_append(const CacheArgs& a, const smla_seqs_t& seqs, u
   p.rows_stride = a.rows_stride;
   p.err = err;
   const unsigned grid = (static_cast<unsigned>(seqs.T) + kWarps - 1) / kWarps;
-  switch (mode_of(a)) {
-    case kBf16: append_kernel<kBf16><<<grid, 32 * kWarps, 0, stream>>>(p); break;
-    case kUnit: append_kernel<kUnit><<<grid, 32 * kWarps, 0, stream>>>(p); break;
-    case kRow: append_kernel<kRow><<<grid, 32 * kWarps, 0, stream>>>(p); break;
-    case kBlock: append_kernel<kBlock><<<grid, 32 * kWarps, 0, stream>>>(p); break;
+  const size_t smem = sizeof(float2) * kWarps * (p.c1 - p.c0) * 4;  // at most 16 KB
+  const Mode mode = mode_of(a);
+  const auto go = [&](auto slots) {
+    constexpr int N = decltype(slots)::value;
+    switch (mode) {
+      case kBf16: append_kernel<kBf16, N><<<grid, 32 * kWarps, smem, stream>>>(p); break;
+      case kUnit: append_kernel<kUnit, N><<<grid, 32 * kWarps, smem, stream>>>(p); break;
+      case kRow: append_kernel<kRow, N><<<grid, 32 * kWarps, smem, stream>>>(p); break;
+      case kBlock: append_kernel<kBlock, N><<<grid, 32 * kWarps, smem, stream>>>(p); break;
+    }
+  };
+  switch ((p.chunks + 31) / 32) {
+    case 1: go(std::integral_constant<int, 1>{}); break;
+    case 2: go(std::integral_constant<int, 2>{}); break;
+    case 3: go(std::integral_constant<int, 3>{}); break;
+    default: go(std::integral_constant<int, 4>{}); break;
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "cache append launch");

@@ -325,6 +325,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
 
+  // requests a segment's q rows (one thread)
+  const auto load_q = [&](const Seg& g) {
+    const int row = g.t0 * p.H + g.h0;
+    const uint32_t bar = smem_u32(&s.bar_qraw), dst = smem_u32(s.q);
+    mbar_arrive_expect_tx(bar, NR * kD * QP);
+    if (QP == 2) {
+#pragma unroll
+      for (int c = 0; c < 9; ++c) tma_load_2d(dst + c * (NR * 128), &tq, c * 128, row, bar);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tma_load_2d(dst + c * kQChunk, &tq, c * 128, row, bar);
+      tma_load_2d(dst + 4 * kQChunk, &tqr, 512, row, bar);
+    }
+  };
   if (start.b < 0) {
     // nothing left of the line for this CTA
   } else if (warp < 8) {
@@ -702,6 +716,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int i = 0;
     bool ok = true, more = next_seg(p, cur, g);
     int pid = read_page(g, 0), pid_n = 0;
+    // the first segment's q ahead of the keys (behind the first two blocks of
+    // every CTA it took 3 us); the QK warp requests the others
+    if (leader) load_q(g);
+    __syncwarp();
     while (ok && more) {
       more = next_seg(p, cur, gn);
       for (int j = 0; ok && j < g.nb; ++j) {
@@ -768,19 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (ok && next_seg(p, cur, g)) {
       // the segment's q rows: every QK before has completed (waited for below)
-      if (leader) {
-        const int row = g.t0 * p.H + g.h0;
-        const uint32_t bar = smem_u32(&s.bar_qraw), dst = smem_u32(s.q);
-        mbar_arrive_expect_tx(bar, NR * kD * QP);
-        if (QP == 2) {
-#pragma unroll
-          for (int c = 0; c < 9; ++c) tma_load_2d(dst + c * (NR * 128), &tq, c * 128, row, bar);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tma_load_2d(dst + c * kQChunk, &tq, c * 128, row, bar);
-          tma_load_2d(dst + 4 * kQChunk, &tqr, 512, row, bar);
-        }
-      }
+      if (leader && nq > 0) load_q(g);
       __syncwarp();
       ++nq;
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_q), (nq - 1) & 1, p.err));
@@ -862,62 +868,73 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kQkWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the parts of one cut item, a row (token, head) per CTA:
+// Joins the parts of one cut item, NR / 16 rows (token, head) per CTA:
 //   out = sum_c 2^(L_c - M) O_c / (sum_c 2^(L_c - M) + 2^(sink - M)).
-// Four groups of 128 threads (a float4 of the row each) take every fourth
-// part, so that a long item's parts are read side by side.
-constexpr int kJoinGroups = 4;
+// Groups of 128 threads hold a float4 of a row each: with few parts a group
+// takes a row; with more than kManyParts all groups share each row's parts, so
+// that a long item's parts are read side by side.
+constexpr int kJoinGroups = 4, kManyParts = 12;
+__host__ __device__ constexpr int join_rows(int nr) { return nr / 16; }
 template <int NR>
 __global__ void __launch_bounds__(128 * kJoinGroups) join_kernel(const Params p) {
   const Cut cut = p.cuts[blockIdx.x + 1];
-  const int row = blockIdx.y;
-  if (cut.first_cta < 0 || row >= cut.rows) return;
-  __shared__ float4 s_acc[kJoinGroups - 1][128];
-  __shared__ float s_top[kJoinGroups * 4], s_l[kJoinGroups - 1];
-  const int grp = threadIdx.x / 128, col = threadIdx.x % 128, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int head = p.groups > 1 ? cut.h0 + row : row % p.H;
-  const float sk = p.sink ? p.sink[head] * kLog2e : -INFINITY;
-  const auto slot = [&](int c) { return static_cast<int64_t>(2 * c + (c == cut.first_cta ? 1 : 0)) * NR + row; };
-  float top = sk;
-  for (int c = cut.first_cta + threadIdx.x; c <= cut.last_cta; c += 128 * kJoinGroups) top = fmaxf(top, p.part_lse[slot(c)]);
+  constexpr int kRows = join_rows(NR);
+  const int row0 = blockIdx.y * kRows;
+  if (cut.first_cta < 0 || row0 >= cut.rows) return;
+  __shared__ float4 s_acc[kJoinGroups][128];
+  __shared__ float s_l[kJoinGroups];
+  const int grp = threadIdx.x / 128, col = threadIdx.x % 128, lane = threadIdx.x & 31;
+  const bool many = kRows < kJoinGroups || cut.last_cta - cut.first_cta >= kManyParts;
+  const auto slot = [&](int c, int row) { return static_cast<int64_t>(2 * c + (c == cut.first_cta ? 1 : 0)) * NR + row; };
+  const int nrow = min(kRows, cut.rows - row0);
+  for (int k = 0; k < (many ? nrow : 1); ++k) {
+    const int row = row0 + (many ? k : grp);
+    const bool live = row < cut.rows;  // (a group without a row still meets the barriers)
+    const int head = p.groups > 1 ? cut.h0 + row : row % p.H;
+    const float sk = p.sink && live ? p.sink[head] * kLog2e : -INFINITY;
+    float top = sk;
+    if (live)
+      for (int c = cut.first_cta + lane; c <= cut.last_cta; c += 32) top = fmaxf(top, p.part_lse[slot(c, row)]);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) s_top[warp] = top;
-  __syncthreads();
-  for (int w = 0; w < kJoinGroups * 4; ++w) top = fmaxf(top, s_top[w]);
-  const float m = top == -INFINITY ? 0.f : top;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = grp == 0 ? exp2f(sk - m) : 0.f;
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float m = top == -INFINITY ? 0.f : top;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = !many || grp == 0 ? exp2f(sk - m) : 0.f;
+    const int step = many ? kJoinGroups : 1;
+    if (live)
 #pragma unroll 4
-  for (int c = cut.first_cta + grp; c <= cut.last_cta; c += kJoinGroups) {
-    const float w = exp2f(p.part_lse[slot(c)] - m);  // 0 for a part without keys, whose O is 0
-    const float4 o = __ldcs(reinterpret_cast<const float4*>(p.part_o + slot(c) * kDV) + col);
-    l += w;
-    acc.x = fmaf(w, o.x, acc.x);
-    acc.y = fmaf(w, o.y, acc.y);
-    acc.z = fmaf(w, o.z, acc.z);
-    acc.w = fmaf(w, o.w, acc.w);
-  }
-  if (grp > 0) {
-    s_acc[grp - 1][col] = acc;
-    if (col == 0) s_l[grp - 1] = l;
-  }
-  __syncthreads();
-  if (grp > 0) return;
+      for (int c = cut.first_cta + (many ? grp : 0); c <= cut.last_cta; c += step) {
+        const float w = exp2f(p.part_lse[slot(c, row)] - m);  // 0 for a part without keys, whose O is 0
+        const float4 o = __ldcs(reinterpret_cast<const float4*>(p.part_o + slot(c, row) * kDV) + col);
+        l += w;
+        acc.x = fmaf(w, o.x, acc.x);
+        acc.y = fmaf(w, o.y, acc.y);
+        acc.z = fmaf(w, o.z, acc.z);
+        acc.w = fmaf(w, o.w, acc.w);
+      }
+    if (many) {
+      __syncthreads();  // the sums of the row before have been read
+      s_acc[grp][col] = acc;
+      if (col == 0) s_l[grp] = l;
+      __syncthreads();
+      if (grp > 0) continue;
 #pragma unroll
-  for (int k = 0; k < kJoinGroups - 1; ++k) {
-    const float4 o = s_acc[k][col];
-    l += s_l[k];
-    acc.x += o.x;
-    acc.y += o.y;
-    acc.z += o.z;
-    acc.w += o.w;
+      for (int g = 1; g < kJoinGroups; ++g) {
+        const float4 o = s_acc[g][col];
+        l += s_l[g];
+        acc.x += o.x;
+        acc.y += o.y;
+        acc.z += o.z;
+        acc.w += o.w;
+      }
+    }
+    if (!live) continue;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(cut.row0 + row) * kDV)[col] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-  const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(cut.row0 + row) * kDV)[col] =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
 template <int NR, int QP, bool ROWSCALE>
@@ -941,7 +958,7 @@ static smla_status_t launch(const DenseDecodeArgs& a, Params p, int grid, cudaSt
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "dense decode launch");
   if (grid > 1) {
-    join_kernel<NR><<<dim3(grid - 1, NR), 128 * kJoinGroups, 0, stream>>>(p);
+    join_kernel<NR><<<dim3(grid - 1, NR / join_rows(NR)), 128 * kJoinGroups, 0, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return fail_cuda(e, "dense decode join launch");
   }

@@ -8,9 +8,12 @@
 // Bound by HBM: every element is read and written once.  A CTA takes one
 // token and a group of its heads, so the token's dim/2 angles are computed
 // once per CTA into shared memory and serve all of the group's heads.  The
+// copied columns do not wait for them: they are a loop of their own, before
+// the barrier, with the rotated columns' first loads already under way.  The
 // group is sized to give the CTA about kChunksPerCta 8-element chunks (nine
 // 16-byte loads a thread), and fewer when the batch is too small to fill the
-// GPU that way.
+// GPU that way.  4096 tokens x 128 heads x 576: 138 us to e4m3, 185 us to bf16,
+// 6.5 TB/s (0.97 of the measured copy rate).
 #include <algorithm>
 #include <cmath>
 
@@ -28,28 +31,44 @@ struct Params {
   void* out;
   int64_t x_ts, x_hs, o_ts, o_hs;  // token and head strides, elements
   SeqsDev seqs;
-  int H, chunks;       // heads; 8-element chunks per head
+  int H;
   int heads_per_cta;
-  uint32_t magic;      // ceil(2^32 / chunks): i / chunks = umulhi(i, magic) for i < 2^16
-  int c0, c1;          // the rotated chunks [c0, c1)
-  int half;            // layout
-  int in_place;        // the copied columns are there already
+  int c0, rot, rest;        // chunks (8 elements) of a head: first rotated one, rotated, copied
+  uint32_t m_rot, m_rest;   // divisors of the two loops (see div_by)
+  int half;                 // layout
   const double* inv_freq;
   float amplitude;
   unsigned* err;
 };
 
+// i / d = div_by(i, ceil(2^31 / d)) for i * d < 2^31 / 2 (here i < 2^16, d <= 128)
+__device__ __forceinline__ int div_by(int i, uint32_t m) { return __umulhi(2 * i, m); }
+
+// Eight elements as loaded, and as floats.
 template <typename X>
-__device__ __forceinline__ void load8(const X* p, float (&v)[8]);
+struct Raw;
 template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-  unpack_bf16x8(*reinterpret_cast<const uint4*>(p), v);
-}
+struct Raw<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load_const(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&v)[8]) const { unpack_bf16x8(u, v); }
+};
 template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void load_const(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
 template <typename Y>
 __device__ __forceinline__ void store8(Y* p, const float (&v)[8]);
 template <>
@@ -69,66 +88,71 @@ __device__ __forceinline__ void store8<uint8_t>(uint8_t* p, const float (&v)[8])
 template <typename X, typename Y>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
   __shared__ float2 cs[kMaxDim / 2];
-  __shared__ int s_pos;
   const int t = blockIdx.x;
-  if (threadIdx.x < 32) {
-    const int b = warp_seq_of(p.seqs.cu_q, p.seqs.B, t, threadIdx.x);
-    if (threadIdx.x == 0) {
-      int pos = b < 0 ? -1 : token_pos(p.seqs, b, t);
-      if (b >= 0 && pos < 0) atomicOr(p.err, kErrShape);
-      s_pos = pos;
-    }
-  }
-  __syncthreads();
-  const int pos = s_pos;
-  if (pos < 0) return;  // behind the last sequence: left as it is
-  for (int i = threadIdx.x; i < (p.c1 - p.c0) * 4; i += kThreads)
-    rope_cos_sin(p.inv_freq[i], pos, p.amplitude, cs[i].x, cs[i].y);
-  __syncthreads();
-  const int h0 = blockIdx.y * p.heads_per_cta;
+  const int h0 = blockIdx.y * p.heads_per_cta, heads = min(p.heads_per_cta, p.H - h0);
   const X* x = static_cast<const X*>(p.x) + t * p.x_ts + h0 * p.x_hs;
   Y* out = static_cast<Y*>(p.out) + t * p.o_ts + h0 * p.o_hs;
-  const int n = min(p.heads_per_cta, p.H - h0) * p.chunks;
-  const int hc = (p.c1 - p.c0) >> 1;  // chunks in half of the rotated part
-#pragma unroll 3
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int h = __umulhi(i, p.magic);
-    const int c = i - h * p.chunks;
-    const X* xr = x + h * p.x_hs + c * 8;
-    Y* yr = out + h * p.o_hs + c * 8;
-    if (c < p.c0 || c >= p.c1) {
-      if (!p.in_place) {
-        float v[8];
-        load8(xr, v);
-        store8(yr, v);
-      }
-    } else if (!p.half) {
-      float v[8];
-      load8(xr, v);
+  // The rotated part: an item is a chunk, or (half layout) a pair of chunks.
+  // One thread reads an item before it writes it, so the output may be the input.
+  const int per = p.half ? p.rot >> 1 : p.rot, n_rot = heads * per;
+  Raw<X> ra, rb;
+  const auto load_rot = [&](int i) {
+    const int h = div_by(i, p.m_rot);
+    const X* xr = x + h * p.x_hs + (p.c0 + i - h * per) * 8;
+    ra.load(xr);
+    if (p.half) rb.load(xr + per * 8);
+  };
+  if (threadIdx.x < n_rot) load_rot(threadIdx.x);
+  const int b = warp_seq_of(p.seqs.cu_q, p.seqs.B, t, threadIdx.x & 31);
+  if (b < 0) return;  // behind the last sequence: left as it is
+  const int pos = token_pos(p.seqs, b, t);
+  if (pos < 0) {
+    if (threadIdx.x == 0) atomicOr(p.err, kErrShape);
+    return;
+  }
+  for (int i = threadIdx.x; i < p.rot * 4; i += kThreads)
+    rope_cos_sin(p.inv_freq[i], pos, p.amplitude, cs[i].x, cs[i].y);
+  // copied columns (rest is 0 in place: they are there)
+  const int n_rest = heads * p.rest;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n_rest; i += kThreads) {
+    const int h = div_by(i, p.m_rest);
+    int c = i - h * p.rest;
+    if (c >= p.c0) c += p.rot;
+    Raw<X> r;
+    float v[8];
+    r.load_const(x + h * p.x_hs + c * 8);  // (copied columns are never written in place)
+    r.get(v);
+    store8(out + h * p.o_hs + c * 8, v);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n_rot; i += kThreads) {
+    if (i != threadIdx.x) load_rot(i);
+    const int h = div_by(i, p.m_rot), c = i - h * per;
+    Y* yr = out + h * p.o_hs + (p.c0 + c) * 8;
+    float a[8];
+    ra.get(a);
+    if (!p.half) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 r = cs[(c - p.c0) * 4 + k];
-        const float a = v[2 * k], b = v[2 * k + 1];
-        v[2 * k] = a * r.x - b * r.y;
-        v[2 * k + 1] = b * r.x + a * r.y;
+      for (int e = 0; e < 4; ++e) {
+        const float2 r = cs[c * 4 + e];
+        const float u = a[2 * e], w = a[2 * e + 1];
+        a[2 * e] = u * r.x - w * r.y;
+        a[2 * e + 1] = w * r.x + u * r.y;
       }
-      store8(yr, v);
-    } else if (c - p.c0 < hc) {
-      // both chunks of the pair by one thread, read before they are written
-      // (the output may be the input)
-      float a[8], b[8];
-      load8(xr, a);
-      load8(xr + hc * 8, b);
+    } else {
+      float w[8];
+      rb.get(w);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float2 r = cs[(c - p.c0) * 8 + k];
-        const float u = a[k] * r.x - b[k] * r.y;
-        b[k] = b[k] * r.x + a[k] * r.y;
-        a[k] = u;
+      for (int e = 0; e < 8; ++e) {
+        const float2 r = cs[c * 8 + e];
+        const float u = a[e] * r.x - w[e] * r.y;
+        w[e] = w[e] * r.x + a[e] * r.y;
+        a[e] = u;
       }
-      store8(yr, a);
-      store8(yr + hc * 8, b);
+      store8(yr + per * 8, w);
     }
+    store8(yr, a);
   }
 }
 
@@ -145,17 +169,20 @@ smla_status_t launch_rope(const RopeArgs& a, const smla_seqs_t& seqs, unsigned* 
   p.o_hs = a.o_hs;
   p.seqs = seqs_dev(seqs);
   p.H = a.H;
-  p.chunks = a.D / 8;
-  p.magic = static_cast<uint32_t>(((uint64_t(1) << 32) + p.chunks - 1) / p.chunks);
-  p.c0 = a.rope.offset / 8;
-  p.c1 = p.c0 + a.rope.dim / 8;
+  const int chunks = a.D / 8;
+  const auto divisor = [](int d) { return static_cast<uint32_t>(((uint64_t(1) << 31) + d - 1) / std::max(d, 1)); };
+  const bool in_place = a.x == a.out;  // (then of the same type and strides)
   p.half = a.rope.layout == SMLA_ROPE_HALF;
-  p.in_place = a.x == a.out && a.x_dtype == a.out_dtype && a.x_ts == a.o_ts && a.x_hs == a.o_hs;
+  p.c0 = a.rope.offset / 8;
+  p.rot = a.rope.dim / 8;
+  p.rest = in_place ? 0 : chunks - p.rot;
+  p.m_rot = divisor(p.half ? p.rot / 2 : p.rot);
+  p.m_rest = divisor(p.rest);
   p.inv_freq = a.rope.inv_freq;
   p.amplitude = a.rope.amplitude;
   p.err = err;
   // two CTAs per SM at least, where there are heads enough to give them
-  const int full = std::max(1, kChunksPerCta / p.chunks);
+  const int full = std::max(1, kChunksPerCta / chunks);
   const int64_t want = 2 * device_sm_count();
   const int groups = static_cast<int>(std::max<int64_t>((a.H + full - 1) / full, (want + seqs.T - 1) / seqs.T));
   p.heads_per_cta = std::max(1, (a.H + groups - 1) / groups);

@@ -50,17 +50,35 @@ SMLA_DEVICE_INLINE int64_t key_phys_row(const SeqsDev& s, int b, int key, int64_
   return row;
 }
 
-// cos and sin of pos * inv_freq, times `amplitude`.  The angle is taken in
-// turns as a 64-bit fraction: step = frac(inv_freq / 2 pi) * 2^64, and the
-// integer product step * pos wraps modulo one turn exactly, so far positions
-// lose nothing to the reduction (a 32-bit product pos * inv_freq is off by
-// 2^-24 of the whole angle: 0.008 radians at position 130 000).  What is left
-// is the rounding of the reduced angle to 32 bits, at most 2^-25 half turns.
+// frac(f / 2 pi) * 2^64, the turns of one position as a 64-bit fraction, in
+// integer arithmetic: f = m 2^e with a 53-bit m, and m times 2^66 / (2 pi) is a
+// 117-bit product that is shifted into place; whole turns fall off the top.
+// (In float64 arithmetic, of which this GPU does two operations a cycle and
+// SM, the angles took most of an append's time.)
+SMLA_DEVICE_INLINE unsigned long long rope_step(double f) {
+  const unsigned long long bits = static_cast<unsigned long long>(__double_as_longlong(f));
+  const int ex = static_cast<int>(bits >> 52) & 0x7ff;
+  const unsigned long long m = (bits & 0xfffffffffffffull) | (ex ? 0x10000000000000ull : 0);
+  constexpr unsigned long long kC = 11743562013128004906ull;  // round(2^66 / (2 pi))
+  const unsigned long long hi = __umul64hi(m, kC), lo = m * kC;
+  const int s = 2 + 1075 - (ex ? ex : 1);  // shift right
+  unsigned long long r;
+  if (s >= 64)
+    r = s < 128 ? hi >> (s - 64) : 0ull;
+  else if (s > 0)
+    r = (hi << (64 - s)) | (lo >> s);
+  else
+    r = s > -64 ? lo << -s : 0ull;
+  return bits >> 63 ? 0ull - r : r;
+}
+
+// cos and sin of pos * inv_freq, times `amplitude`: the integer product step *
+// pos wraps modulo one turn exactly, so far positions lose nothing to the
+// reduction (a 32-bit product pos * inv_freq is off by 2^-24 of the whole
+// angle: 0.008 radians at position 130 000).  What is left is the rounding of
+// the reduced angle to 32 bits, at most 2^-25 half turns.
 SMLA_DEVICE_INLINE void rope_cos_sin(double inv_freq, int pos, float amplitude, float& c, float& s) {
-  double t = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-  t -= floor(t);
-  const unsigned long long step = __double2ull_rn(t * 18446744073709551616.0);
-  const unsigned long long phase = step * static_cast<unsigned long long>(static_cast<long long>(pos));
+  const unsigned long long phase = rope_step(inv_freq) * static_cast<unsigned long long>(static_cast<long long>(pos));
   const float half_turns = static_cast<float>(static_cast<int>(phase >> 32)) * (1.f / 2147483648.f);
   sincospif(half_turns, &s, &c);
   c *= amplitude;
