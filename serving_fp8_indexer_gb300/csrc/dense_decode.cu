@@ -53,6 +53,10 @@ constexpr int kTmaWarp = 8, kQkWarp = 9, kPvWarp = 10;
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTau = 8.f, kPOffset = 4.f;  // lazy rescale; the largest weight is 2^4 .. 2^8 (two-term e4m3's best range)
+// An item's first blocks cost their CTA more than the blocks themselves (its q
+// is loaded and split, its result reduced and stored): the line counts that as
+// this many blocks.
+constexpr int kItemCost = 5;
 constexpr int kOrdMin = static_cast<int>(0x80000000u);
 
 struct Cut;
@@ -71,6 +75,7 @@ struct Params {
   float* part_o;        // [2 * grid][NR][512], each normalised by its own sum
   float* part_lse;      // [2 * grid][NR], log2 units
   Cut* cuts;            // [grid]
+  int grid;
   unsigned* err;
 };
 // What CTA c's part begins with: an item cut at its first block, and whether
@@ -98,10 +103,13 @@ struct Smem {
 
 // ------------------------------------------------------------- the work line
 // Items in order: sequence after sequence, its token groups, their head
-// groups; each `nblk` blocks of 128 keys (at least one, so that tokens
-// without keys are visited and get their zeros).
+// groups; each kItemCost units without keys, then a unit for each of its
+// `nblk` blocks of 128 keys (at least one, so that tokens without keys are
+// visited and get their zeros).
 struct SeqWork {
   int q0, q_len, kv, nblk, items;
+  __device__ __forceinline__ int item_units() const { return kItemCost + nblk; }
+  __device__ __forceinline__ int units() const { return items * item_units(); }
 };
 __device__ __forceinline__ SeqWork seq_work(const Params& p, int b) {
   SeqWork w;
@@ -118,11 +126,11 @@ __device__ __forceinline__ SeqWork seq_work(const Params& p, int b) {
   return w;
 }
 
-// All blocks (below 2^31: the launcher checks the bound), by the whole warp.
+// All units (below 2^31: the launcher checks the bound), by the whole warp.
 __device__ __forceinline__ int warp_sum(int n) { return __reduce_add_sync(0xffffffffu, n); }
 
-// Sequence that holds block x of the line, and the line's position of its
-// first block; by the whole warp, lane l holding sequence b0 + l's blocks n.
+// Sequence that holds unit x of the line, and the line's position of its
+// first unit; by the whole warp, lane l holding sequence b0 + l's units n.
 // -1 when x lies behind these; `base` then moves past them.
 __device__ __forceinline__ int find_among(int x, int n, int lane, int& base) {
   int inc = n;
@@ -143,8 +151,8 @@ __device__ __forceinline__ int find_among(int x, int n, int lane, int& base) {
 
 // A CTA's walk along its part of the line.
 struct Cursor {
-  int b, item, blk;  // next: sequence, item of the sequence, block of the item
-  int left;          // blocks left
+  int b, item, at;  // next: sequence, item of the sequence, unit of the item
+  int left;         // units left
 };
 // One item's blocks within the part.
 struct Seg {
@@ -154,30 +162,33 @@ struct Seg {
   bool whole;              // all of the item's blocks
 };
 __device__ __forceinline__ bool next_seg(const Params& p, Cursor& c, Seg& s) {
-  if (c.left <= 0) return false;
-  SeqWork w = seq_work(p, c.b);
-  while (c.item >= w.items) {  // past the sequence's items
-    if (++c.b >= p.seqs.B) return false;
-    c.item = 0;
-    w = seq_work(p, c.b);
+  for (;;) {
+    if (c.left <= 0) return false;
+    SeqWork w = seq_work(p, c.b);
+    while (c.item >= w.items) {  // past the sequence's items
+      if (++c.b >= p.seqs.B) return false;
+      c.item = 0;
+      w = seq_work(p, c.b);
+    }
+    const int tg = c.item / p.groups, hg = c.item - tg * p.groups;
+    const int take = min(w.item_units() - c.at, c.left), end = c.at + take - kItemCost;  // first block not taken
+    s.b = c.b;
+    s.t0 = w.q0 + tg * p.tok_per_item;
+    s.ntok = min(p.tok_per_item, w.q_len - tg * p.tok_per_item);
+    s.h0 = hg * 64;
+    s.rows = p.groups > 1 ? 64 : s.ntok * p.H;
+    s.pos1 = w.kv - w.q_len + tg * p.tok_per_item + 1;
+    s.j0 = max(0, c.at - kItemCost);
+    s.nb = end - s.j0;
+    s.whole = s.nb == w.nblk;
+    c.left -= take;
+    c.at += take;
+    if (c.at >= w.item_units()) {
+      c.at = 0;
+      ++c.item;
+    }
+    if (s.nb > 0) return true;  // (a part that ends before the item's blocks has nothing of it)
   }
-  const int tg = c.item / p.groups, hg = c.item - tg * p.groups;
-  s.b = c.b;
-  s.t0 = w.q0 + tg * p.tok_per_item;
-  s.ntok = min(p.tok_per_item, w.q_len - tg * p.tok_per_item);
-  s.h0 = hg * 64;
-  s.rows = p.groups > 1 ? 64 : s.ntok * p.H;
-  s.pos1 = w.kv - w.q_len + tg * p.tok_per_item + 1;
-  s.j0 = c.blk;
-  s.nb = min(w.nblk - c.blk, c.left);
-  s.whole = s.nb == w.nblk;
-  c.left -= s.nb;
-  c.blk += s.nb;
-  if (c.blk >= w.nblk) {
-    c.blk = 0;
-    ++c.item;
-  }
-  return true;
 }
 __device__ __forceinline__ int seg_keys(const Seg& s) { return max(0, s.pos1 + s.ntok - 1); }  // the last token's keys
 
@@ -278,12 +289,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   Cursor start{-1, 0, 0, 0};
   {
     const int B = p.seqs.B;
-    int n0 = 0, total = 0;  // n0: the lane's blocks among the first 32 sequences
+    int n0 = 0, total = 0;  // n0: the lane's units among the first 32 sequences
     for (int b0 = 0; b0 < B; b0 += 32) {
       int n = 0;
       if (b0 + lane < B) {
         const SeqWork w = seq_work(p, b0 + lane);
-        n = w.items * w.nblk;
+        n = w.units();
       }
       if (b0 == 0) n0 = n;
       total += warp_sum(n);
@@ -299,17 +310,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n = 0;
         if (b0 + lane < B) {
           const SeqWork w = seq_work(p, b0 + lane);
-          n = w.items * w.nblk;
+          n = w.units();
         }
         const int at = find_among(x0, n, lane, base);
         if (at >= 0) start.b = b0 + at;
       }
       const SeqWork w = seq_work(p, max(start.b, 0));
-      start.item = (x0 - base) / w.nblk;
-      start.blk = x0 - base - start.item * w.nblk;
+      start.item = (x0 - base) / w.item_units();
+      start.at = x0 - base - start.item * w.item_units();
       start.left = min(per, total - x0);
-      if (start.b >= 0 && start.blk > 0) {
-        const int w0 = x0 - start.blk;  // the item's first block
+      if (start.b >= 0 && start.at > kItemCost) {
+        const int w0 = x0 - start.at + kItemCost;  // the item's first block
         if (w0 / per + 1 == cta) {
           Cursor c = start;
           Seg g;
@@ -443,9 +454,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     Cursor cur = start;
     Seg g;
     bool ok = next_seg(p, cur, g);
-    float sr_next = key_scale(g, 0, key_page(g, 0));
-    int pid_next = g.nb > 1 ? key_page(g, 1) : -1;
-    ok = ok && convert_q(g);
+    float sr_next = 1.f;
+    int pid_next = -1;
+    if (ok) {
+      sr_next = key_scale(g, 0, key_page(g, 0));
+      if (g.nb > 1) pid_next = key_page(g, 1);
+      ok = convert_q(g);
+    }
     int gb = 0;  // blocks of the segments before
     bool more = ok;
     while (ok && more) {
@@ -472,7 +487,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           sr_next = key_scale(gn, 0, key_page(gn, 0));
           if (gn.nb > 1) pid_next = key_page(gn, 1);
         }
-        if (!named_bar_and(1, kSoftThreads, mbar_wait(smem_u32(&s.bar_s[buf]), (i >> 1) & 1, p.err))) { ok = false; break; }
+        // (a wait that gives up is told to the others at the vote below)
+        const bool late = !mbar_wait(smem_u32(&s.bar_s[buf]), (i >> 1) & 1, p.err);
+        __syncwarp();
         tc_fence_after();
         float y[NC];
         {
@@ -501,7 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int h = 0; h < NC; ++h) ymax = fmaxf(ymax, y[h]);
-        if (named_bar_or(1, kSoftThreads, j == 0 || ymax + lg > kTau)) {
+        if (named_bar_or(1, kSoftThreads, late || j == 0 || ymax + lg > kTau)) {
+          if (named_bar_or(1, kSoftThreads, late)) { ok = false; break; }
           // Rows whose largest exceeds their reference by 2^8 (all of them in
           // the first block) get a new one, and their sums and O^T columns
           // are rescaled.
@@ -555,16 +573,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // ---- P^T row r, this thread's rows, as hi + lo; row sums
+        const bool tiny = ROWSCALE && !(sr > 1e-18f);  // (2^-60: P = 2^(y + lg) has 126 - 4 binary places)
+        const float isr = 1.f / sr;
         uint8_t* p_row = s.kv[slot] + kRopeOff;
         uint16_t hi[NC / 2], lo[NC / 2];
 #pragma unroll
         for (int k = 0; k < NC / 2; ++k) {
           const float a = ex2_approx(ROWSCALE ? y[2 * k] + lg : y[2 * k]);
           const float b = ex2_approx(ROWSCALE ? y[2 * k + 1] + lg : y[2 * k + 1]);
-          // (the sum takes the weight itself: a / sr would lose it where the
-          // scale is 0 or tiny)
-          lv[2 * k] += ROWSCALE ? ex2_approx(y[2 * k]) : a;
-          lv[2 * k + 1] += ROWSCALE ? ex2_approx(y[2 * k + 1]) : b;
+          // the sum takes the weight itself: P / scale, or where that is 0 or
+          // so small that P has underflowed, from the logit
+          lv[2 * k] = !ROWSCALE ? lv[2 * k] + a : tiny ? lv[2 * k] + ex2_approx(y[2 * k]) : fmaf(a, isr, lv[2 * k]);
+          lv[2 * k + 1] =
+              !ROWSCALE ? lv[2 * k + 1] + b : tiny ? lv[2 * k + 1] + ex2_approx(y[2 * k + 1]) : fmaf(b, isr, lv[2 * k + 1]);
           split2(a, b, hi[k], lo[k]);
         }
         auto pack = [](const uint16_t* h) { return static_cast<uint32_t>(h[0]) | static_cast<uint32_t>(h[1]) << 16; };
@@ -715,11 +736,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     Seg g, gn;
     int i = 0;
     bool ok = true, more = next_seg(p, cur, g);
-    int pid = read_page(g, 0), pid_n = 0;
     // the first segment's q ahead of the keys (behind the first two blocks of
     // every CTA it took 3 us); the QK warp requests the others
-    if (leader) load_q(g);
+    if (leader && more) load_q(g);
     __syncwarp();
+    int pid = more ? read_page(g, 0) : 0, pid_n = 0;
     while (ok && more) {
       more = next_seg(p, cur, gn);
       for (int j = 0; ok && j < g.nb; ++j) {
@@ -868,72 +889,124 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kQkWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the parts of one cut item, NR / 16 rows (token, head) per CTA:
+// Joins the parts of the cut items, row (token, head) by row:
 //   out = sum_c 2^(L_c - M) O_c / (sum_c 2^(L_c - M) + 2^(sink - M)).
-// Groups of 128 threads hold a float4 of a row each: with few parts a group
-// takes a row; with more than kManyParts all groups share each row's parts, so
-// that a long item's parts are read side by side.
-constexpr int kJoinGroups = 4, kManyParts = 12;
-__host__ __device__ constexpr int join_rows(int nr) { return nr / 16; }
+// Two CTAs an SM; each lists the cut items in shared memory and takes its
+// share of their rows (a CTA for every possible row spent more on CTAs without
+// work than on the sums: 13 us against 4).  A row of few parts is taken by a
+// group of 128 threads, a float4 each; one of more than kManyParts by the four
+// groups of a CTA together, every fourth part each.
+constexpr int kJoinGroups = 4, kManyParts = 16, kMaxGrid = 256;
+
+struct RowSum {
+  float4 acc;
+  float l;
+};
+// Parts first, first + step, ... of a row against the reference m.
 template <int NR>
-__global__ void __launch_bounds__(128 * kJoinGroups) join_kernel(const Params p) {
-  const Cut cut = p.cuts[blockIdx.x + 1];
-  constexpr int kRows = join_rows(NR);
-  const int row0 = blockIdx.y * kRows;
-  if (cut.first_cta < 0 || row0 >= cut.rows) return;
-  __shared__ float4 s_acc[kJoinGroups][128];
-  __shared__ float s_l[kJoinGroups];
-  const int grp = threadIdx.x / 128, col = threadIdx.x % 128, lane = threadIdx.x & 31;
-  const bool many = kRows < kJoinGroups || cut.last_cta - cut.first_cta >= kManyParts;
-  const auto slot = [&](int c, int row) { return static_cast<int64_t>(2 * c + (c == cut.first_cta ? 1 : 0)) * NR + row; };
-  const int nrow = min(kRows, cut.rows - row0);
-  for (int k = 0; k < (many ? nrow : 1); ++k) {
-    const int row = row0 + (many ? k : grp);
-    const bool live = row < cut.rows;  // (a group without a row still meets the barriers)
+__device__ __forceinline__ RowSum sum_parts(const Params& p, const Cut& cut, int row, int parts, int first, int step,
+                                            float m, int col) {
+  const auto slot = [&](int c) { return static_cast<int64_t>(2 * (cut.first_cta + c) + (c == 0 ? 1 : 0)) * NR + row; };
+  RowSum s{make_float4(0.f, 0.f, 0.f, 0.f), 0.f};
+  for (int c0 = first; c0 < parts; c0 += 8 * step) {
+    float w[8];
+    float4 o[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int c = c0 + u * step;
+      w[u] = c < parts ? p.part_lse[slot(c)] : -INFINITY;
+      o[u] = c < parts ? __ldcs(reinterpret_cast<const float4*>(p.part_o + slot(c) * kDV) + col)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float f = exp2f(w[u] - m);  // 0 for a part without keys, whose O is 0
+      s.l += f;
+      s.acc.x = fmaf(f, o[u].x, s.acc.x);
+      s.acc.y = fmaf(f, o[u].y, s.acc.y);
+      s.acc.z = fmaf(f, o[u].z, s.acc.z);
+      s.acc.w = fmaf(f, o[u].w, s.acc.w);
+    }
+  }
+  return s;
+}
+
+template <int NR>
+__global__ void __launch_bounds__(128 * kJoinGroups, 2) join_kernel(const Params p) {
+  __shared__ Cut s_cut[kMaxGrid];
+  __shared__ int s_warp[kMaxGrid / 32];
+  __shared__ float4 s_acc[kJoinGroups - 1][128];
+  __shared__ float s_l[kJoinGroups - 1];
+  const int grp = threadIdx.x / 128, col = threadIdx.x % 128, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // the cut items, in the order of their cuts
+  Cut mine{-1, 0, 0, 0, 0};
+  if (threadIdx.x > 0 && threadIdx.x < p.grid) mine = p.cuts[threadIdx.x];
+  const unsigned cuts = __ballot_sync(0xffffffffu, mine.first_cta >= 0);
+  if (warp < kMaxGrid / 32 && lane == 0) s_warp[warp] = __popc(cuts);
+  __syncthreads();
+  int n = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kMaxGrid / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    n += s_warp[w];
+  }
+  if (mine.first_cta >= 0) s_cut[before + __popc(cuts & ((1u << lane) - 1))] = mine;
+  __syncthreads();
+
+  // the row's reference: the largest of its parts' (and the sink's)
+  const auto reference = [&](const Cut& cut, int row, int parts, float& sk) {
     const int head = p.groups > 1 ? cut.h0 + row : row % p.H;
-    const float sk = p.sink && live ? p.sink[head] * kLog2e : -INFINITY;
+    sk = p.sink ? p.sink[head] * kLog2e : -INFINITY;
     float top = sk;
-    if (live)
-      for (int c = cut.first_cta + lane; c <= cut.last_cta; c += 32) top = fmaxf(top, p.part_lse[slot(c, row)]);
+    for (int c = lane; c < parts; c += 32)
+      top = fmaxf(top, p.part_lse[static_cast<int64_t>(2 * (cut.first_cta + c) + (c == 0 ? 1 : 0)) * NR + row]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float m = top == -INFINITY ? 0.f : top;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = !many || grp == 0 ? exp2f(sk - m) : 0.f;
-    const int step = many ? kJoinGroups : 1;
-    if (live)
-#pragma unroll 4
-      for (int c = cut.first_cta + (many ? grp : 0); c <= cut.last_cta; c += step) {
-        const float w = exp2f(p.part_lse[slot(c, row)] - m);  // 0 for a part without keys, whose O is 0
-        const float4 o = __ldcs(reinterpret_cast<const float4*>(p.part_o + slot(c, row) * kDV) + col);
-        l += w;
-        acc.x = fmaf(w, o.x, acc.x);
-        acc.y = fmaf(w, o.y, acc.y);
-        acc.z = fmaf(w, o.z, acc.z);
-        acc.w = fmaf(w, o.w, acc.w);
-      }
-    if (many) {
-      __syncthreads();  // the sums of the row before have been read
-      s_acc[grp][col] = acc;
-      if (col == 0) s_l[grp] = l;
-      __syncthreads();
-      if (grp > 0) continue;
-#pragma unroll
-      for (int g = 1; g < kJoinGroups; ++g) {
-        const float4 o = s_acc[g][col];
-        l += s_l[g];
-        acc.x += o.x;
-        acc.y += o.y;
-        acc.z += o.z;
-        acc.w += o.w;
-      }
-    }
-    if (!live) continue;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    return top == -INFINITY ? 0.f : top;
+  };
+  const auto store = [&](const Cut& cut, int row, const RowSum& s) {
+    const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
+    const __nv_bfloat162 a = __floats2bfloat162_rn(s.acc.x * inv, s.acc.y * inv);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(s.acc.z * inv, s.acc.w * inv);
     reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(cut.row0 + row) * kDV)[col] =
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  };
+  for (int u = blockIdx.x * kJoinGroups + grp; u < n * NR; u += gridDim.x * kJoinGroups) {
+    const Cut cut = s_cut[u / NR];
+    const int row = u % NR, parts = cut.last_cta - cut.first_cta + 1;
+    if (row >= cut.rows || parts > kManyParts) continue;
+    float sk;
+    const float m = reference(cut, row, parts, sk);
+    RowSum s = sum_parts<NR>(p, cut, row, parts, 0, 1, m, col);
+    s.l += exp2f(sk - m);
+    store(cut, row, s);
+  }
+  for (int u = blockIdx.x; u < n * NR; u += gridDim.x) {
+    const Cut cut = s_cut[u / NR];
+    const int row = u % NR, parts = cut.last_cta - cut.first_cta + 1;
+    if (row >= cut.rows || parts <= kManyParts) continue;  // (the same for the whole CTA)
+    float sk;
+    const float m = reference(cut, row, parts, sk);
+    RowSum s = sum_parts<NR>(p, cut, row, parts, grp, kJoinGroups, m, col);
+    __syncthreads();  // the sums of the row before have been read
+    if (grp > 0) {
+      s_acc[grp - 1][col] = s.acc;
+      if (col == 0) s_l[grp - 1] = s.l;
+    }
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+      for (int g = 0; g < kJoinGroups - 1; ++g) {
+        const float4 o = s_acc[g][col];
+        s.l += s_l[g];
+        s.acc.x += o.x;
+        s.acc.y += o.y;
+        s.acc.z += o.z;
+        s.acc.w += o.w;
+      }
+      s.l += exp2f(sk - m);
+      store(cut, row, s);
+    }
   }
 }
 
@@ -958,7 +1031,7 @@ static smla_status_t launch(const DenseDecodeArgs& a, Params p, int grid, cudaSt
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "dense decode launch");
   if (grid > 1) {
-    join_kernel<NR><<<dim3(grid - 1, NR / join_rows(NR)), 128 * kJoinGroups, 0, stream>>>(p);
+    join_kernel<NR><<<2 * device_sm_count(), 128 * kJoinGroups, 0, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return fail_cuda(e, "dense decode join launch");
   }
@@ -976,7 +1049,7 @@ static int tokens_per_item(int T, int B, int H) {
 static int rows_per_item(int T, int B, int H) { return H >= 48 ? 64 : tokens_per_item(T, B, H) * H; }
 static int decode_grid(int T, int H, int max_kv_len) {
   const int64_t blocks = static_cast<int64_t>(T) * std::max(1, H / 64) * ((max_kv_len + kBK - 1) / kBK);
-  return static_cast<int>(std::min<int64_t>(device_sm_count(), std::max<int64_t>(blocks, 1)));
+  return static_cast<int>(std::min<int64_t>(std::min(device_sm_count(), kMaxGrid), std::max<int64_t>(blocks, 1)));
 }
 
 }  // namespace dd
@@ -991,7 +1064,7 @@ size_t dense_decode_workspace_bytes(int T, int H, int max_kv_len) {
 smla_status_t launch_dense_decode(const DenseDecodeArgs& a, unsigned* err, cudaStream_t stream) {
   using namespace dd;
   const int64_t line = static_cast<int64_t>(a.T) * std::max(1, a.H / 64) *
-                       ((static_cast<int64_t>(a.seqs->max_pages) * a.seqs->page_size + kBK - 1) / kBK + 1);
+                       ((static_cast<int64_t>(a.seqs->max_pages) * a.seqs->page_size + kBK - 1) / kBK + 1 + kItemCost);
   if (line >= (int64_t(1) << 30))
     return fail(SMLA_ERR_UNSUPPORTED, "dense decode: T=%d tokens of up to %d pages of %d keys are too much for one call",
                 a.T, a.seqs->max_pages, a.seqs->page_size);
@@ -1008,6 +1081,7 @@ smla_status_t launch_dense_decode(const DenseDecodeArgs& a, unsigned* err, cudaS
   p.sink = a.sink;
   p.out = a.out;
   p.err = err;
+  p.grid = grid;
   if (grid > 1) {
     p.part_o = static_cast<float*>(a.workspace);
     p.part_lse = p.part_o + static_cast<size_t>(2) * grid * nr * kDV;
