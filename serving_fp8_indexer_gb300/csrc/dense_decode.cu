@@ -573,19 +573,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // ---- P^T row r, this thread's rows, as hi + lo; row sums
-        const bool tiny = ROWSCALE && !(sr > 1e-18f);  // (2^-60: P = 2^(y + lg) has 126 - 4 binary places)
-        const float isr = 1.f / sr;
+        // The sums take the weights themselves, P / scale; where the scale is 0
+        // or so small that P may have underflowed (P = 2^(y + lg) has 122 binary
+        // places), from the logits instead.
+        float isr = ROWSCALE ? 1.f / sr : 1.f;
+        if (ROWSCALE && !(sr > 1e-18f)) {
+          isr = 0.f;
+#pragma unroll
+          for (int h = 0; h < NC; ++h) lv[h] += ex2_approx(y[h]);
+        }
         uint8_t* p_row = s.kv[slot] + kRopeOff;
         uint16_t hi[NC / 2], lo[NC / 2];
 #pragma unroll
         for (int k = 0; k < NC / 2; ++k) {
           const float a = ex2_approx(ROWSCALE ? y[2 * k] + lg : y[2 * k]);
           const float b = ex2_approx(ROWSCALE ? y[2 * k + 1] + lg : y[2 * k + 1]);
-          // the sum takes the weight itself: P / scale, or where that is 0 or
-          // so small that P has underflowed, from the logit
-          lv[2 * k] = !ROWSCALE ? lv[2 * k] + a : tiny ? lv[2 * k] + ex2_approx(y[2 * k]) : fmaf(a, isr, lv[2 * k]);
-          lv[2 * k + 1] =
-              !ROWSCALE ? lv[2 * k + 1] + b : tiny ? lv[2 * k + 1] + ex2_approx(y[2 * k + 1]) : fmaf(b, isr, lv[2 * k + 1]);
+          lv[2 * k] = ROWSCALE ? fmaf(a, isr, lv[2 * k]) : lv[2 * k] + a;
+          lv[2 * k + 1] = ROWSCALE ? fmaf(b, isr, lv[2 * k + 1]) : lv[2 * k + 1] + b;
           split2(a, b, hi[k], lo[k]);
         }
         auto pack = [](const uint16_t* h) { return static_cast<uint32_t>(h[0]) | static_cast<uint32_t>(h[1]) << 16; };

@@ -234,3 +234,17 @@ def test_rows_past_32_bits():
         pool[b:b + 64] = small[a:a + 64]
     seqs = smla.Seqs(seqs.cu_q, seqs.kv_len, far, 64, 2)
     _close(_run(seqs, q, pool, None, 0, 100), *_reference(s, q, val, **_carried(scales, pool)))
+
+
+def test_zero_and_tiny_row_scales_keep_their_weight():
+    """A row of scale 0 (or almost) has value 0, logit 0 and still its share of
+    the softmax."""
+    s, seqs, q, pool, scales, sbs, val = _case([1], [300], 16, "bf16", "row", seed=13)
+    rows = torch.from_numpy(wl.logical_to_phys(s, 0, np.arange(300))).cuda()
+    scales[rows[10:200]] = 0.0
+    scales[rows[200:220]] = 1e-36
+    val[rows[10:220]] *= 0.0
+    pool[rows[10:200]] = 0x38
+    got = _run(seqs, q, pool, scales, sbs, 300)
+    srow = scales.double()[:, 0].clamp_min(1e-30)
+    _close(got, *_reference(s, q, val, srow=srow))
