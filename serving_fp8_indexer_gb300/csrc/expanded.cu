@@ -174,10 +174,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       s.tile = ft;
     }
   }
-  __syncthreads();
-  if (s.b < 0) return;  // a slot past the batch's tiles
-  const Work w = work_of(p, s.b, s.tile);
-  if (threadIdx.x == 0) {
+  // beside the search: barriers, TMEM, descriptors
+  if (threadIdx.x == 32) {
     mbar_init(smem_u32(&s.bar_q), 1);
     for (int i = 0; i < kKSlots; ++i) {
       mbar_init(smem_u32(&s.bar_k_full[i]), 1);
@@ -198,6 +196,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&s.bar_tail), 32);
     fence_mbar_init();
   }
+  if (threadIdx.x == kTmaWarp * 32) {
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tr);
+    tma_prefetch_desc(&tv);
+  }
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&s.tmem_base), kTmemCols);
     tmem_relinquish();
@@ -205,6 +209,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (s.b < 0) {  // a slot past the batch's tiles
+    if (warp == kMmaWarp) tmem_dealloc(s.tmem_base, kTmemCols);
+    return;
+  }
+  const Work w = work_of(p, s.b, s.tile);
   const uint32_t tmem = s.tmem_base;
   // The sequence ends inside the last block: the rows behind it are another
   // sequence's (or nobody's), and a weight of 0 does not cancel an infinity
@@ -629,10 +638,14 @@ smla_status_t launch_expanded(const ExpandedArgs& a, unsigned* err, cudaStream_t
                                           "expanded kernel");
   if (st != SMLA_OK) return st;
   p.slots = static_cast<int>(expanded_slots(a.T, a.B));
-  // heads whose keys and values (512 bytes a row) take at most kGroupBytes,
-  // under half of L2
-  constexpr int64_t kGroupBytes = int64_t(48) << 20;
-  p.head_group = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(a.H, kGroupBytes / (int64_t(512) * std::max(a.S, 1)))));
+  // Groups of heads of even size whose keys and values (512 bytes a row) take
+  // at most kGroupBytes, two thirds of L2: larger groups order more tiles by
+  // their length, smaller ones read less again from HBM (4096 tokens, 128
+  // heads: 12 MB 511 us, 48 MB 486, 80 MB 471, 112 MB 478, all heads 535).
+  constexpr int64_t kGroupBytes = int64_t(80) << 20;
+  const int most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(a.H, kGroupBytes / (int64_t(512) * std::max(a.S, 1)))));
+  const int n_groups = (a.H + most - 1) / most;
+  p.head_group = (a.H + n_groups - 1) / n_groups;
   const int64_t ctas = static_cast<int64_t>(p.slots) * a.H;
   if (ctas > 0x7fffffff || static_cast<int64_t>(p.slots) * p.head_group > 0x7fffffff)
     return fail(SMLA_ERR_UNSUPPORTED, "expanded prefill: too many tiles (T=%d, B=%d, H=%d)", a.T, a.B, a.H);
