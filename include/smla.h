@@ -303,7 +303,7 @@ smla_status_t smla_rope_frequencies(int32_t dim, double base, int32_t scaling, d
  *   out  bf16, f32 or e4m3, likewise; either x itself (same pointer, type and
  *        strides: rotated in place) or memory that x does not overlap
  * D: a multiple of 8, 16..1024.  H: 1..65535.  Strides: in elements,
- * multiples of 8.  Alignment: x and out 16 bytes (out e4m3: 8).
+ * multiples of 8, out's not 0 (x's may be: one row for several heads).  Alignment: x and out 16 bytes (out e4m3: 8).
  * Reads only cu_q and kv_len of seqs (page_table may be any valid pointer). */
 smla_status_t smla_rope(const void* x, int32_t x_dtype, int64_t x_token_stride, int64_t x_head_stride,
                         smla_seqs_t seqs, int32_t H, int32_t D, smla_rope_t rope, void* out, int32_t out_dtype,
@@ -369,7 +369,7 @@ smla_status_t smla_cache_gather(const void* pool, int32_t pool_dtype, int64_t ph
  * Inside a sequence, a NaN or infinity in v at key j may also reach tokens of
  * that sequence before j (within the 128-key block), which weigh it by 0.
  * Strides: in elements, multiples of 8, at least the row's width.
- * H: 1..65535.  softmax_scale: finite, > 0.  Alignment: q, k_nope, k_rope, v,
+ * H: 1..65535.  softmax_scale: 1e-30 .. 1e30.  Alignment: q, k_nope, k_rope, v,
  * out 16 bytes; the others 4.  workspace: caller-owned device scratch of at
  * least smla_expanded_prefill_workspace_size(T, S, B, H) bytes on the
  * current device (16-byte aligned; NULL when that is 0), used when the

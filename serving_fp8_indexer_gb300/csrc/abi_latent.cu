@@ -106,6 +106,8 @@ smla_status_t smla_rope(const void* x, int32_t x_dtype, int64_t x_token_stride, 
   if (st != SMLA_OK) return st;
   if (!stride8(x_token_stride) || !stride8(x_head_stride) || !stride8(out_token_stride) || !stride8(out_head_stride))
     return fail(SMLA_ERR_INVALID_ARG, "strides must be multiples of 8 elements");
+  if (out_token_stride == 0 || out_head_stride == 0)
+    return fail(SMLA_ERR_INVALID_ARG, "out's strides must not be 0: its rows may not share memory");
   if (seqs.T == 0) return SMLA_OK;
   if (!x || !out) return fail(SMLA_ERR_INVALID_ARG, "null pointer");
   const uintptr_t out_mask = out_dtype == SMLA_E4M3 ? 7u : 15u;
@@ -146,6 +148,7 @@ smla_status_t smla_cache_append(const uint16_t* x, int64_t x_stride, smla_seqs_t
   if (!x) return fail(SMLA_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(x) || (rows_out && !aligned16(rows_out)))
     return fail(SMLA_ERR_INVALID_ARG, "x and rows_out must be 16-byte aligned");
+  if (rows_out == x) return fail(SMLA_ERR_INVALID_ARG, "rows_out must not be x");
   unsigned* err = nullptr;
   st = device_err_ptr(&err);
   if (st != SMLA_OK) return st;

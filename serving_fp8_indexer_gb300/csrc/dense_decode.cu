@@ -95,6 +95,7 @@ struct Smem {
   alignas(16) float negm[NR];  // minus the reference, log2 units
   float delta[NR], fac[NR];
   int mx[NR];
+  float sums[4][NR];           // row sums of each quarter of the key lanes
   int nk[NR];                  // keys each row sees
   unsigned long long bar_qraw, bar_q, bar_full[kNST], bar_empty[kNST][2];
   unsigned long long bar_s[2], bar_s_free[2], bar_p[2][2], bar_pv[2], bar_drain[2];
@@ -116,10 +117,10 @@ __device__ __forceinline__ SeqWork seq_work(const Params& p, int b) {
   w.q0 = max(0, p.seqs.cu_q[b]);
   w.q_len = max(0, min(p.T, p.seqs.cu_q[b + 1]) - w.q0);
   w.kv = max(0, p.seqs.kv_len[b]);
-  const int most = p.seqs.max_pages << p.seqs.page_shift;
+  const int64_t most = static_cast<int64_t>(p.seqs.max_pages) << p.seqs.page_shift;
   if (w.kv > most) {
     atomicOr(p.err, kErrShape);
-    w.kv = most;
+    w.kv = static_cast<int>(most);
   }
   w.nblk = max(1, (w.kv + kBK - 1) / kBK);
   w.items = (w.q_len + p.tok_per_item - 1) / p.tok_per_item * p.groups;
@@ -624,10 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       gb += g.nb;
-      // ---- row sums over the key lanes
-      float* linv = s.fac;
-      if (threadIdx.x < NR) linv[threadIdx.x] = 0.f;
-      named_bar_sync(1, kSoftThreads);
+      // ---- row sums over the key lanes, in an order that never changes
       // halving exchanges: lane l ends with the sum of row hb + l % NC
 #pragma unroll
       for (int step = NC / 2; step >= 1; step >>= 1) {
@@ -641,12 +639,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll
       for (int o = NC; o < 32; o <<= 1) lv[0] += __shfl_xor_sync(0xffffffffu, lv[0], o);
-      if (lane < NC) atomicAdd(&linv[hb + lane], lv[0]);
+      if (lane < NC) s.sums[warp & 3][hb + lane] = lv[0];
       named_bar_sync(1, kSoftThreads);
+      float* linv = s.fac;
       // the next segment's q while this one's last PV runs
       float l_row = 0.f, ref_row = 0.f;
       if (threadIdx.x < NR) {
-        l_row = linv[threadIdx.x];
+        l_row = (s.sums[0][threadIdx.x] + s.sums[1][threadIdx.x]) + (s.sums[2][threadIdx.x] + s.sums[3][threadIdx.x]);
         ref_row = s.negm[threadIdx.x];
       }
       if (has_next && !convert_q(gn)) { ok = false; break; }
@@ -772,9 +771,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int pg = __shfl_sync(0xffffffffu, pid, k), key = key0 + k * box;
           int64_t row64 = (static_cast<int64_t>(pg) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
-          if (pg < 0 || row64 >= p.phys_rows) {
+          // (rows past the pool's end, where a page hangs over it, arrive as zeros)
+          if (pg < 0 || row64 + min(box, seg_keys(g) - key) > p.phys_rows) {
             if (leader) atomicOr(p.err, kErrPage);
-            row64 = 0;
+            if (pg < 0 || row64 >= p.phys_rows) row64 = 0;
           }
           const int row = static_cast<int>(row64);
           if (leader) {

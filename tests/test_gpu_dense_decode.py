@@ -248,3 +248,35 @@ def test_zero_and_tiny_row_scales_keep_their_weight():
     got = _run(seqs, q, pool, scales, sbs, 300)
     srow = scales.double()[:, 0].clamp_min(1e-30)
     _close(got, *_reference(s, q, val, srow=srow))
+
+
+@pytest.mark.parametrize("qd,mode", [("bf16", "unit"), ("bf16", "row"), ("e4m3", "row")])
+def test_the_same_call_gives_the_same_bits(qd, mode):
+    for q_lens, kv_lens, H in (([1, 2], [3000, 1100], 128), ([2] * 3, [500, 900, 1300], 16)):
+        s, seqs, q, pool, scales, sbs, val = _case(q_lens, kv_lens, H, qd, mode, seed=14)
+        first = _run(seqs, q, pool, scales, sbs, 3000)
+        for _ in range(4):
+            assert torch.equal(_run(seqs, q, pool, scales, sbs, 3000), first)
+
+
+def test_a_page_that_hangs_over_the_pool_is_reported():
+    """A pool that ends inside a page: keys before its end are read, later ones
+    reported."""
+    s, seqs, q, pool, scales, sbs, val = _case([1], [60], 16, "bf16", "unit", seed=15)
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    one = smla.Seqs(seqs.cu_q, seqs.kv_len, table, 64, 1)
+    _run(one, q, pool[:60].contiguous(), None, 0, 60)
+    with pytest.raises(smla.SmlaError) as e:
+        _run(one, q, pool[:59].contiguous(), None, 0, 60)
+    assert e.value.status == 5
+
+
+def test_many_sequences_and_odd_groups():
+    """More sequences than a warp holds at once, empty ones among them, and
+    token groups that end inside a sequence's tokens."""
+    q_lens = [(3 * i) % 4 for i in range(70)]
+    kv_lens = [max(q, (37 * i) % 300) for i, q in enumerate(q_lens)]
+    for H in (16, 32):
+        s, seqs, q, pool, scales, sbs, val = _case(q_lens, kv_lens, H, "bf16", "row", page=16, seed=16)
+        for most in (300, 1):
+            _close(_run(seqs, q, pool, scales, sbs, most), *_reference(s, q, val, **_carried(scales, pool)))

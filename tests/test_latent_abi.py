@@ -58,7 +58,7 @@ def test_rope_refusals(lib):
 
     for kw, st in ((dict(xd=1), INVALID), (dict(od=3), INVALID), (dict(D=12), UNSUPPORTED), (dict(D=8), UNSUPPORTED),
                    (dict(D=2048), UNSUPPORTED), (dict(H=0), UNSUPPORTED), (dict(H=65536), UNSUPPORTED),
-                   (dict(xts=130), INVALID), (dict(ohs=4), INVALID), (dict(x=None), INVALID), (dict(out=None), INVALID),
+                   (dict(xts=130), INVALID), (dict(ohs=4), INVALID), (dict(ots=0), INVALID), (dict(ohs=0), INVALID), (dict(x=None), INVALID), (dict(out=None), INVALID),
                    (dict(x=P + 8), INVALID), (dict(out=P + 8), INVALID), (dict(out=P + 4, od=1), INVALID),
                    (dict(out=P, od=2), INVALID), (dict(out=P, ots=64), INVALID), (dict(s=_seqs(page_size=48)), UNSUPPORTED),
                    (dict(s=_seqs(B=0)), INVALID)):
@@ -85,7 +85,7 @@ def test_append_and_gather_refusals(lib):
     for kw, st in both:
         assert append(**kw) == st and gather(**kw) == st, kw
     for kw, st in ((dict(x=None), INVALID), (dict(x=P + 2), INVALID), (dict(xs=56), INVALID), (dict(xs=68), INVALID),
-                   (dict(ro=P, rs=63), INVALID), (dict(ro=P + 8), INVALID), (dict(w=P, nd=12), UNSUPPORTED),
+                   (dict(ro=P + 16, rs=63), INVALID), (dict(ro=P + 8), INVALID), (dict(ro=P), INVALID), (dict(w=P, nd=12), UNSUPPORTED),
                    (dict(w=P, nd=72), UNSUPPORTED), (dict(w=P, nd=0), UNSUPPORTED), (dict(w=P, nd=64, eps=-1.0), INVALID),
                    (dict(w=P, nd=64, eps=math.nan), INVALID), (dict(w=P + 8, nd=64), INVALID)):
         assert append(**kw) == st, kw
