@@ -1,6 +1,7 @@
 /*
  * smla.h -- C ABI of libsmla: the FP8 lightning indexer, per-token top-k and
- * sparse MLA prefill attention for GB300 (sm_103a).
+ * MLA attention (sparse, dense, expanded; prefill and decode), with the rotary
+ * positions and the cache writes and reads around them, for GB300 (sm_103a).
  *
  * Every entry point takes plain device pointers and sizes, validates them on
  * the host, enqueues its kernels asynchronously on `stream` and returns an
@@ -303,7 +304,9 @@ smla_status_t smla_rope_frequencies(int32_t dim, double base, int32_t scaling, d
  *   out  bf16, f32 or e4m3, likewise; either x itself (same pointer, type and
  *        strides: rotated in place) or memory that x does not overlap
  * D: a multiple of 8, 16..1024.  H: 1..65535.  Strides: in elements,
- * multiples of 8, out's not 0 (x's may be: one row for several heads).  Alignment: x and out 16 bytes (out e4m3: 8).
+ * multiples of 8; out's rows may not overlap (a stride of 0 is refused; x's
+ * may be 0: one row for several heads).  Alignment: x and out 16 bytes (out
+ * e4m3: 8).
  * Reads only cu_q and kv_len of seqs (page_table may be any valid pointer). */
 smla_status_t smla_rope(const void* x, int32_t x_dtype, int64_t x_token_stride, int64_t x_head_stride,
                         smla_seqs_t seqs, int32_t H, int32_t D, smla_rope_t rope, void* out, int32_t out_dtype,
@@ -402,7 +405,10 @@ smla_status_t smla_expanded_prefill(const uint16_t* q, int64_t q_token_stride, i
  * Block scales (32) take e4m3 q; a bf16 cache takes bf16 q and
  * scale_block_size 0 (SMLA_ERR_UNSUPPORTED otherwise).  Tokens behind the
  * last sequence keep their outputs.  A token of a sequence without keys gets
- * zeros.  workspace: caller-owned device scratch of at least
+ * zeros.  Cache rows outside a sequence's keys never reach its outputs,
+ * whatever they hold; a NaN in the row (or its scale) of one of a sequence's
+ * new tokens may also reach the new tokens before it, which weigh it by 0.  A
+ * row of q with a NaN or an infinity gets NaN.  workspace: caller-owned device scratch of at least
  * smla_dense_decode_workspace_size(T, H, max_kv_len) bytes on the current
  * device (16-byte aligned; NULL when that is 0); contents on entry do not
  * matter, unspecified on return; not shared by calls that may overlap. */

@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           Cursor c = start;
           Seg g;
           next_seg(p, c, g);
-          cut = {w0 / per, (w0 + w.nblk - 1) / per, g.t0 * p.H + g.h0, g.rows, g.h0};
+          cut = {w0 / per, min((w0 + w.nblk - 1) / per, grid - 1), g.t0 * p.H + g.h0, g.rows, g.h0};
         }
       }
     }
@@ -398,7 +398,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           // 2^e that puts amax into [128, 256), from its exponent bits; capped
           // (an all-zero or subnormal row keeps a finite factor)
           const int e = min(7 + 127 - static_cast<int>(__float_as_uint(amax) >> 23), 120);
-          const float sigma = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          // (an infinite q has no finite logits: its row becomes NaN, where e4m3
+          // would have made it a large number)
+          const float sigma = amax < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : NAN;
           if (row < NR) {
 #pragma unroll
             for (int c = 0; c < 9; ++c) {

@@ -280,3 +280,21 @@ def test_many_sequences_and_odd_groups():
         s, seqs, q, pool, scales, sbs, val = _case(q_lens, kv_lens, H, "bf16", "row", page=16, seed=16)
         for most in (300, 1):
             _close(_run(seqs, q, pool, scales, sbs, most), *_reference(s, q, val, **_carried(scales, pool)))
+
+
+@pytest.mark.parametrize("mode", ["unit", "row"])
+@pytest.mark.parametrize("H", [16, 64, 128])
+def test_infinite_and_nan_queries_stay_in_their_row(mode, H):
+    """Every logit of such a row is infinite or NaN, and so its softmax NaN;
+    the other rows do not see it."""
+    s, seqs, q, pool, scales, sbs, val = _case([2, 1], [400, 90], H, "bf16", mode, seed=17)
+    clean = _run(seqs, q, pool, scales, sbs, 400)
+    bad = q.clone()
+    bad[0, 3, 100] = float("inf")
+    bad[1, H - 1, 575] = float("-inf")
+    bad[2, 0, 0] = float("nan")
+    got = _run(seqs, bad, pool, scales, sbs, 400)
+    rows = torch.zeros((3, H), dtype=torch.bool, device="cuda")
+    rows[0, 3] = rows[1, H - 1] = rows[2, 0] = True
+    assert bool(got[rows].isnan().all())
+    assert torch.equal(got[~rows], clean[~rows])
