@@ -37,6 +37,13 @@
 // cores idle: 12 % slower).
 // When one wave of (tile, head) items leaves SMs idle, the keys are split
 // over grid.z and a second kernel joins the partial results.
+//
+// Measured: 4096 tokens x 128 heads 471 us (1460 TFLOP/s, 0.76 of the measured
+// bf16 rate), 8192 x 16 heads 208 us (0.86), 1025 tokens over 6100 keys in four
+// sequences x 32 heads 238 us (0.69).  What bounds it: a pair of blocks takes
+// about 3400 cycles for 2560 of tensor time, and 2700 of them are the
+// shared-memory traffic of the operands (Q and K twelve times 8 KB a tile, V,
+// and the TMA writes); then a CTA's start and epilogue, 8-10 k cycles.
 #include <algorithm>
 #include <cstddef>
 
