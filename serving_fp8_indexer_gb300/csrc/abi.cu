@@ -413,7 +413,7 @@ static smla_status_t sparse_decode_impl(const void* q, int32_t q_dtype, const ui
              nullptr, T, H, softmax_scale, attn_sink, out, nsplit, nsplit > 1 ? part_o : nullptr, part_lse};
   st = launch_attention(a, err, stream);
   if (st != SMLA_OK || nsplit == 1) return st;
-  return launch_decode_combine(part_o, part_lse, attn_sink, T, H, nsplit, out, nullptr, stream);
+  return launch_decode_combine(part_o, part_lse, attn_sink, T, H, nsplit, out, stream);
 }
 
 }  // namespace smla

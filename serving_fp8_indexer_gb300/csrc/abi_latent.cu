@@ -1,6 +1,5 @@
 // The C ABI of the operators around the attention calls (include/smla.h):
 // host-side argument validation and dispatch to their launchers.
-#include <algorithm>
 #include <cmath>
 
 #include "smla_internal.h"
@@ -233,9 +232,7 @@ smla_status_t smla_expanded_prefill(const uint16_t* q, int64_t q_token_stride, i
 
 size_t smla_dense_decode_workspace_size(int32_t T, int32_t H, int32_t max_kv_len) {
   if (T <= 0 || H <= 0 || max_kv_len <= 0) return 0;
-  // the larger of the two forms' needs: which one runs depends on the cache
-  return std::max(decode_workspace_bytes(T, H, decode_splits(T, H, max_kv_len)),
-                  dense_decode_workspace_bytes(T, H, max_kv_len));
+  return dense_decode_workspace_bytes(T, H, max_kv_len);
 }
 
 smla_status_t smla_dense_decode(const void* q, int32_t q_dtype, const void* latent_pool, int32_t pool_dtype,
@@ -255,7 +252,6 @@ smla_status_t smla_dense_decode(const void* q, int32_t q_dtype, const void* late
                   v_depth, softmax_scale, attn_sink, out);
   if (st != SMLA_OK) return st;
   const int T = seqs.T;
-  const int nsplit = T > 0 ? decode_splits(T, H, max_kv_len) : 1;
   const size_t need = smla_dense_decode_workspace_size(T, H, max_kv_len);
   if (workspace_bytes < need || (need && !workspace))
     return fail(SMLA_ERR_INVALID_ARG, "workspace: %zu bytes given, %zu needed", workspace_bytes, need);
@@ -264,23 +260,13 @@ smla_status_t smla_dense_decode(const void* q, int32_t q_dtype, const void* late
   unsigned* err = nullptr;
   st = device_err_ptr(&err);
   if (st != SMLA_OK) return st;
-  if (pool_dtype == SMLA_E4M3 && scale_block_size != 32) {
-    const DenseDecodeArgs d{q, q_dtype, static_cast<const uint8_t*>(latent_pool), phys_rows,
-                            scale_block_size == 0 ? nullptr : scales, &seqs, T, H, max_kv_len, softmax_scale, attn_sink,
-                            out, workspace};
-    return launch_dense_decode(d, err, stream);
-  }
-  // block scales and bf16 caches: the prefill kernel over page-table keys.
-  // Partial outputs [T, nsplit, H, 512] f32, then log2-sum-exps [T, nsplit, H] f32
-  float* part_o = nsplit > 1 ? static_cast<float*>(workspace) : nullptr;
-  const size_t o_bytes = (static_cast<size_t>(T) * nsplit * H * 512 * sizeof(float) + 255) & ~size_t(255);
-  float* part_lse = nsplit > 1 ? reinterpret_cast<float*>(static_cast<char*>(workspace) + o_bytes) : nullptr;
-  AttnArgs a{q, q_dtype, static_cast<const uint8_t*>(latent_pool), phys_rows, scales, scale_block_size, nullptr, 0,
-             nullptr, &seqs, T, H, softmax_scale, attn_sink, out, nsplit, part_o, part_lse,
-             pool_dtype == SMLA_BF16, 1};
-  st = launch_attention(a, err, stream);
-  if (st != SMLA_OK || nsplit == 1) return st;
-  return launch_decode_combine(part_o, part_lse, attn_sink, T, H, nsplit, out, seqs.cu_q + seqs.B, stream);
+  const DenseDecodeArgs d{q,    q_dtype, latent_pool, phys_rows,     scale_block_size == 0 ? nullptr : scales,
+                          &seqs, T,       H,           max_kv_len,    softmax_scale,
+                          attn_sink, out, workspace};
+  // scales by the row (or none) leave the bytes as MMA operands; the others
+  // take 16-bit ones
+  const bool wide = pool_dtype == SMLA_BF16 || scale_block_size == 32;
+  return wide ? launch_dense_decode_wide(d, err, stream) : launch_dense_decode(d, err, stream);
 }
 
 }  // extern "C"

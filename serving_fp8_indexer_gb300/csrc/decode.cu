@@ -27,11 +27,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 __global__ void __launch_bounds__(kThreads) combine_kernel(const float* __restrict__ part_o,
                                                            const float* __restrict__ part_lse,
                                                            const float* __restrict__ sink, int H, int nsplit,
-                                                           uint16_t* __restrict__ out,
-                                                           const int32_t* __restrict__ tokens) {
+                                                           uint16_t* __restrict__ out) {
   const int row = blockIdx.x;  // t * H + h
   const int t = row / H, h = row - t * H;
-  if (tokens && t >= *tokens) return;  // behind the last sequence: no partial was written
   const int64_t base = static_cast<int64_t>(t) * nsplit * H + h;  // split s at base + s * H
   float m = sink ? sink[h] * kLog2e : -INFINITY;
   for (int sp = 0; sp < nsplit; ++sp) m = fmaxf(m, part_lse[base + static_cast<int64_t>(sp) * H]);
@@ -92,13 +90,12 @@ size_t decode_workspace_bytes(int T, int H, int nsplit) {
 }
 
 smla_status_t launch_decode_combine(const float* part_o, const float* part_lse, const float* sink, int T, int H,
-                                    int nsplit, uint16_t* out, const int32_t* tokens,
-                                    cudaStream_t stream) {
+                                    int nsplit, uint16_t* out, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(T) * H;
   if (rows <= 0) return SMLA_OK;
   if (rows > 0x7fffffff) return fail(SMLA_ERR_UNSUPPORTED, "decode combine grid too large");
   dec::combine_kernel<<<static_cast<unsigned>(rows), dec::kThreads, 0, stream>>>(part_o, part_lse, sink, H, nsplit,
-                                                                                  out, tokens);
+                                                                                  out);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "decode combine launch");
   return SMLA_OK;

@@ -428,6 +428,7 @@ __global__ void __launch_bounds__(threads_for(KVP), 1)
   constexpr int kCh = kChunks * EB;       // 64-byte chunks per cache row
   constexpr int kSlotBytes = EB * kKVBytes;
   constexpr int kRopeCh = kRope * EB;     // chunk of column 512 (P goes there)
+  static_assert(!(PP == 2 && KVP == 2), "P lo has a buffer only when rows are single-term");
   static_assert(KVP == 1 || NST == 1, "the blockwise quarter barriers complete once per block (one slot)");
   static_assert(offsetof(S, kv) % 1024 == 0 && offsetof(S, plo) % 1024 == 0,
                 "swizzled operand tiles need 1024-byte alignment");
@@ -1242,16 +1243,9 @@ smla_status_t launch_attention(const AttnArgs& a, unsigned* err, cudaStream_t st
   if (a.cache_bf16) {
     // bf16 cache: bf16 x bf16 MMAs, one gather slot (a 128-row block of
     // 1152-byte rows and the 64-head bf16 q fill shared memory)
-    if (!bf16 || sbs != 0) return fail(SMLA_ERR_UNSUPPORTED, "a bf16 cache takes bf16 q and no scales");
-    return p.keys == kCausal ? launch_k<1, 1, 1, 1, kUnit, kCausal, 2>(tq, p, stream)
-                             : launch_k<1, 1, 1, 1, kUnit, kIndexed, 2>(tq, p, stream);
-  }
-  if (a.two_term_p && !bf16) {
-    // e4m3 q with P as hi + lo, as for bf16 q: the output keeps bf16's accuracy
-    if (p.keys != kCausal) return fail(SMLA_ERR_UNSUPPORTED, "two-term P with e4m3 q is built for dense keys");
-    if (sbs == 0) return launch_k<1, 1, 2, 2, kUnit, kCausal>(tq, p, stream);
-    if (sbs >= kD) return launch_k<1, 1, 2, 2, kRow, kCausal>(tq, p, stream);
-    return launch_k<1, 2, 2, 1, kBlock, kCausal>(tq, p, stream);
+    if (!bf16 || sbs != 0 || p.keys != kIndexed)
+      return fail(SMLA_ERR_UNSUPPORTED, "a bf16 cache takes bf16 q, no scales and indexed keys");
+    return launch_k<1, 1, 1, 1, kUnit, kIndexed, 2>(tq, p, stream);
   }
   if (sbs == 0) return bf16 ? launch_t<2, 1, 2, 2, kUnit>(tq, p, stream) : launch_t<1, 1, 1, 2, kUnit>(tq, p, stream);
   if (sbs >= kD) return bf16 ? launch_t<2, 1, 2, 2, kRow>(tq, p, stream) : launch_t<1, 1, 1, 2, kRow>(tq, p, stream);

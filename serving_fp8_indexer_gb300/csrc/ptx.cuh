@@ -346,6 +346,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, in
          | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// The same with f16 A and B (format 0).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
+  return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
 // ------------------------------------------------------------------ conversions
 // Two floats -> two e4m3 bytes (round to nearest even, saturating), lo byte = a.
 SMLA_DEVICE_INLINE uint16_t f32x2_to_e4m3x2(float a, float b) {

@@ -83,13 +83,11 @@ struct AttnArgs {
   float* part_o;    // [T, nsplit, H, 512]
   float* part_lse;  // [T, nsplit, H]
   int cache_bf16;   // latent_pool holds bf16 [phys_rows, 576] (q bf16, no scales)
-  int two_term_p;   // P as hi + lo also for e4m3 q (dense keys)
 };
 smla_status_t launch_attention(const AttnArgs& a, unsigned* err, cudaStream_t stream);
 
 // Split-K decode: the split count for these sizes, the workspace it needs,
-// and the kernel that combines the partials into the bf16 output (`tokens`:
-// device count of the tokens that have partials, or null for all T).
+// and the kernel that combines the partials into the bf16 output.
 int decode_splits(int T, int H, int indices_stride);
 size_t decode_workspace_bytes(int T, int H, int nsplit);
 // Fixed scratch of smla_sparse_decode_noalloc (a static device array): its
@@ -98,7 +96,7 @@ size_t decode_workspace_bytes(int T, int H, int nsplit);
 size_t noalloc_scratch_bytes();
 smla_status_t noalloc_scratch_for(size_t need, void** out);
 smla_status_t launch_decode_combine(const float* part_o, const float* part_lse, const float* sink, int T, int H,
-                                    int nsplit, uint16_t* out, const int32_t* tokens, cudaStream_t stream);
+                                    int nsplit, uint16_t* out, cudaStream_t stream);
 
 // Rotary positions of x [T, H, D] into out.
 struct RopeArgs {
@@ -159,13 +157,14 @@ int expanded_splits(int T, int S, int B, int H);
 size_t expanded_workspace_bytes(int T, int H, int nsplit);
 smla_status_t launch_expanded(const ExpandedArgs& a, unsigned* err, cudaStream_t stream);
 
-// Dense decode over an e4m3 cache with unit or per-row scales.
+// Dense decode: over an e4m3 cache with unit or per-row scales, and (`wide`:
+// 16-bit operands) over a bf16 cache or one with block scales.
 struct DenseDecodeArgs {
   const void* q;
   int q_dtype;
-  const uint8_t* latent;
+  const void* latent;
   int64_t phys_rows;
-  const float* scales;  // null: unit
+  const float* scales;  // null: unit (wide: a bf16 cache)
   const smla_seqs_t* seqs;
   int T, H, max_kv_len;
   float softmax_scale;
@@ -175,5 +174,6 @@ struct DenseDecodeArgs {
 };
 size_t dense_decode_workspace_bytes(int T, int H, int max_kv_len);
 smla_status_t launch_dense_decode(const DenseDecodeArgs& a, unsigned* err, cudaStream_t stream);
+smla_status_t launch_dense_decode_wide(const DenseDecodeArgs& a, unsigned* err, cudaStream_t stream);
 
 }  // namespace smla

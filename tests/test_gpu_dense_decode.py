@@ -298,3 +298,20 @@ def test_infinite_and_nan_queries_stay_in_their_row(mode, H):
     rows[0, 3] = rows[1, H - 1] = rows[2, 0] = True
     assert bool(got[rows].isnan().all())
     assert torch.equal(got[~rows], clean[~rows])
+
+
+@pytest.mark.parametrize("qd,mode", [("bf16", "row"), ("e4m3", "row"), ("e4m3", "block")])
+@pytest.mark.parametrize("tiny", [0.0, 1e-36])
+def test_rows_of_tiny_scale_ahead_of_the_others(qd, mode, tiny):
+    """The first blocks' rows have scale 0 (or almost), the later ones' ordinary
+    scales: the first ones' logits and values are 0, their share is not."""
+    s, seqs, q, pool, scales, sbs, val = _case([1], [700], 16, qd, mode, seed=18)
+    rows = torch.from_numpy(wl.logical_to_phys(s, 0, np.arange(700))).cuda()
+    scales[rows[:400]] = tiny
+    val[rows[:400]] *= 0.0
+    carried = _carried(scales.clamp_min(1e-30), pool)
+    for most in (700, 1):
+        _close(_run(seqs, q, pool, scales, sbs, most), *_reference(s, q, val, **carried))
+    scales[rows] = tiny
+    got = _run(seqs, q, pool, scales, sbs, 700)
+    assert bool((got.float().abs() <= 1e-33).all())
