@@ -11,7 +11,7 @@ namespace dd {
 
 constexpr int kD = 576, kDV = 512;
 constexpr int kBK = 128;                 // keys of a block
-constexpr int kSoftThreads = 256, kThreads = 384;
+constexpr int kSoftThreads = 256, kSoftWarps = 8, kThreads = 384;
 constexpr int kTmaWarp = 8, kQkWarp = 9, kPvWarp = 10;
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -200,6 +200,13 @@ __device__ __forceinline__ float ord_float(int o) { return __int_as_float(o >= 0
 // byte offset of 16-byte piece c of row r in a 128- (64-) byte-swizzled chunk
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
 __device__ __forceinline__ uint32_t sw64(int r, int c) { return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
+
+// One arrival for the warp, behind what every lane did (an arrival from each
+// lane is 32 in a row on one word).
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
 
 // N (8, 16 or 32) TMEM columns of the thread's lane, waited for.
 template <int N>

@@ -111,9 +111,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s.bar_s[i]), 1);
-      mbar_init(smem_u32(&s.bar_s_free[i]), kSoftThreads);
-      mbar_init(smem_u32(&s.bar_p[i][0]), kSoftThreads / 2);
-      mbar_init(smem_u32(&s.bar_p[i][1]), kSoftThreads / 2);
+      mbar_init(smem_u32(&s.bar_s_free[i]), kSoftWarps);
+      mbar_init(smem_u32(&s.bar_p[i][0]), kSoftWarps / 2);
+      mbar_init(smem_u32(&s.bar_p[i][1]), kSoftWarps / 2);
       mbar_init(smem_u32(&s.bar_pv[i]), 1);
       mbar_init(smem_u32(&s.bar_drain[i]), 1);
     }
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < NC; ++h) y[h] = QP == 2 ? __uint_as_float(v0[h]) + __uint_as_float(v1[h]) : __uint_as_float(v0[h]);
         }
         tc_fence_before();
-        mbar_arrive(smem_u32(&s.bar_s_free[buf]));
+        warp_arrive(smem_u32(&s.bar_s_free[buf]), lane);
         const float lg = ROWSCALE ? __log2f(sr) : 0.f, lgc = ROWSCALE ? fmaxf(lg, kLeastLg) : 0.f;
         float ymax = -INFINITY;
 #pragma unroll
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(smem_u32(&s.bar_p[i & 1][(warp & 3) >> 1]));
+        warp_arrive(smem_u32(&s.bar_p[i & 1][(warp & 3) >> 1]), lane);
       }
       if (!ok) break;
       gb += g.nb;
@@ -531,11 +531,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto parts_of = [&](const Seg& g, int j) {  // parts with keys in them
       return (min(kBK, max(0, seg_keys(g) - (g.j0 + j) * kBK)) + box - 1) / box;
     };
-    const auto read_page = [&](const Seg& g, int j) {
+    // the first physical row of the lane's part of block j
+    const auto read_row = [&](const Seg& g, int j) -> int {
       const int key = (g.j0 + j) * kBK + lane * box;
-      return lane < parts_of(g, j)
-                 ? p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)]
-                 : 0;
+      if (lane >= parts_of(g, j)) return 0;
+      const int pg = p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)];
+      const int64_t row = (static_cast<int64_t>(pg) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
+      // (rows past the pool's end, where a page hangs over it, arrive as zeros)
+      if (pg < 0 || row + min(box, seg_keys(g) - key) > p.phys_rows) {
+        atomicOr(p.err, kErrPage);
+        if (pg < 0 || row >= p.phys_rows) return 0;
+      }
+      return static_cast<int>(row);
     };
     Cursor cur = start;
     Seg g, gn;
@@ -545,18 +552,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every CTA it took 3 us); the QK warp requests the others
     if (leader && more) load_q(g);
     __syncwarp();
-    int pid = more ? read_page(g, 0) : 0, pid_n = 0;
+    int row = more ? read_row(g, 0) : 0, row_n = 0;
     while (ok && more) {
       more = next_seg(p, cur, gn);
       for (int j = 0; ok && j < g.nb; ++j) {
         if (j + 1 < g.nb)
-          pid_n = read_page(g, j + 1);
+          row_n = read_row(g, j + 1);
         else if (more)
-          pid_n = read_page(gn, 0);
-        const int slot = i % kNST, key0 = (g.j0 + j) * kBK, parts = parts_of(g, j);
+          row_n = read_row(gn, 0);
+        const int slot = i % kNST, parts = parts_of(g, j);
         const uint32_t bar = smem_u32(&s.bar_full[slot]);
         const uint32_t dst = smem_u32(s.kv[slot]);
         const uint32_t par = ((i / kNST) & 1) ^ 1;
+        const auto load = [&](int k, int y) {  // part k's keys
+          const uint32_t d = dst + k * box * 128;
+          tma_load_2d(d, &tk, 0, y, bar);
+          tma_load_2d(d + kChunk, &tk, 128, y, bar);
+          tma_load_2d(d + 2 * kChunk, &tk, 256, y, bar);
+          tma_load_2d(d + 3 * kChunk, &tk, 384, y, bar);
+          tma_load_2d(dst + kRopeOff + k * box * 64, &tr, 512, y, bar);
+        };
+        const int y0 = __shfl_sync(0xffffffffu, row, 0), y1 = __shfl_sync(0xffffffffu, row, 1);
+        if (parts == 2 && half_parts == 1) {
+          // two pages (the usual case), straight from one thread
+          int done = 0;
+          if (leader) {
+            ok = mbar_wait(smem_u32(&s.bar_empty[slot][0]), par, p.err);
+            if (ok) {
+              done = 1;
+              mbar_arrive_expect_tx(bar, 2 * box * kD);
+              load(0, y0);
+              // the second half of the keys once PV has given it back
+              ok = mbar_wait(smem_u32(&s.bar_empty[slot][1]), par, p.err);
+              if (ok) load(1, y1);
+            }
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          i += __any_sync(0xffffffffu, done) ? 1 : 0;
+          row = row_n;
+          continue;
+        }
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_empty[slot][0]), par, p.err))) { ok = false; break; }
         if (leader) {
           if (parts > 0)
@@ -564,33 +599,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             mbar_arrive(bar);
         }
-        // the second half of the keys once PV has given it back
         for (int k = 0; k < parts; ++k) {
           if (k == half_parts &&
               !__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_empty[slot][1]), par, p.err))) {
             ok = false;
             break;
           }
-          const int pg = __shfl_sync(0xffffffffu, pid, k), key = key0 + k * box;
-          int64_t row64 = (static_cast<int64_t>(pg) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
-          // (rows past the pool's end, where a page hangs over it, arrive as zeros)
-          if (pg < 0 || row64 + min(box, seg_keys(g) - key) > p.phys_rows) {
-            if (leader) atomicOr(p.err, kErrPage);
-            if (pg < 0 || row64 >= p.phys_rows) row64 = 0;
-          }
-          const int row = static_cast<int>(row64);
-          if (leader) {
-            const uint32_t d = dst + k * box * 128;
-            tma_load_2d(d, &tk, 0, row, bar);
-            tma_load_2d(d + kChunk, &tk, 128, row, bar);
-            tma_load_2d(d + 2 * kChunk, &tk, 256, row, bar);
-            tma_load_2d(d + 3 * kChunk, &tk, 384, row, bar);
-            tma_load_2d(dst + kRopeOff + k * box * 64, &tr, 512, row, bar);
-          }
+          const int y = __shfl_sync(0xffffffffu, row, k);
+          if (leader) load(k, y);
           __syncwarp();
         }
         ++i;
-        pid = pid_n;
+        row = row_n;
       }
       g = gn;
     }

@@ -48,11 +48,12 @@ constexpr float kTinyLg = -60.f;   // rows of smaller scales take their sums fro
 template <int NR, bool BLOCK>
 struct Smem {
   static constexpr int kPairs = BLOCK || NR == 64 ? 4 : 5;
-  static constexpr int kRaws = NR == 16 ? 3 : 2;
+  static constexpr int kRaws = 2;  // one for each group of converting warps, which then keep to their own barriers
   uint8_t q[NR * kD * 2];  // nine chunks [NR][128 bytes]
   uint8_t pair[kPairs][2 * kChunk];
   uint8_t rope[kChunk];    // then P^T [128 keys][128 bytes]
   uint8_t raw[BLOCK ? kRaws * kChunk : 16];
+  alignas(1024) uint8_t raw_rope[BLOCK ? kChunk / 2 : 16];
   alignas(16) float negm[NR];  // minus the reference, log2 units
   float delta[NR], fac[NR];
   int mx[NR];
@@ -60,7 +61,7 @@ struct Smem {
   int nk[NR];
   float smax[BLOCK ? 2 : 1][BLOCK ? kBK : 1];  // largest scale of each half of a row's blocks
   unsigned long long bar_q, bar_pair_full[kPairs], bar_pair_empty[kPairs], bar_rope_full, bar_rope_empty;
-  unsigned long long bar_raw_full[kRaws], bar_raw_empty[kRaws];
+  unsigned long long bar_raw_full[kRaws], bar_raw_empty[kRaws], bar_raw_rope_full, bar_raw_rope_empty;
   unsigned long long bar_s[2], bar_s_free[2], bar_p, bar_pv, bar_drain[2];
   uint32_t tmem_base;
 };
@@ -96,24 +97,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    constexpr int kFullCount = BLOCK ? kSoftThreads : 1;
     mbar_init(smem_u32(&s.bar_q), kSoftThreads);
     for (int i = 0; i < kPairs; ++i) {
-      mbar_init(smem_u32(&s.bar_pair_full[i]), kFullCount);
+      mbar_init(smem_u32(&s.bar_pair_full[i]), BLOCK ? kSoftWarps / 2 : 1);
       mbar_init(smem_u32(&s.bar_pair_empty[i]), 1);
     }
-    mbar_init(smem_u32(&s.bar_rope_full), kFullCount);
+    mbar_init(smem_u32(&s.bar_rope_full), BLOCK ? kSoftWarps : 1);
     mbar_init(smem_u32(&s.bar_rope_empty), 1);
     for (int i = 0; i < kRaws; ++i) {
       mbar_init(smem_u32(&s.bar_raw_full[i]), 1);
-      mbar_init(smem_u32(&s.bar_raw_empty[i]), kSoftThreads);
+      mbar_init(smem_u32(&s.bar_raw_empty[i]), kSoftWarps / 2);
     }
+    mbar_init(smem_u32(&s.bar_raw_rope_full), 1);
+    mbar_init(smem_u32(&s.bar_raw_rope_empty), kSoftWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s.bar_s[i]), 1);
-      mbar_init(smem_u32(&s.bar_s_free[i]), kSoftThreads);
+      mbar_init(smem_u32(&s.bar_s_free[i]), kSoftWarps);
       mbar_init(smem_u32(&s.bar_drain[i]), 1);
     }
-    mbar_init(smem_u32(&s.bar_p), kSoftThreads);
+    mbar_init(smem_u32(&s.bar_p), kSoftWarps);
     mbar_init(smem_u32(&s.bar_pv), 1);
     fence_mbar_init();
   }
@@ -173,8 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // Page of the thread's key of block j (-1 outside the keys), and the nine of
     // its row's scales that this half of the warps converts with (1 there, and
-    // on a bad page, which the TMA warp reports): blocks 4t + 2 half, + 1 of
-    // pair t, 16 + half of the rotary chunk.  Read two blocks and one ahead.
+    // on a bad page, which the TMA warp reports): those of pairs half and half
+    // + 2, and 16 + half of the rotary chunk.  Read two blocks and one ahead.
     auto key_page = [&](const Seg& g, int j) -> int {
       const int key = (g.j0 + j) * kBK + r;
       return BLOCK && key < seg_keys(g)
@@ -189,44 +191,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool bad = pid < 0 || row >= p.phys_rows;
       const float* src = p.scales + (bad ? 0 : row * 18);
 #pragma unroll
-      for (int t = 0; t < 9; ++t) sc[t] = bad ? 1.f : src[t < 8 ? (t >> 1) * 4 + 2 * half + (t & 1) : 16 + half];
+      for (int k = 0; k < 9; ++k) sc[k] = bad ? 1.f : src[k < 8 ? (k >> 2) * 8 + 4 * half + (k & 3) : 16 + half];
     };
-    // block i's bytes to f16; `ex` receives the row's exponent
+    const uint32_t nil = static_cast<uint32_t>(p.grid) >> 16;  // 0
+    // Block i's bytes to f16; `ex` receives the row's exponent.  Pairs 0 and 2
+    // are the first four warps' work, 1 and 3 the others', so that one group's
+    // latencies run beside the other's; the rotary chunk is shared.
     auto convert = [&](int i, int& ex) -> bool {
       bool fine = true;
       float most = 0.f;
 #pragma unroll
-      for (int t = 0; t < 9; ++t) most = fmaxf(most, fabsf(sc[t]));
+      for (int k = 0; k < 9; ++k) most = fmaxf(most, fabsf(sc[k]));
       s.smax[half][r] = most;
       named_bar_sync(2 + (warp & 3), 64);
       ex = min(max(static_cast<int>(__float_as_uint(fmaxf(most, s.smax[half ^ 1][r])) >> 23), 1), 253);
       const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);  // 2^(127 - ex)
       uint32_t s2[9];
 #pragma unroll
-      for (int t = 0; t < 9; ++t) s2[t] = f32x2_to_f16x2(sc[t] * down, sc[t] * down);
+      for (int k = 0; k < 9; ++k) s2[k] = f32x2_to_f16x2(sc[k] * down, sc[k] * down);
 #pragma unroll
-      for (int t = 0; t < 5; ++t) {
-        const int rg = 5 * i + t, rs = rg % kRaws, g = 4 * i + t, sl = g % kPairs;
-        fine = mbar_wait(smem_u32(&s.bar_raw_full[rs]), (rg / kRaws) & 1, p.err) && fine;
-        uint4 u[4];
-        const uint8_t* raw = s.raw + rs * kChunk;
+      for (int k = 0; k < 3; ++k) {
+        const bool nope = k < 2;
+        const int n = 4 * i + half + 2 * k, rs = half, sl = n % kPairs;  // the pair (k < 2)
+        const int par = nope ? (n / kRaws) & 1 : i & 1;
+        fine = mbar_wait(nope ? smem_u32(&s.bar_raw_full[rs]) : smem_u32(&s.bar_raw_rope_full), par, p.err) && fine;
+        uint4 u[8];
+        uint32_t seen = 0;
 #pragma unroll
-        for (int c = 0; c < (t < 4 ? 4 : 2); ++c)
-          u[c] = *reinterpret_cast<const uint4*>(raw + (t < 4 ? sw128(r, half * 4 + c) : sw64(r, half * 2 + c)));
-        mbar_arrive(smem_u32(&s.bar_raw_empty[rs]));
-        fine = (t < 4 ? mbar_wait(smem_u32(&s.bar_pair_empty[sl]), ((g / kPairs) & 1) ^ 1, p.err)
-                      : mbar_wait(smem_u32(&s.bar_rope_empty), (i & 1) ^ 1, p.err)) && fine;
-        uint8_t* dst = t < 4 ? s.pair[sl] + half * kChunk : s.rope;
-        const int c0 = t < 4 ? 0 : half * 4;
+        for (int c = 0; c < (nope ? 8 : 2); ++c) {
+          u[c] = *reinterpret_cast<const uint4*>(nope ? s.raw + rs * kChunk + sw128(r, c) : s.raw_rope + sw64(r, half * 2 + c));
+          seen |= u[c].x;
+        }
+        // The raw chunk goes back once the reads have returned.  The arrival takes
+        // their values (times a 0 that the compiler does not know): one that only
+        // follows them in the program may overtake them while the tensor cores
+        // keep shared memory busy, and TMA then writes what is still to be read.
+        warp_arrive((nope ? smem_u32(&s.bar_raw_empty[rs]) : smem_u32(&s.bar_raw_rope_empty)) + (seen & nil), lane);
+        fine = (nope ? mbar_wait(smem_u32(&s.bar_pair_empty[sl]), ((n / kPairs) & 1) ^ 1, p.err)
+                     : mbar_wait(smem_u32(&s.bar_rope_empty), (i & 1) ^ 1, p.err)) && fine;
 #pragma unroll
-        for (int c = 0; c < (t < 4 ? 4 : 2); ++c) {
+        for (int c = 0; c < (nope ? 8 : 2); ++c) {
           uint4 a, b;
-          scaled16(u[c], s2[t < 4 ? 2 * t + (c >> 1) : 8], a, b);
-          *reinterpret_cast<uint4*>(dst + sw128(r, c0 + 2 * c)) = a;
-          *reinterpret_cast<uint4*>(dst + sw128(r, c0 + 2 * c + 1)) = b;
+          scaled16(u[c], s2[nope ? 4 * k + (c >> 1) : 8], a, b);
+          uint8_t* dst = nope ? s.pair[sl] + (c >> 2) * kChunk : s.rope;
+          const int piece = nope ? (c & 3) * 2 : half * 4 + 2 * c;
+          *reinterpret_cast<uint4*>(dst + sw128(r, piece)) = a;
+          *reinterpret_cast<uint4*>(dst + sw128(r, piece + 1)) = b;
         }
         fence_proxy_async_smem();
-        mbar_arrive(t < 4 ? smem_u32(&s.bar_pair_full[sl]) : smem_u32(&s.bar_rope_full));
+        warp_arrive(nope ? smem_u32(&s.bar_pair_full[sl]) : smem_u32(&s.bar_rope_full), lane);
       }
       return fine;
     };
@@ -286,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < NC; ++h) y[h] = fmaf(__uint_as_float(v[h]), csr, s.negm[hb + h]);
         }
         tc_fence_before();
-        mbar_arrive(smem_u32(&s.bar_s_free[buf]));
+        warp_arrive(smem_u32(&s.bar_s_free[buf]), lane);
         float ymax = -INFINITY;
         const int key = (g.j0 + j) * kBK + r;
         const bool edge = (g.j0 + j + 1) * kBK > g.pos1;  // some row's keys end in this block (or before it)
@@ -386,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(smem_u32(&s.bar_p));
+        warp_arrive(smem_u32(&s.bar_p), lane);
       }
       if (!ok) break;
       gb += g.nb;
@@ -498,65 +511,92 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     Cursor cur = start;
     Seg g, gn;
-    int i = 0, n_pair = 0, n_rope = 0, n_raw = 0;
+    int n_pair = 0, n_rope = 0;
     bool ok = true, more = next_seg(p, cur, g);
     int row = more ? read_row(g, 0) : 0, row_n = 0;
     while (ok && more) {
       more = next_seg(p, cur, gn);
-      for (int j = 0; ok && j < g.nb; ++j, ++i) {
+      for (int j = 0; ok && j < g.nb; ++j) {
         if (j + 1 < g.nb)
           row_n = read_row(g, j + 1);
         else if (more)
           row_n = read_row(gn, 0);
         const int parts = parts_of(g, j);
-        for (int t = 0; ok && t < 5; ++t) {
-          uint32_t empty, full, dst, par;
-          if (BLOCK) {
-            const int rs = n_raw % kRaws;
-            empty = smem_u32(&s.bar_raw_empty[rs]);
-            full = smem_u32(&s.bar_raw_full[rs]);
-            dst = smem_u32(s.raw) + rs * kChunk;
-            par = ((n_raw / kRaws) & 1) ^ 1;
-          } else if (t < 4) {
-            const int sl = n_pair % kPairs;
-            empty = smem_u32(&s.bar_pair_empty[sl]);
-            full = smem_u32(&s.bar_pair_full[sl]);
-            dst = smem_u32(s.pair[sl]);
-            par = ((n_pair / kPairs) & 1) ^ 1;
+        // chunk t of the block: its barriers and place
+        const auto place = [&](int t, uint32_t& empty, uint32_t& full, uint32_t& dst, uint32_t& par) {
+          if (t < 4) {
+            const int sl = n_pair % kPairs, rs = n_pair % kRaws;
+            empty = BLOCK ? smem_u32(&s.bar_raw_empty[rs]) : smem_u32(&s.bar_pair_empty[sl]);
+            full = BLOCK ? smem_u32(&s.bar_raw_full[rs]) : smem_u32(&s.bar_pair_full[sl]);
+            dst = BLOCK ? smem_u32(s.raw) + rs * kChunk : smem_u32(s.pair[sl]);
+            par = ((n_pair / (BLOCK ? kRaws : kPairs)) & 1) ^ 1;
           } else {
-            empty = smem_u32(&s.bar_rope_empty);
-            full = smem_u32(&s.bar_rope_full);
-            dst = smem_u32(s.rope);
+            empty = BLOCK ? smem_u32(&s.bar_raw_rope_empty) : smem_u32(&s.bar_rope_empty);
+            full = BLOCK ? smem_u32(&s.bar_raw_rope_full) : smem_u32(&s.bar_rope_full);
+            dst = BLOCK ? smem_u32(s.raw_rope) : smem_u32(s.rope);
             par = (n_rope & 1) ^ 1;
           }
-          ok = __all_sync(0xffffffffu, mbar_wait(empty, par, p.err));
-          if (!ok) break;
-          if (BLOCK)
-            ++n_raw;
-          else if (t < 4)
+        };
+        const auto requested = [&](int t) {
+          if (t < 4)
             ++n_pair;
           else
             ++n_rope;
-          const int width = BLOCK ? (t < 4 ? 128 : 64) : (t < 4 ? 256 : 128);  // bytes of a key
+        };
+        const auto load = [&](int t, uint32_t dst, int y, uint32_t full) {  // one part's keys
+          if (BLOCK) {
+            if (t < 4)
+              tma_load_2d(dst, &tk, t * 128, y, full);
+            else
+              tma_load_2d(dst, &tr, 512, y, full);
+          } else {
+            tma_load_2d(dst, &tk, t * 256, y, full);
+            if (t < 4) tma_load_2d(dst + kChunk, &tk, t * 256 + 128, y, full);
+          }
+        };
+        // bytes of a key in chunk t, and in a row of its place
+        const auto width = [](int t) { return BLOCK ? (t < 4 ? 128 : 64) : (t < 4 ? 256 : 128); };
+        const auto pitch = [](int t) { return BLOCK && t == 4 ? 64 : 128; };
+        const int y0 = __shfl_sync(0xffffffffu, row, 0), y1 = __shfl_sync(0xffffffffu, row, 1);
+        if (parts == 2) {
+          // two pages (the usual case), straight from one thread: a third of the
+          // time of the loop below, which took 220 cycles a box
+          if (leader) {
+#pragma unroll
+            for (int t = 0; t < 5; ++t) {
+              uint32_t empty, full, dst, par;
+              place(t, empty, full, dst, par);
+              ok = ok && mbar_wait(empty, par, p.err);
+              if (!ok) break;
+              requested(t);
+              mbar_arrive_expect_tx(full, 2 * box * width(t));
+              load(t, dst, y0, full);
+              load(t, dst + box * pitch(t), y1, full);
+            }
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!leader) {
+#pragma unroll
+            for (int t = 0; t < 5; ++t) requested(t);
+          }
+          row = row_n;
+          continue;
+        }
+        for (int t = 0; ok && t < 5; ++t) {
+          uint32_t empty, full, dst, par;
+          place(t, empty, full, dst, par);
+          ok = __all_sync(0xffffffffu, mbar_wait(empty, par, p.err));
+          if (!ok) break;
+          requested(t);
           if (leader) {
             if (parts > 0)
-              mbar_arrive_expect_tx(full, parts * box * width);
+              mbar_arrive_expect_tx(full, parts * box * width(t));
             else
               mbar_arrive(full);
           }
           for (int k = 0; k < parts; ++k) {
             const int y = __shfl_sync(0xffffffffu, row, k);
-            if (leader) {
-              if (BLOCK) {
-                if (t < 4)
-                  tma_load_2d(dst + k * box * 128, &tk, t * 128, y, full);
-                else
-                  tma_load_2d(dst + k * box * 64, &tr, 512, y, full);
-              } else {
-                tma_load_2d(dst + k * box * 128, &tk, t * 256, y, full);
-                if (t < 4) tma_load_2d(dst + kChunk + k * box * 128, &tk, t * 256 + 128, y, full);
-              }
-            }
+            if (leader) load(t, dst + k * box * pitch(t), y, full);
           }
           __syncwarp();
         }
@@ -565,17 +605,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       g = gn;
     }
     // nothing is still landing when the CTA ends
-    for (int sl = 0; sl < kRaws; ++sl) {
-      const int loads = (n_raw + kRaws - 1 - sl) / kRaws;
-      if (loads > 0) mbar_wait(smem_u32(&s.bar_raw_full[sl]), (loads - 1) & 1, p.err);
-    }
-    if (!BLOCK) {
-      for (int sl = 0; sl < kPairs; ++sl) {
-        const int loads = (n_pair + kPairs - 1 - sl) / kPairs;
-        if (loads > 0) mbar_wait(smem_u32(&s.bar_pair_full[sl]), (loads - 1) & 1, p.err);
+    if (leader) {
+      constexpr int kRing = BLOCK ? kRaws : kPairs;
+      for (int sl = 0; sl < kRing; ++sl) {
+        const int loads = (n_pair + kRing - 1 - sl) / kRing;
+        if (loads > 0)
+          mbar_wait(BLOCK ? smem_u32(&s.bar_raw_full[sl]) : smem_u32(&s.bar_pair_full[sl]), (loads - 1) & 1, p.err);
       }
-      if (n_rope > 0) mbar_wait(smem_u32(&s.bar_rope_full), (n_rope - 1) & 1, p.err);
+      if (n_rope > 0)
+        mbar_wait(BLOCK ? smem_u32(&s.bar_raw_rope_full) : smem_u32(&s.bar_rope_full), (n_rope - 1) & 1, p.err);
     }
+    __syncwarp();
   } else if (warp == kQkWarp) {
     // ==================================================================== QK
     Cursor cur = start;
