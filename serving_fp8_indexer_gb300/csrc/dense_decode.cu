@@ -17,8 +17,9 @@
 //   sequence.  A part that is a whole item writes its output; the others
 //   write f32 partial results (at most two per CTA), which a second kernel
 //   joins per cut item.
-// * Loads.  Pages are contiguous, so a block is 10 TMA boxes (64-key pages)
-//   instead of 4608 16-byte gathers; nothing but the page table is read to
+// * Loads.  Pages are contiguous, so a block is 10 TMA boxes (64-key pages,
+//   issued straight from one thread: 220 cycles a box out of a loop with
+//   shuffles) instead of 4608 16-byte gathers; nothing but the page table is read to
 //   address them.  Columns 0..511 lie in four 128-byte-swizzled chunks (each
 //   the K-major QK operand and, read MN-major, one 128-column tile of V), the
 //   rotary part in a 64-byte-swizzled one, which P^T reuses after QK.
@@ -31,9 +32,9 @@
 // at NR = 64 (2688 cycles), where the shared-memory reads of N = 64 operands
 // set their rate (48 cycles an MMA).
 //
-// Measured: 16 heads over 4 x <= 120 K keys 51 us (4.4 TB/s; 6.2 while the line
+// Measured: 16 heads over 4 x <= 120 K keys 50 us (4.5 TB/s; 6.2 while the line
 // runs, then 6 us of start and 5.7 of join); 8 x 2 tokens x 128 heads over <= 8192
-// keys 49 us (640 TFLOP/s): 3.9 k cycles a block for the chain load 3 k, QK 1.5 k,
+// keys 48 us (653 TFLOP/s): 3.9 k cycles a block for the chain load 3 k, QK 1.5 k,
 // softmax 2.4 k, PV 2.4 k over two slots, 12 k cycles of start, 7.7 us of join.
 //
 // Warps: 0-7 softmax and epilogue (thread = one key x NR/2 rows), 8 TMA, 9 QK,

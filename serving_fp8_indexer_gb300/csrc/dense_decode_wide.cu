@@ -7,26 +7,36 @@
 // as in the e4m3 kernel, with kind::f16 MMAs and one term for everything.  A
 // bf16 cache: q, K and P in bf16 (P's rounding is 2^-9 of a weight).  Block
 // scales: f16, a row carried as byte * scale_blk 2^-e with 2^e the power of two
-// below its largest scale (the scale and the product are off by 2^-12 and 2^-11;
-// e4m3 q is exact); its logits and its weights take 2^e instead, as the e4m3
-// kernel does with a row's scale.  The product is one f16x2 multiply for two
-// elements; through f32 to bf16 it was five instructions and @@.  The line of
-// work, the walk along it and the join are shared with the e4m3 kernel.
+// below its largest scale (the scale is off by 2^-12, the product by 2^-11; e4m3
+// q is exact); its logits and its weights take 2^e instead, as the e4m3 kernel
+// does with a row's scale.  The product is one f16x2 multiply for two elements
+// (through f32 to bf16 it was five instructions: 101 us against 85 at 16 heads
+// x 4 x <= 120 K keys).  The line of work, the walk along it and the join are
+// shared with the e4m3 kernel.
 //
-// A block's 128 rows take 147 KB as bf16, so there is room for one block and a
-// little: eight 64-column chunks as four pairs (a pair is K's columns for QK
+// A block's 128 rows take 147 KB in 16 bits, so there is room for one block and
+// a little: eight 64-column chunks as four pairs (a pair is K's columns for QK
 // and one 128-column tile of V) in a ring of pairs, and the rotary chunk, which
 // P^T reuses after QK.  PV runs tile by tile and hands each pair back, so the
 // next block streams in behind it:
 //   bf16 cache   TMA loads the pairs; a fifth one ahead where q leaves room.
-//   block scales TMA loads the bytes into a ring of raw chunks (that is what
-//                keeps HBM busy), and the softmax warps, which have nothing else
-//                to do until S is there, multiply and round them into the pairs.
+//   block scales TMA loads the bytes into raw chunks, and the softmax warps,
+//                which have nothing else to do until S is there, multiply and
+//                round them into the pairs: two groups of four warps, each with
+//                the raw slot and the pairs that are its own, so that one
+//                group's waits run beside the other's (one group of eight: 103
+//                us against 88).  Eight more warps for this alone, beside the
+//                softmax, were slower (96-109 us: the registers then spill).
 //
 // Bound: HBM for a bf16 cache and few rows (147 KB a block, 6260 cycles of an
-// SM's share); for block scales the shared memory, which every row passes five
-// times (bytes in and out, bf16 in, QK, PV: 4600 cycles a block against 3530 of
-// HBM).
+// SM's share), its tensor and softmax chain for 64 rows; for block scales the
+// chain of a block, 7.6 k cycles: raw chunks awaited 1.5 k, read 0.6 k, converted
+// and stored 1.7 k, fenced and handed on 1.2 k, pairs awaited 0.5 k, softmax 1.4 k.
+//
+// Measured: 16 heads over 4 x <= 120 K keys, bf16 cache 85 us (5.3 TB/s), block
+// scales 87 us (2.9 TB/s); 8 x 2 tokens x 128 heads over <= 8192 keys, bf16 62 us
+// (510 TFLOP/s), block scales 104 us.  (The prefill kernel's form with one block
+// in flight: 142, 179, 85 and 115 us.)
 //
 // Warps: 0-7 conversion, softmax and epilogue (thread = one key x NR/2 rows),
 // 8 TMA, 9 QK, 10 PV.
@@ -41,7 +51,7 @@ namespace dw {
 using namespace dd;
 
 constexpr int kChunk = kBK * 128;  // 64 columns of a block in bf16 (128 in e4m3)
-constexpr int kItemCost = 4;       // an item's fixed cost, in blocks
+constexpr int kItemCost = 3;       // an item's fixed cost, in blocks
 constexpr float kPOffset = 4.f;    // the largest weight is 2^4 .. 2^12
 constexpr float kTinyLg = -60.f;   // rows of smaller scales take their sums from the logits
 

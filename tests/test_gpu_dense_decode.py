@@ -315,3 +315,14 @@ def test_rows_of_tiny_scale_ahead_of_the_others(qd, mode, tiny):
     scales[rows] = tiny
     got = _run(seqs, q, pool, scales, sbs, 700)
     assert bool((got.float().abs() <= 1e-33).all())
+
+
+@pytest.mark.parametrize("qd,mode", [("e4m3", "block"), ("bf16", "bf16"), ("bf16", "row"), ("e4m3", "unit")])
+@pytest.mark.parametrize("q_lens,kv_lens,H,page", [SHAPES[4], SHAPES[6], SHAPES[7], ([1] * 5, [4000 + i for i in range(5)], 128, 32)])
+def test_forty_calls_give_the_same_bits(qd, mode, q_lens, kv_lens, H, page):
+    """Ring slots that are handed back too early, or seen a phase early, show
+    as results that differ from call to call."""
+    s, seqs, q, pool, scales, sbs, val = _case(q_lens, kv_lens, H, qd, mode, page, seed=19)
+    first = _run(seqs, q, pool, scales, sbs, max(kv_lens))
+    for _ in range(40):
+        assert torch.equal(_run(seqs, q, pool, scales, sbs, max(kv_lens)), first)
