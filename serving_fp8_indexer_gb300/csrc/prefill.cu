@@ -369,10 +369,6 @@ __device__ __forceinline__ int seq_of(const Params& p, int t) {
 template <int KEYS>
 __device__ __forceinline__ int token_keys(const Params& p, int t, int& b) {
   if (KEYS == kCausal) {
-    if (t >= p.cu_q[p.B]) {  // behind the last sequence: nothing to compute, nothing to write
-      b = 0;
-      return -1;
-    }
     b = seq_of(p, t);
     const int q_len = p.cu_q[b + 1] - p.cu_q[b];
     const int n = p.kv_len[b] - q_len + (t - p.cu_q[b]) + 1;
@@ -401,7 +397,7 @@ __device__ __forceinline__ Item item_make(const Params& p, int w, int groups, in
   it.hv = min(kNH, p.H - it.h0);
   it.n = n;
   it.b = b;
-  const int nb = (n + kBK - 1) / kBK;  // 0 for n = -1
+  const int nb = (n + kBK - 1) / kBK;
   const int per = (nb + p.nsplit - 1) / p.nsplit;
   it.j0 = min(nb, it.s * per);
   it.nblk = min(nb, it.j0 + per) - it.j0;
@@ -591,9 +587,8 @@ __global__ void __launch_bounds__(threads_for(KVP), 1)
       if (nblk == 0) {
         // nothing to attend to: zeros (no softmax mass), or for a split an
         // empty partial (log-sum-exp -inf, which the combine skips); the QK
-        // warp skips the item.  A token outside the batch keeps its output.
-        if (n < 0) {
-        } else if (p.nsplit > 1) {
+        // warp skips the item
+        if (p.nsplit > 1) {
           if (threadIdx.x < I.hv) p.part_lse[part_row() + threadIdx.x] = -INFINITY;
         } else {
           for (int i = threadIdx.x; i < I.hv * kDV / 8; i += kSoftThreads)
