@@ -27,7 +27,8 @@
 // A row's reference m is raised only when a block exceeds it by more than
 // 2^8 (P <= 256; bf16 P keeps its relative precision), so O is rescaled
 // rarely.  l sums the f32 weights before their rounding to bf16; that
-// rounding (2^-9 relative, random) is the only one beside the output's.
+// rounding (2^-8 relative at most, random) is the only one beside the output's,
+// and as large; calls of a few rows carry P as two terms instead.
 //
 // Warps: 0-3 softmax of tile A, 4-7 of tile B (thread = row = TMEM lane, no
 // exchange between threads), 8 TMA, 9 MMA issue and TMEM, 10 the V tail.  One
@@ -38,12 +39,14 @@
 // When one wave of (tile, head) items leaves SMs idle, the keys are split
 // over grid.z and a second kernel joins the partial results.
 //
-// Measured: 4096 tokens x 128 heads 471 us (1460 TFLOP/s, 0.76 of the measured
-// bf16 rate), 8192 x 16 heads 208 us (0.86), 1025 tokens over 6100 keys in four
-// sequences x 32 heads 238 us (0.69).  What bounds it: a pair of blocks takes
-// about 3400 cycles for 2560 of tensor time, and 2700 of them are the
-// shared-memory traffic of the operands (Q and K twelve times 8 KB a tile, V,
-// and the TMA writes); then a CTA's start and epilogue, 8-10 k cycles.
+// Measured: 4096 tokens x 128 heads 440 us (1560 TFLOP/s, 0.81 of the measured
+// bf16 rate), 8192 x 16 heads 201 us (0.89), 1025 tokens over 6100 keys in four
+// sequences x 32 heads 230 us (0.71).  What bounds it: the shared-memory traffic
+// of the operands (Q and K twelve times 8 KB a tile, V, and the TMA writes: 2700
+// cycles a pair of blocks beside 2560 of tensor time), the issue of the MMAs
+// (ring slots taken from a loop instead of unrolled: 500 us; the waits' polling
+// loops unrolled, which filled the instruction cache: 467), then a CTA's start
+// and epilogue, 8-10 k cycles.
 #include <algorithm>
 #include <cstddef>
 
@@ -68,6 +71,7 @@ constexpr uint32_t kTmemO = 256;          // O_A, O_B after S_A, S_B
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTau = 8.f;
+constexpr int kTwoTermRows = 64;
 constexpr int kLaunchRegs = 168, kSoftRegs = 208, kOtherRegs = 80;
 static_assert(kSoftThreads * kSoftRegs + (kThreads - kSoftThreads) * kOtherRegs <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
@@ -138,6 +142,8 @@ __device__ __forceinline__ Work work_of(const Params& p, int b, int tile) {
   return w;
 }
 
+// kTwo: P as two bf16 terms (hi + lo, side by side over S's columns).
+template <bool kTwo>
 __global__ void __launch_bounds__(kThreads, 1)
     expanded_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tr, const __grid_constant__ CUtensorMap tv, const Params p) {
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 c2 = make_float2(p.c, p.c), n2 = make_float2(neg, neg);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        uint32_t pk[32];
+        uint32_t pk[32], pl[kTwo ? 32 : 1];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const int q = hf * 2 + (e >> 4), a = (e & 15) * 2;
@@ -301,8 +307,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           l2[e & 1] = add2(l2[e & 1], w2);
           const __nv_bfloat162 b2 = __floats2bfloat162_rn(w2.x, w2.y);
           pk[e] = *reinterpret_cast<const uint32_t*>(&b2);
+          if constexpr (kTwo) {
+            const float2 r = __bfloat1622float2(b2);
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(w2.x - r.x, w2.y - r.y);
+            pl[e] = *reinterpret_cast<const uint32_t*>(&lo);
+          }
         }
         tmem_st32(ts + 32 * hf, pk);
+        if constexpr (kTwo) tmem_st32(ts + kBN / 2 + 32 * hf, pl);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(smem_u32(&s.bar_p[x][hf]));  // PV starts on the first 64 keys
@@ -494,6 +506,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ks = h * 4 + kk;  // 16 keys: 8 columns of P, 16 rows of V
             mma_f16_ts(tmem + kTmemO + x * kDV, tmem + x * kBN + ks * 8,
                        b + static_cast<uint64_t>((ks * 16 * 128) >> 4), IDESC_PV, (j > 0 || ks > 0) ? 1u : 0u);
+            if (kTwo)
+              mma_f16_ts(tmem + kTmemO + x * kDV, tmem + x * kBN + kBN / 2 + ks * 8,
+                         b + static_cast<uint64_t>((ks * 16 * 128) >> 4), IDESC_PV, 1u);
           }
         }
         if (done) mma_commit(smem_u32(&s.bar_v_empty[sl]));
@@ -640,8 +655,15 @@ smla_status_t launch_expanded(const ExpandedArgs& a, unsigned* err, cudaStream_t
   const size_t smem = sizeof(Smem);
   static_assert(sizeof(Smem) <= 232448, "shared memory exceeds a CTA's 227 KB");
   static_assert(offsetof(Smem, k) % 1024 == 0 && offsetof(Smem, v) % 1024 == 0, "swizzled tiles need 1024-byte alignment");
-  static std::atomic<unsigned long long> ready{0};
-  const smla_status_t st = prepare_kernel(reinterpret_cast<const void*>(expanded_kernel), smem, kLaunchRegs, ready,
+  // A call of a few rows in all takes P as two terms: its rounding would show
+  // beside the output's (1.4 times the error against 64 bits, and up to 1.5 in
+  // single rows, where it averages over few elements), and the time is mostly
+  // the launch (1 row of 4000 keys 14 -> 17 us).  With many rows it would cost a
+  // third (32 tokens x 128 heads over 4 x 8000 keys 334 -> 450 us).
+  const bool two = static_cast<int64_t>(a.T) * a.H <= kTwoTermRows;
+  const auto kernel = two ? expanded_kernel<true> : expanded_kernel<false>;
+  static std::atomic<unsigned long long> ready[2];
+  const smla_status_t st = prepare_kernel(reinterpret_cast<const void*>(kernel), smem, kLaunchRegs, ready[two],
                                           "expanded kernel");
   if (st != SMLA_OK) return st;
   p.slots = static_cast<int>(expanded_slots(a.T, a.B));
@@ -657,7 +679,7 @@ smla_status_t launch_expanded(const ExpandedArgs& a, unsigned* err, cudaStream_t
   if (ctas > 0x7fffffff || static_cast<int64_t>(p.slots) * p.head_group > 0x7fffffff)
     return fail(SMLA_ERR_UNSUPPORTED, "expanded prefill: too many tiles (T=%d, B=%d, H=%d)", a.T, a.B, a.H);
   const dim3 grid(static_cast<unsigned>(ctas), 1, static_cast<unsigned>(a.nsplit));
-  expanded_kernel<<<grid, kThreads, smem, stream>>>(tq, tk, tr, tv, p);
+  kernel<<<grid, kThreads, smem, stream>>>(tq, tk, tr, tv, p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "expanded launch");
   if (a.nsplit > 1) {

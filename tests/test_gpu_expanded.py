@@ -232,3 +232,16 @@ def test_bad_key_offsets_are_reported():
     with pytest.raises(smla.SmlaError) as e:
         smla.check_device_errors()
     assert e.value.status == 5
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,H", [([1], [5000], 1), ([3, 2], [900, 40], 8), ([64], [64], 1),
+                                              ([16], [300], 4), ([2, 2, 1], [212, 130, 180], 1)])
+def test_calls_of_few_rows_round_only_the_output(q_lens, kv_lens, H):
+    """P in two terms is off by 2^-16 of a weight, a hundredth of the output's
+    rounding (2^-8 / sqrt(3) of an element, root mean square): beside the exact
+    result rounded to bf16 the error may grow by a tenth at most."""
+    q, kv, kr, cu_q, cu_kv = _inputs(q_lens, kv_lens, H, seed=21)
+    ref, _, tol = _reference(q, kv, kr, q_lens, kv_lens)
+    got = _run(q, kv, kr, cu_q, cu_kv)
+    _close(got, ref, tol)
+    assert float((got.double() - ref).norm()) <= 1.1 * float((ref.bfloat16().double() - ref).norm())
