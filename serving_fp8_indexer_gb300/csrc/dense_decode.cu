@@ -32,9 +32,9 @@
 // at NR = 64 (2688 cycles), where the shared-memory reads of N = 64 operands
 // set their rate (48 cycles an MMA).
 //
-// Measured: 16 heads over 4 x <= 120 K keys 50 us (4.5 TB/s; 6.2 while the line
+// Measured: 16 heads over 4 x <= 120 K keys 49 us (4.6 TB/s; 6.2 while the line
 // runs, then 6 us of start and 5.7 of join); 8 x 2 tokens x 128 heads over <= 8192
-// keys 48 us (653 TFLOP/s): 3.9 k cycles a block for the chain load 3 k, QK 1.5 k,
+// keys 47 us (670 TFLOP/s): 3.9 k cycles a block for the chain load 3 k, QK 1.5 k,
 // softmax 2.4 k, PV 2.4 k over two slots, 12 k cycles of start, 7.7 us of join.
 //
 // Warps: 0-7 softmax and epilogue (thread = one key x NR/2 rows), 8 TMA, 9 QK,

@@ -30,12 +30,12 @@
 //
 // Bound: HBM for a bf16 cache and few rows (147 KB a block, 6260 cycles of an
 // SM's share), its tensor and softmax chain for 64 rows; for block scales the
-// chain of a block, 7.6 k cycles: raw chunks awaited 1.5 k, read 0.6 k, converted
-// and stored 1.7 k, fenced and handed on 1.2 k, pairs awaited 0.5 k, softmax 1.4 k.
+// chain of a block, about 6.5 k cycles, of which raw chunks awaited 1.5 k, read
+// 0.6 k, converted and stored 1.7 k, fenced and handed on 1.2 k, softmax 1.4 k.
 //
 // Measured: 16 heads over 4 x <= 120 K keys, bf16 cache 85 us (5.3 TB/s), block
-// scales 87 us (2.9 TB/s); 8 x 2 tokens x 128 heads over <= 8192 keys, bf16 62 us
-// (510 TFLOP/s), block scales 104 us.  (The prefill kernel's form with one block
+// scales 77 us (3.3 TB/s); 8 x 2 tokens x 128 heads over <= 8192 keys, bf16 60 us
+// (527 TFLOP/s), block scales 87 us.  (The prefill kernel's form with one block
 // in flight: 142, 179, 85 and 115 us.)
 //
 // Warps: 0-7 conversion, softmax and epilogue (thread = one key x NR/2 rows),
