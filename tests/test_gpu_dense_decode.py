@@ -77,6 +77,8 @@ def _reference(s, q, val, srow, sink=None, block=False):
         k = val[rows]
         for t in range(int(s.cu_q[b]), int(s.cu_q[b + 1])):
             n = int(s.kv_len[b]) - int(s.cu_q[b + 1]) + t + 1
+            if n <= 0:  # nothing to attend to: zeros
+                continue
             z = SCALE * q64[t] @ k[:n].T
             if sink is not None:
                 z = torch.cat([z, sink.double()[:, None]], 1)
@@ -326,3 +328,31 @@ def test_forty_calls_give_the_same_bits(qd, mode, q_lens, kv_lens, H, page):
     first = _run(seqs, q, pool, scales, sbs, max(kv_lens))
     for _ in range(40):
         assert torch.equal(_run(seqs, q, pool, scales, sbs, max(kv_lens)), first)
+
+
+@pytest.mark.parametrize("qd,mode", MODES)
+@pytest.mark.parametrize("H,page", [(192, 4096), (256, 8), (48, 32)])
+def test_more_heads_and_extreme_pages(qd, mode, H, page):
+    s, seqs, q, pool, scales, sbs, val = _case([1, 3], [777, 1500], H, qd, mode, page, seed=20)
+    ref, tol = _reference(s, q, val, **_carried(scales, pool))
+    for most in (1500, 1):
+        _close(_run(seqs, q, pool, scales, sbs, most), ref, tol)
+
+
+@pytest.mark.parametrize("qd,mode", MODES)
+def test_one_captured_call_serves_growing_lengths(qd, mode):
+    """The grid is chosen from max_kv_len at the capture; lengths beyond it and
+    empty sequences are served by the same graph."""
+    s, seqs, q, pool, scales, sbs, val = _case([1, 2, 1], [2000, 1200, 300], 32, qd, mode, seed=22)
+    n = smla.dense_decode_workspace_size(4, 32, 500)
+    ws = torch.full((max(n, 16),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.zeros((4, 32, 512), dtype=torch.bfloat16, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        smla.dense_decode(q, pool, scales, sbs, seqs, 500, SCALE, out, ws)
+    for lens in ([5, 130, 0], [2000, 1200, 300], [1, 2, 257]):
+        seqs.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+        s.kv_len = seqs.kv_len.cpu().numpy()
+        g.replay()
+        smla.check_device_errors()
+        _close(out, *_reference(s, q, val, **_carried(scales, pool)))
