@@ -379,7 +379,7 @@ smla_status_t smla_cache_gather(const void* pool, int32_t pool_dtype, int64_t ph
  * queries alone are too few to fill the GPU; contents on entry do not matter,
  * unspecified on return; not shared by calls that may overlap.  The products
  * run as tcgen05 kind::f16 (bf16) MMAs with f32 TMEM accumulation; P is
- * rounded to bf16. */
+ * rounded to bf16 (kept as two bf16 terms where T * H <= 64). */
 size_t smla_expanded_prefill_workspace_size(int32_t T, int32_t S, int32_t B, int32_t H);
 smla_status_t smla_expanded_prefill(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
                                     const uint16_t* k_nope, int64_t k_token_stride, int64_t k_head_stride,

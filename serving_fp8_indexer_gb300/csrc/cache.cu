@@ -14,7 +14,7 @@
 // A few rows (a decode step) cost a launch and the chain cu_q -> page -> row:
 // 16 rows of 576 are written in 3.3 us, 257 read in 2.6.  For many rows the
 // append is bound by instruction issue (12 117 rows of 576 with block scales
-// and rows_out: 771 warp instructions a row, issue slots 59 % busy, 13.7 us
+// and rows_out: 771 warp instructions a row, issue slots 59 % busy, 13.0 us
 // against 5.3 of HBM time), the gather by HBM (8 sequences, 49 K rows: 16.8 us,
 // 5.0 TB/s).  The angles come from integer phases: in float64 they were the
 // append's bound (27 us).
@@ -62,9 +62,10 @@ __device__ __forceinline__ float scale_of(float amax) {
   return amax > 0.f ? fmaxf(amax / kE4m3Max, 1.17549435e-38f) : 1.f;
 }
 
-// kSlots: 8-element chunks a lane holds.
+// kSlots: 8-element chunks a lane holds.  Ten CTAs an SM (48 registers instead
+// of 64) hide more of the rows' latency, 13.5 -> 13.0 us; four slots would spill.
 template <int MODE, int kSlots>
-__global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(32 * kWarps, kSlots <= 3 ? 10 : 1) append_kernel(const AppendParams p) {
   // the rotary angles' cos and sin, for each warp its token's
   extern __shared__ float2 s_cs[];
   const int lane = threadIdx.x & 31;
