@@ -234,10 +234,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           seen |= u[c].x;
         }
         // The raw chunk goes back once the reads have returned.  The arrival takes
-        // their values (times a 0 that the compiler does not know): one that only
-        // follows them in the program may overtake them while the tensor cores
-        // keep shared memory busy, and TMA then writes what is still to be read.
-        warp_arrive((nope ? smem_u32(&s.bar_raw_empty[rs]) : smem_u32(&s.bar_raw_rope_empty)) + (seen & nil), lane);
+        // every lane's values (against a 0 that the compiler does not know): one
+        // that only follows the reads in the program may overtake them while the
+        // tensor cores keep shared memory busy, and TMA then writes what is still
+        // to be read.
+        const uint32_t none = __any_sync(0xffffffffu, (seen & nil) != 0) ? 8u : 0u;  // 0
+        warp_arrive((nope ? smem_u32(&s.bar_raw_empty[rs]) : smem_u32(&s.bar_raw_rope_empty)) + none, lane);
         fine = (nope ? mbar_wait(smem_u32(&s.bar_pair_empty[sl]), ((n / kPairs) & 1) ^ 1, p.err)
                      : mbar_wait(smem_u32(&s.bar_rope_empty), (i & 1) ^ 1, p.err)) && fine;
 #pragma unroll
