@@ -393,8 +393,14 @@ smla_status_t smla_expanded_prefill(const uint16_t* q, int64_t q_token_stride, i
  * the whole cache of their sequence: out[t,h] as for smla_dense_prefill, with
  *   - the keys of a token divided among several CTAs when the tokens are too
  *     few to fill the GPU, and the partial results merged by a second kernel;
- *   - q, and the weights P, carried at bf16's accuracy whatever q's type
- *     (smla_dense_prefill and the sparse calls round P to one e4m3 term for e4m3 q);
+ *   - the weights P carried at bf16's accuracy whatever q's type: each is off by
+ *     at most 2^-8 of itself, or by 2^-28 of its row's largest where that is more
+ *     (of p_j s_j, s_j the row's scale), so that the many keys far below a
+ *     dominant one keep their weight.  (smla_dense_prefill and the sparse calls
+ *     round P to one e4m3 term for e4m3 q, and to two, which end 2^-14 below a
+ *     row's largest, for bf16 q.)  bf16 q is exact down to 2^-9 of its row's
+ *     largest element over an e4m3 cache, smaller elements are off by up to 2^-17
+ *     of that, and exact over a bf16 cache;
  *   - e4m3 caches in every scale mode, or a bf16 cache.
  *   q            [T, H, 576], bf16 or e4m3 (q_dtype)
  *   latent_pool  [phys_rows, 576], e4m3 or bf16 (pool_dtype)

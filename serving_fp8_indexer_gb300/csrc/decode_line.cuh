@@ -17,9 +17,13 @@ constexpr uint32_t kTmemCols = 512, kTmemS = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 // The reference of a row's weights P = p * scale counts no scale as smaller than
 // 2^kLeastLg: the sums of p itself stay finite where a block's rows all have
-// scale 0 or almost (values below 2^-96 are then not told from 0).
-constexpr float kLeastLg = -96.f;
-constexpr float kTau = 8.f;  // a row's reference is raised when a block exceeds it by more than 2^8
+// scale 0 or almost (values below 2^-88 are then not told from 0).
+constexpr float kLeastLg = -88.f;
+// A row's largest weight is kept at 2^11 .. 2^15: a block's largest sets the
+// reference to 2^kPOffset below it, and the reference is raised when a later
+// block's exceeds it by more than 2^kTau.  That is the upper end of e5m2 and f16
+// (57344, 65504): what they have below is left to the small weights.
+constexpr float kPOffset = 11.f, kTau = 15.f;
 constexpr int kOrdMin = static_cast<int>(0x80000000u);
 
 struct Cut;

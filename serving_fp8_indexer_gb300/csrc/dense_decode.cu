@@ -4,10 +4,17 @@
 // Orientation and precision are those of the prefill attention kernel: keys
 // are the MMA M dimension and query rows the N dimension,
 //   S^T[128 keys x NR rows] = K . Q^T,   O^T[512 x NR] += V^T . P^T,
-// all on the FP8 pipe, with bf16 q and the weights P as two e4m3 terms (hi +
-// lo), so that the e4m3 cache rows are used as they lie in memory.  What is
-// different here:
+// all on the FP8 pipe, with bf16 q as two e4m3 terms (hi + lo), so that the e4m3
+// cache rows are used as they lie in memory.  What is different here:
 //
+// * Weights.  A cache is long: thousands of keys far below one that dominates
+//   still hold much of the weight between them, and each has to be carried to
+//   the same relative accuracy.  P is three e5m2 terms (3 bits each, 2^-9 of a
+//   weight together), whose range of 32 binary places keeps eight bits down to
+//   2^-19 of a row's largest weight (13 nats) and something down to 2^-28.  (Two
+//   e4m3 terms, as in the prefill kernel, end 2^-14 below the largest: a key 10
+//   nats above 32 K others left an eighth of their weight.  46.8 us at 64 rows
+//   then, where the third term is a pass of its own; no difference at 16.)
 // * Rows.  An item is up to NR rows (tokens x heads) of one sequence that
 //   share every key: up to NR / H consecutive tokens of a sequence when H <
 //   64, or 64 of one token's heads.  NR is 16, 32 or 64, so that a few heads
@@ -23,19 +30,21 @@
 //   address them.  Columns 0..511 lie in four 128-byte-swizzled chunks (each
 //   the K-major QK operand and, read MN-major, one 128-column tile of V), the
 //   rotary part in a 64-byte-swizzled one, which P^T reuses after QK.
-// * For NR < 64, P's hi and lo are one operand of 2 NR columns with an
-//   accumulator each (summed at the end): half the MMAs.  With NR = 64 there
-//   is no TMEM for that, and PV runs twice into one accumulator.
+// * For NR < 64, P's three terms are one operand of 3 NR columns with an
+//   accumulator each (summed at the end): a third of the MMAs.  With NR = 64
+//   there is no TMEM for that, and PV runs three times into one accumulator; the
+//   second and third product of a tile keep its V operand in the tensor core
+//   (55.7 -> 54.2 us).
 //
 // Bound: HBM for few rows (a block of 73.7 KB is 3140 cycles of an SM's share
-// of 6.8 TB/s; its MMAs 1360 cycles at NR = 16, 1632 at 32), the tensor cores
-// at NR = 64 (2688 cycles), where the shared-memory reads of N = 64 operands
-// set their rate (48 cycles an MMA).
+// of 6.8 TB/s; its MMAs about 1430 cycles at NR = 16, 1760 at 32), at NR = 64 the
+// chain load -> QK -> softmax -> PV over two slots (tensor time about 3200 cycles
+// a block, where the shared-memory reads of N = 64 operands set the rate: 48
+// cycles an MMA, 32 with A kept).
 //
 // Measured: 16 heads over 4 x <= 120 K keys 49 us (4.6 TB/s; 6.2 while the line
-// runs, then 6 us of start and 5.7 of join); 8 x 2 tokens x 128 heads over <= 8192
-// keys 47 us (670 TFLOP/s): 3.9 k cycles a block for the chain load 3 k, QK 1.5 k,
-// softmax 2.4 k, PV 2.4 k over two slots, 12 k cycles of start, 7.7 us of join.
+// runs, then 6 us of start and 5.7 of join), 32 heads 54; 8 x 2 tokens x 128 heads
+// over <= 8192 keys 54 us (580 TFLOP/s).
 //
 // Warps: 0-7 softmax and epilogue (thread = one key x NR/2 rows), 8 TMA, 9 QK,
 // 10 PV.
@@ -52,7 +61,8 @@ constexpr int kChunk = kBK * 128;        // 128 columns of a block
 constexpr int kRopeOff = 4 * kChunk;     // columns 512..575: [128][64 bytes]
 constexpr int kSlot = kRopeOff + kBK * 64;
 constexpr int kNST = 2;                  // block slots
-constexpr float kPOffset = 4.f;  // the largest weight is 2^4 .. 2^8 (two-term e4m3's best range)
+constexpr int kHalf = kBK / 2;           // keys that one PV step of the pipeline takes
+constexpr int kPRow = kBK * 64;          // a term of P^T, 64 bytes a key
 // An item's first blocks cost their CTA more than the blocks themselves (its q
 // is loaded and split, its result reduced and stored): the line counts that as
 // this many blocks.
@@ -62,7 +72,10 @@ template <int NR, int QP>
 struct Smem {
   uint8_t q[QP * NR * kD];  // [4][QP * NR rows][128] then [QP * NR][64]: hi rows, then lo rows
   uint8_t kv[kNST][kSlot];
-  uint8_t plo[NR == 64 ? kBK * 64 : 16];
+  // What P's first place (the rotary chunk of the block's slot) does not hold.
+  // NR = 64: the second and third term of half a block's keys; 32: the third
+  // term, a place for each slot.
+  uint8_t pmore[NR == 64 ? kPRow : NR == 32 ? kNST * kPRow : 16];
   alignas(16) float cs[NR];    // softmax_scale * log2(e) / 2^e per row
   alignas(16) float negm[NR];  // minus the reference, log2 units
   float delta[NR], fac[NR];
@@ -70,16 +83,27 @@ struct Smem {
   float sums[4][NR];           // row sums of each quarter of the key lanes
   int nk[NR];                  // keys each row sees
   unsigned long long bar_qraw, bar_q, bar_full[kNST], bar_empty[kNST][2];
-  unsigned long long bar_s[2], bar_s_free[2], bar_p[2][2], bar_pv[2], bar_drain[2];
+  unsigned long long bar_s[2], bar_s_free[2], bar_p[2][2], bar_more[2], bar_pv[2], bar_drain[2];
   uint32_t tmem_base;
 };
 
 // Two floats -> e4m3 hi and lo pairs, through f16 (|x| <= 448): hi = e4m3(x),
-// lo = e4m3(x - hi), the difference exact in f16.
+// lo = e4m3(x - hi), the difference exact in f16.  A bf16 query's eight bits fit
+// both, down to 2^-9 of its row's largest value.
 __device__ __forceinline__ void split2(float a, float b, uint16_t& hi, uint16_t& lo) {
   const uint32_t h = f32x2_to_f16x2(a, b);
   hi = f16x2_to_e4m3x2(h);
   lo = f16x2_to_e4m3x2(hsub2(h, e4m3x2_to_f16x2(hi)));
+}
+// Two weights (0 .. 2^15) -> three e5m2 terms each, through f16, every difference
+// exact there: off by 2^-3 of 2^-3 of 2^-3, and 2^-11 for the f16, of the weight,
+// or by half of e5m2's smallest step, 2^-17.
+__device__ __forceinline__ void split3(float a, float b, uint16_t& t1, uint16_t& t2, uint16_t& t3) {
+  uint32_t h = f32x2_to_f16x2(a, b);
+  t1 = f16x2_to_e5m2x2(h);
+  h = hsub2(h, e5m2x2_to_f16x2(t1));
+  t2 = f16x2_to_e5m2x2(h);
+  t3 = f16x2_to_e5m2x2(hsub2(h, e5m2x2_to_f16x2(t2)));
 }
 
 template <int NR, int QP, bool ROWSCALE>
@@ -89,11 +113,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Smem<NR, QP>;
   constexpr int kQN = QP * NR;                 // QK's N
   constexpr int kQChunk = kQN * 128;           // a 128-column chunk of Q
-  constexpr int kPasses = NR == 64 ? 2 : 1;    // PV passes (hi, lo)
-  constexpr int kPN = NR == 64 ? 64 : 2 * NR;  // PV's N
+  constexpr int kParts = NR == 64 ? 1 : 3;     // accumulators of a V tile: one for each term, or one for all
+  constexpr int kPN = kParts * NR;             // PV's N
+  constexpr uint32_t kS = NR == 32 ? 384 : kTmemS;  // S's columns, behind O's
   constexpr int NC = NR / 2;                   // rows of a softmax thread
-  static_assert(offsetof(S, kv) % 1024 == 0 && offsetof(S, plo) % 1024 == 0, "swizzled tiles need 1024-byte alignment");
-  static_assert(4 * kPN <= static_cast<int>(kTmemS) && 2 * kQN <= static_cast<int>(kTmemCols - kTmemS), "TMEM budget");
+  static_assert(offsetof(S, kv) % 1024 == 0 && offsetof(S, pmore) % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+  static_assert(4 * kPN <= static_cast<int>(kS) && 2 * kQN <= static_cast<int>(kTmemCols - kS), "TMEM budget");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (smem_u32(smem_raw) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrShape);
@@ -115,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&s.bar_s_free[i]), kSoftWarps);
       mbar_init(smem_u32(&s.bar_p[i][0]), kSoftWarps / 2);
       mbar_init(smem_u32(&s.bar_p[i][1]), kSoftWarps / 2);
+      mbar_init(smem_u32(&s.bar_more[i]), kSoftWarps / 2);
       mbar_init(smem_u32(&s.bar_pv[i]), 1);
       mbar_init(smem_u32(&s.bar_drain[i]), 1);
     }
@@ -297,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         float y[NC];
         {
-          const uint32_t a = tmem + lanes + kTmemS + buf * kQN + hb;
+          const uint32_t a = tmem + lanes + kS + buf * kQN + hb;
           uint32_t v0[NC], v1[NC];
           tmem_issue_ld(a, v0);
           if (QP == 2) tmem_issue_ld(a + NR, v1);
@@ -324,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < NC; ++h) ymax = fmaxf(ymax, y[h]);
         if (named_bar_or(1, kSoftThreads, late || j == 0 || ymax + lgc > kTau)) {
           if (named_bar_or(1, kSoftThreads, late)) { ok = false; break; }
-          // Rows whose largest exceeds their reference by 2^8 (all of them in
+          // Rows whose largest exceeds their reference by 2^15 (all of them in
           // the first block) get a new one, and their sums and O^T columns
           // are rescaled.
           int mine = kOrdMin;
@@ -356,7 +382,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = 0; h < NC; ++h) lv[h] *= s.fac[hb + h];
             if (!named_bar_and(1, kSoftThreads, wait_pv(i - 1))) { ok = false; break; }
             tc_fence_after();
-            constexpr int kParts = kPN / NR;  // hi (and lo) accumulators
 #pragma unroll 1
             for (int part = 0; part < 4 * kParts; ++part) {
               const uint32_t a = tmem + lanes + (part / kParts) * kPN + (part % kParts) * NR + hb;
@@ -376,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_bar_sync(1, kSoftThreads);  // all lanes are rescaled before any P is published
           }
         }
-        // ---- P^T row r, this thread's rows, as hi + lo; row sums
+        // ---- P^T row r, this thread's rows, in three terms; row sums
         // The sums take the weights themselves, P / scale; where the scale is 0
         // or so small that P may have underflowed (P = 2^(y + lg) has 122 binary
         // places), from the logits instead.
@@ -387,35 +412,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < NC; ++h) lv[h] += ex2_approx(y[h]);
         }
         uint8_t* p_row = s.kv[slot] + kRopeOff;
-        uint16_t hi[NC / 2], lo[NC / 2];
+        uint16_t t1[NC / 2], t2[NC / 2], t3[NC / 2];
 #pragma unroll
         for (int k = 0; k < NC / 2; ++k) {
           const float a = ex2_approx(ROWSCALE ? y[2 * k] + lg : y[2 * k]);
           const float b = ex2_approx(ROWSCALE ? y[2 * k + 1] + lg : y[2 * k + 1]);
           lv[2 * k] = ROWSCALE ? fmaf(a, isr, lv[2 * k]) : lv[2 * k] + a;
           lv[2 * k + 1] = ROWSCALE ? fmaf(b, isr, lv[2 * k + 1]) : lv[2 * k + 1] + b;
-          split2(a, b, hi[k], lo[k]);
+          split3(a, b, t1[k], t2[k], t3[k]);
         }
         auto pack = [](const uint16_t* h) { return static_cast<uint32_t>(h[0]) | static_cast<uint32_t>(h[1]) << 16; };
+        auto pack4 = [&](const uint16_t* h) { return make_uint4(pack(h), pack(h + 2), pack(h + 4), pack(h + 6)); };
         if constexpr (NR == 64) {
-          // 32 bytes of hi in the slot's rope chunk (read by QK, now dead);
-          // lo's own buffer is free once the previous PV is done with it
+          // the first term in the slot's rotary chunk (read by QK, now dead)
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            *reinterpret_cast<uint4*>(p_row + sw64(r, (hb >> 4) + c)) =
-                make_uint4(pack(hi + 8 * c), pack(hi + 8 * c + 2), pack(hi + 8 * c + 4), pack(hi + 8 * c + 6));
-          if (i > 0) wait_pv(i - 1);
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            *reinterpret_cast<uint4*>(s.plo + sw64(r, (hb >> 4) + c)) =
-                make_uint4(pack(lo + 8 * c), pack(lo + 8 * c + 2), pack(lo + 8 * c + 4), pack(lo + 8 * c + 6));
+          for (int c = 0; c < 2; ++c) *reinterpret_cast<uint4*>(p_row + sw64(r, (hb >> 4) + c)) = pack4(t1 + 8 * c);
         } else if constexpr (NR == 32) {
-          *reinterpret_cast<uint4*>(p_row + sw64(r, hb >> 4)) = make_uint4(pack(hi), pack(hi + 2), pack(hi + 4), pack(hi + 6));
-          *reinterpret_cast<uint4*>(p_row + sw64(r, 2 + (hb >> 4))) =
-              make_uint4(pack(lo), pack(lo + 2), pack(lo + 4), pack(lo + 6));
+          // (the third's place was last read by PV(i - 2), which has completed)
+          *reinterpret_cast<uint4*>(p_row + sw64(r, hb >> 4)) = pack4(t1);
+          *reinterpret_cast<uint4*>(p_row + sw64(r, 2 + (hb >> 4))) = pack4(t2);
+          *reinterpret_cast<uint4*>(s.pmore + slot * kPRow + sw64(r, hb >> 4)) = pack4(t3);
         } else {
-          *reinterpret_cast<uint2*>(p_row + sw64(r, 0) + hb) = make_uint2(pack(hi), pack(hi + 2));
-          *reinterpret_cast<uint2*>(p_row + sw64(r, 1) + hb) = make_uint2(pack(lo), pack(lo + 2));
+          *reinterpret_cast<uint2*>(p_row + sw64(r, 0) + hb) = make_uint2(pack(t1), pack(t1 + 2));
+          *reinterpret_cast<uint2*>(p_row + sw64(r, 1) + hb) = make_uint2(pack(t2), pack(t2 + 2));
+          *reinterpret_cast<uint2*>(p_row + sw64(r, 2) + hb) = make_uint2(pack(t3), pack(t3 + 2));
         }
         if (edge && key >= n_item) {
           // nobody's key: whatever lies there must not meet a weight of 0
@@ -424,7 +444,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        warp_arrive(smem_u32(&s.bar_p[i & 1][(warp & 3) >> 1]), lane);
+        const int half = (warp & 3) >> 1;  // of the block's keys
+        warp_arrive(smem_u32(&s.bar_p[i & 1][half]), lane);
+        if constexpr (NR == 64) {
+          // The other two terms of 64 keys have one place, which each half takes in
+          // its turn: the first once the block before has been read, the second
+          // once the first half has (8 KB more for both do not fit).
+          if (half == 0) {
+            if (i > 0) wait_pv(i - 1);
+          } else {
+            mbar_wait(smem_u32(&s.bar_empty[slot][0]), (i / kNST) & 1, p.err);
+          }
+          const int kr = r & (kHalf - 1);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            *reinterpret_cast<uint4*>(s.pmore + sw64(kr, (hb >> 4) + c)) = pack4(t2 + 8 * c);
+            *reinterpret_cast<uint4*>(s.pmore + kPRow / 2 + sw64(kr, (hb >> 4) + c)) = pack4(t3 + 8 * c);
+          }
+          fence_proxy_async_smem();
+          warp_arrive(smem_u32(&s.bar_more[half]), lane);
+        }
       }
       if (!ok) break;
       gb += g.nb;
@@ -477,18 +516,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t a = tmem + lanes + tile * kPN + hb;
 #pragma unroll
           for (int c = 0; c < NC; c += 8) {
-            uint32_t v0[8], v1[8];
-            tmem_issue_ld(a + c, v0);
-            if (kPN > NR) tmem_issue_ld(a + NR + c, v1);
+            uint32_t v[kParts][8];
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) tmem_issue_ld(a + k * NR + c, v[k]);
             tmem_wait_ld();
-            after_wait(v0);
-            if (kPN > NR) {
-              after_wait(v1);
 #pragma unroll
-              for (int h = 0; h < 8; ++h) o[c + h] = __uint_as_float(v0[h]) + __uint_as_float(v1[h]);
-            } else {
+            for (int k = 0; k < kParts; ++k) after_wait(v[k]);
 #pragma unroll
-              for (int h = 0; h < 8; ++h) o[c + h] = __uint_as_float(v0[h]);
+            for (int h = 0; h < 8; ++h) {
+              o[c + h] = __uint_as_float(v[kParts - 1][h]);  // the small terms first
+#pragma unroll
+              for (int k = kParts - 2; k >= 0; --k) o[c + h] += __uint_as_float(v[k][h]);
             }
           }
           if (!g.whole) {
@@ -646,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (leader) {
           const uint64_t so = static_cast<uint64_t>(slot * (kSlot >> 4));
-          const uint32_t d = tmem + kTmemS + buf * kQN;
+          const uint32_t d = tmem + kS + buf * kQN;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -673,32 +711,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     Cursor cur = start;
     Seg g;
     const bool leader = elect_one();
-    constexpr uint32_t IDESC = idesc_e4m3_f32(128, kPN, 1, 1);
+    constexpr uint32_t IDESC = idesc_e4m3_e5m2_f32(128, kPN, 1, 1);
     const uint64_t va = make_sdesc(smem_u32(s.kv[0]), kChunk, 1024, kSwizzle128B);
-    const uint64_t ph = make_sdesc(smem_u32(s.kv[0]) + kRopeOff, kBK * 64, 512, kSwizzle64B);
-    const uint64_t pl = make_sdesc(smem_u32(s.plo), kBK * 64, 512, kSwizzle64B);
+    // P^T of each slot.  NR = 32 is 96 columns wide: 64 in the rotary chunk, 32 in
+    // the slot's further place.
+    const auto p_desc = [&](int slot) {
+      const uint32_t a = smem_u32(s.kv[slot]) + kRopeOff;
+      return make_sdesc(a, NR == 32 ? smem_u32(s.pmore) + slot * kPRow - a : kPRow, 512, kSwizzle64B);
+    };
+    const uint64_t p0 = p_desc(0), p1 = p_desc(1);
+    const uint64_t pm = make_sdesc(smem_u32(s.pmore), kPRow, 512, kSwizzle64B);
     int i = 0;
     bool ok = true;
     while (ok && next_seg(p, cur, g)) {
       for (int j = 0; ok && j < g.nb; ++j, ++i) {
         const int slot = i % kNST;
-        const uint64_t so = static_cast<uint64_t>(slot * (kSlot >> 4));
+        const uint64_t vs = va + static_cast<uint64_t>(slot * (kSlot >> 4)), ps = slot ? p1 : p0;
+        // 32 keys (of half h: the kk-th) against a term at pd; `add` to what is there
+        const auto pv = [&](int h, int kk, uint64_t pd, bool add) {
+#pragma unroll
+          for (int tile = 0; tile < 4; ++tile)
+            mma_f8f6f4_ss(tmem + tile * kPN,
+                          vs + static_cast<uint64_t>((tile * kChunk + (h * kHalf + kk * 32) * 128) >> 4), pd, IDESC,
+                          add ? 1u : 0u);
+        };
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_p[i & 1][h]), (i >> 1) & 1, p.err))) { ok = false; break; }
           tc_fence_after();
           if (leader) {
 #pragma unroll
-            for (int ps = 0; ps < kPasses; ++ps)
+            for (int kk = 0; kk < 2; ++kk)
+              pv(h, kk, ps + static_cast<uint64_t>(((h * kHalf + kk * 32) * 64) >> 4), j > 0 || (h | kk));
+          }
+          __syncwarp();
+          if constexpr (NR == 64) {
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_more[h]), i & 1, p.err))) { ok = false; break; }
+            tc_fence_after();
+            if (leader) {
 #pragma unroll
               for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int tile = 0; tile < 4; ++tile) {
-                  const int key = h * 64 + kk * 32;
-                  mma_f8f6f4_ss(tmem + tile * kPN, va + so + static_cast<uint64_t>((tile * kChunk + key * 128) >> 4),
-                                (ps == 0 ? ph + so : pl) + static_cast<uint64_t>((key * 64) >> 4), IDESC,
-                                (j > 0 || (ps | kk | h)) ? 1u : 0u);
-                }
+                for (int tile = 0; tile < 4; ++tile)
+                  mma_f8f6f4_ss_pair(tmem + tile * kPN,
+                                     vs + static_cast<uint64_t>((tile * kChunk + (h * kHalf + kk * 32) * 128) >> 4),
+                                     pm + static_cast<uint64_t>((kk * 32 * 64) >> 4),
+                                     pm + static_cast<uint64_t>((kPRow / 2 + kk * 32 * 64) >> 4), IDESC, 1u);
+            }
+          }
+          if (leader) {
             mma_commit(smem_u32(&s.bar_empty[slot][h]));
             if (h == 1) mma_commit(smem_u32(&s.bar_pv[i & 1]));
           }

@@ -52,7 +52,6 @@ using namespace dd;
 
 constexpr int kChunk = kBK * 128;  // 64 columns of a block in bf16 (128 in e4m3)
 constexpr int kItemCost = 3;       // an item's fixed cost, in blocks
-constexpr float kPOffset = 4.f;    // the largest weight is 2^4 .. 2^12
 constexpr float kTinyLg = -60.f;   // rows of smaller scales take their sums from the logits
 
 template <int NR, bool BLOCK>
@@ -325,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < NC; ++h) ymax = fmaxf(ymax, y[h]);
         if (named_bar_or(1, kSoftThreads, late || j == 0 || ymax + lgc > kTau)) {
           if (named_bar_or(1, kSoftThreads, late)) { ok = false; break; }
-          // Rows whose largest exceeds their reference by 2^8 (all of them in
+          // Rows whose largest exceeds their reference by 2^15 (all of them in
           // the first block) get a new one, and their sums and O^T columns
           // are rescaled.
           int mine = kOrdMin;

@@ -242,6 +242,17 @@ SMLA_DEVICE_INLINE void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// kind::f8f6f4 products of one A with two B's in turn: the first keeps A in the
+// tensor core's operand buffer, the second takes it from there.
+SMLA_DEVICE_INLINE void mma_f8f6f4_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b0, uint64_t b1, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::fill [%0], %1, %2, %4, p;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::lastuse [%0], %1, %3, %4, 1;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b0), "l"(b1), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // D[tmem] (+)= A[tmem] * B[smem]^T, kind::f16 (bf16 x bf16), issued by one
 // thread: A row r is TMEM lane r, two consecutive K elements per column.
 SMLA_DEVICE_INLINE void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -339,6 +350,11 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int a_mn, in
          | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// The same with e5m2 B (format 1).
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2_f32(int M, int N, int a_mn, int b_mn) {
+  return idesc_e4m3_f32(M, N, a_mn, b_mn) | (1u << 10);
+}
+
 // Instruction descriptor for kind::f16 with bf16 A and B, f32 accumulator
 // (same field layout as above; A / B format 1 = bf16).
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, int b_mn) {
@@ -402,6 +418,14 @@ SMLA_DEVICE_INLINE uint16_t f16x2_to_e4m3x2(uint32_t v) {
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
   return r;
 }
+// half2 -> two e5m2 bytes (round to nearest even, saturating), and back: an e5m2
+// value is the f16 whose upper byte it is.
+SMLA_DEVICE_INLINE uint16_t f16x2_to_e5m2x2(uint32_t v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
+  return r;
+}
+SMLA_DEVICE_INLINE uint32_t e5m2x2_to_f16x2(uint16_t v) { return __byte_perm(v, 0, 0x1404); }
 SMLA_DEVICE_INLINE uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
