@@ -65,7 +65,7 @@ struct Smem {
   alignas(1024) uint8_t raw_rope[BLOCK ? kChunk / 2 : 16];
   alignas(16) float negm[NR];  // minus the reference, log2 units
   float delta[NR], fac[NR];
-  int mx[NR];
+  int mx[NR], bad[NR];         // bad: the next segment's row has a query element that is not finite
   float sums[4][NR];
   int nk[NR];
   int part_row[kBK / 8];
@@ -129,7 +129,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&s.bar_pv), 1);
     fence_mbar_init();
   }
-  if (threadIdx.x < NR) s.mx[threadIdx.x] = kOrdMin;
+  if (threadIdx.x < NR) {
+    s.mx[threadIdx.x] = kOrdMin;
+    s.bad[threadIdx.x] = 0;
+  }
   if (warp == kQkWarp) {
     tmem_alloc(smem_u32(&s.tmem_base), kTmemCols);
     tmem_relinquish();
@@ -153,7 +156,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int hb = half * NC;           // rows [hb, hb + NC)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float cs = p.softmax_scale * kLog2e;
-    // the q rows of a segment, those past it zeros
+    // The q rows of a segment, those past it zeros.  A row with an infinity has no
+    // finite logits; where they are all -inf it would look like one without keys,
+    // so such rows are marked, and made NaN.
     auto load_q = [&](const Seg& g) {
       constexpr int kPieces = BLOCK ? kD / 16 : kD / 8;  // 16-byte pieces of a row in memory
       constexpr int kPer = (NR * kPieces + kSoftThreads - 1) / kSoftThreads, kBatch = 9;
@@ -177,6 +182,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(s.q + (pc >> 2) * kQChunk + sw128(row, (pc & 3) * 2 + 1)) = b;
           } else {
             *reinterpret_cast<uint4*>(s.q + (pc >> 3) * kQChunk + sw128(row, pc & 7)) = v[k];
+            // exponents of all ones, of two elements a word
+            const auto full = [](uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+            if (full(v[k].x) | full(v[k].y) | full(v[k].z) | full(v[k].w)) s.bad[row] = 1;
           }
         }
       }
@@ -263,13 +271,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       key_scales(g, 0, key_page(g, 0));
       if (g.nb > 1) pid_next = key_page(g, 1);
       load_q(g);
+      named_bar_sync(1, kSoftThreads);  // every row's mark is there
     }
     int gb = 0;  // blocks of the segments before
     bool more = ok;
     while (ok && more) {
       const int n_item = seg_keys(g);
       if (threadIdx.x < NR) {
-        s.negm[threadIdx.x] = 0.f;  // the first block sets the reference
+        s.negm[threadIdx.x] = s.bad[threadIdx.x] ? NAN : 0.f;  // the first block sets the reference
+        s.bad[threadIdx.x] = 0;
         const int tok = p.groups > 1 ? 0 : threadIdx.x / p.H;
         s.nk[threadIdx.x] = threadIdx.x < g.rows ? g.pos1 + tok : 0;
       }

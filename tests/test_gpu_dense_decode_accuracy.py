@@ -137,3 +137,29 @@ def test_dominant_keys_in_every_block(qd, mode, H):
     q, pool, scales, sbs, val = _peaked(s, seqs, H, qd, mode, np.arange(5, 400, 100), 0.25, seed=7)
     ref, tol = _reference(q, val, scales, lens, seqs.page_table, 64, mode)
     _close(_decode(q, pool, scales, sbs, seqs, max(lens)), ref, tol)
+
+
+@pytest.mark.parametrize("qd,mode", [("bf16", "unit"), ("bf16", "row"), ("bf16", "bf16")])
+@pytest.mark.parametrize("H", [16, 64, 128])
+def test_infinite_queries_give_nan_whatever_their_logits(qd, mode, H):
+    """An infinite query element against keys of one sign: every logit is -inf
+    (or +inf), and the row NaN all the same; the other rows do not see it, and a
+    token without keys still gets zeros."""
+    lens = [1, 900, 0, 40, 129]
+    s, seqs = _batch([max(n, 1) for n in lens])
+    seqs.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((s.phys_rows, 576), generator=g, device="cuda").abs() + 0.1
+    pool, scales, sbs, _ = _pool(x, mode, g)
+    q = torch.randn((5, H, 576), generator=g, device="cuda").bfloat16()
+    clean = {most: _decode(q, pool, scales, sbs, seqs, most) for most in (1, 900)}
+    bad = q.clone()
+    rows = torch.zeros((5, H), dtype=torch.bool, device="cuda")
+    for b in range(5):
+        bad[b, 1, 7] = -float("inf")
+        bad[b, H - 1, 575] = float("inf")
+        rows[b, 1] = rows[b, H - 1] = lens[b] > 0
+    for most in (1, 900):  # whole, and cut
+        got = _decode(bad, pool, scales, sbs, seqs, most)
+        assert bool(got[rows].isnan().all())
+        assert torch.equal(got[~rows], clean[most][~rows]) and bool((got[2] == 0).all())
