@@ -409,7 +409,9 @@ smla_status_t smla_expanded_prefill(const uint16_t* q, int64_t q_token_stride, i
  *   max_kv_len   a bound on every kv_len, for the choice of the split; larger
  *                lengths are served too, only less evenly
  * Block scales (32) take e4m3 q; a bf16 cache takes bf16 q and
- * scale_block_size 0 (SMLA_ERR_UNSUPPORTED otherwise).  Tokens behind the
+ * scale_block_size 0 (SMLA_ERR_UNSUPPORTED otherwise).  A block-scaled row's
+ * values are carried in f16, off by at most 2^-10 of themselves or, in blocks of
+ * very small scale, by 2^-30 of the row's largest scale.  Tokens behind the
  * last sequence keep their outputs.  A token of a sequence without keys gets
  * zeros.  Cache rows outside a sequence's keys never reach its outputs,
  * whatever they hold; a NaN in the row (or its scale) of one of a sequence's

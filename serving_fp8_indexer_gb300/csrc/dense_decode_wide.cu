@@ -5,14 +5,17 @@
 //   S^T[128 keys x NR rows] = K . Q^T,   O^T[512 x NR] += V^T . P^T
 //
 // as in the e4m3 kernel, with kind::f16 MMAs and one term for everything.  A
-// bf16 cache: q, K and P in bf16 (P's rounding is 2^-9 of a weight).  Block
-// scales: f16, a row carried as byte * scale_blk 2^-e with 2^e the power of two
-// below its largest scale (the scale is off by 2^-12, the product by 2^-11; e4m3
-// q is exact); its logits and its weights take 2^e instead, as the e4m3 kernel
-// does with a row's scale.  The product is one f16x2 multiply for two elements
-// (through f32 to bf16 it was five instructions: 101 us against 85 at 16 heads
-// x 4 x <= 120 K keys).  The line of work, the walk along it and the join are
-// shared with the e4m3 kernel.
+// bf16 cache: q, K and P in bf16 (P's rounding is up to 2^-8 of a weight).  Block
+// scales: f16, a row carried as byte * scale_blk 2^-e with 2^e five binary places
+// below its largest scale (the scale and the product are off by up to 2^-11 each;
+// e4m3 q is exact); its logits and its weights take 2^e instead, as the e4m3
+// kernel does with a row's scale.  The largest product is below 2^15, the upper
+// end of f16, so that blocks of much smaller scales keep their bits: those below
+// 2^-19 of the largest are multiplied in two steps (see convert), and end at half
+// of f16's smallest step, 2^-30 of the largest scale.  The product is one f16x2
+// multiply for two elements (through f32 to bf16 it was five instructions: 101 us
+// against 85 at 16 heads x 4 x <= 120 K keys).  The line of work, the walk along
+// it and the join are shared with the e4m3 kernel.
 //
 // A block's 128 rows take 147 KB in 16 bits, so there is room for one block and
 // a little: eight 64-column chunks as four pairs (a pair is K's columns for QK
@@ -85,7 +88,7 @@ __device__ __forceinline__ void scaled16(const uint4& u, uint32_t scale2, uint4&
   lo = make_uint4(o[0], o[1], o[2], o[3]);
   hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
-constexpr uint32_t kOneF16x2 = 0x3c003c00u;
+constexpr uint32_t kOneF16x2 = 0x3c003c00u, kDownF16x2 = 0x01000100u;  // 1, 2^-16
 
 template <int NR, bool BLOCK>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -222,11 +225,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 9; ++k) most = fmaxf(most, fabsf(sc[k]));
       s.smax[half][r] = most;
       named_bar_sync(2 + (warp & 3), 64);
-      ex = min(max(static_cast<int>(__float_as_uint(fmaxf(most, s.smax[half ^ 1][r])) >> 23), 1), 253);
+      ex = min(max(static_cast<int>(__float_as_uint(fmaxf(most, s.smax[half ^ 1][r])) >> 23) - 5, 1), 253);
       const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);  // 2^(127 - ex)
-      uint32_t s2[9];
+      // A scale that f16 would round as a subnormal is taken 2^16 larger, and the
+      // products of its block are brought down again: then nothing but the
+      // products themselves can be subnormal.  (The branch alone costs 32 rows 89
+      // -> 94 us, 16 rows 78.5 -> 79.0; without it such blocks lose a bit for each
+      // factor of two.)
+      uint32_t s2[5], deep = 0;  // two scales a word
 #pragma unroll
-      for (int k = 0; k < 9; ++k) s2[k] = f32x2_to_f16x2(sc[k] * down, sc[k] * down);
+      for (int k = 0; k < 9; k += 2) {
+        float f[2] = {sc[k] * down, k < 8 ? sc[k + 1] * down : 1.f};
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (fabsf(f[u]) < 0x1p-14f) {
+            f[u] *= 0x1p16f;
+            deep |= 1u << (k + u);
+          }
+        s2[k >> 1] = f32x2_to_f16x2(f[0], f[1]);
+      }
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
         const bool nope = k < 2;
@@ -252,11 +269,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < (nope ? 8 : 2); ++c) {
           uint4 a, b;
-          scaled16(u[c], s2[nope ? 4 * k + (c >> 1) : 8], a, b);
+          const int blk = nope ? 4 * k + (c >> 1) : 8;
+          scaled16(u[c], __byte_perm(s2[blk >> 1], 0, blk & 1 ? 0x3232 : 0x1010), a, b);
           uint8_t* dst = nope ? s.pair[sl] + (c >> 2) * kChunk : s.rope;
           const int piece = nope ? (c & 3) * 2 : half * 4 + 2 * c;
           *reinterpret_cast<uint4*>(dst + sw128(r, piece)) = a;
           *reinterpret_cast<uint4*>(dst + sw128(r, piece + 1)) = b;
+        }
+        if (__builtin_expect((deep & (nope ? 0xfu << (4 * k) : 0x100u)) != 0, 0)) {
+#pragma unroll 1
+          for (int c = 0; c < (nope ? 16 : 4); ++c) {  // 16-byte pieces, four a block
+            if (!(deep >> (nope ? 4 * k + (c >> 2) : 8) & 1)) continue;
+            uint8_t* dst = nope ? s.pair[sl] + (c >> 3) * kChunk : s.rope;
+            uint4& v = *reinterpret_cast<uint4*>(dst + sw128(r, nope ? c & 7 : half * 4 + c));
+            v = make_uint4(hmul2(v.x, kDownF16x2), hmul2(v.y, kDownF16x2), hmul2(v.z, kDownF16x2), hmul2(v.w, kDownF16x2));
+          }
         }
         fence_proxy_async_smem();
         warp_arrive(nope ? smem_u32(&s.bar_pair_full[sl]) : smem_u32(&s.bar_rope_full), lane);

@@ -163,3 +163,50 @@ def test_infinite_queries_give_nan_whatever_their_logits(qd, mode, H):
         got = _decode(bad, pool, scales, sbs, seqs, most)
         assert bool(got[rows].isnan().all())
         assert torch.equal(got[~rows], clean[most][~rows]) and bool((got[2] == 0).all())
+
+
+def _spread_blocks(rows, spread, zeros, gen):
+    """A block-scaled pool whose row blocks differ by the powers of two `spread`
+    (in turn, by block), with other scales' bits at random; the rotary blocks'
+    scales are 1.  `zeros`: the blocks of the largest scale hold nothing."""
+    x = torch.randn((rows, 18, 32), generator=gen, device="cuda") * 64
+    e = torch.tensor([spread[i % len(spread)] for i in range(16)] + [0, 0], device="cuda").float()
+    s = 2.0 ** -e * (1 + torch.rand((rows, 18), generator=gen, device="cuda"))
+    s[:, 16:] = 1.0
+    if zeros:
+        x[:, :16][:, e[:16] == 0] = 0.0
+    x[:, 16:] /= 64
+    b = _e4m3(x)
+    return b.view(rows, 576).view(torch.uint8), s.contiguous(), (b.double() * s.double()[:, :, None]).view(rows, 576)
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("spread", [(0, 3), (0, 13, 14, 15), (0, 17, 18, 19), (0, 20, 21, 24), (0, 26)])
+@pytest.mark.parametrize("H", [16, 64])
+def test_blocks_of_very_different_scales(H, spread, zeros):
+    """Every block's columns to the same relative accuracy, whatever the scales
+    of the row's other blocks.  The rotary part's products are exact in f16, so
+    no logit is off by more than its float32 sum; a value is off by 2^-11 for its
+    scale and 2^-11 for its product, or half of f16's smallest step in units of
+    2^-5 of the row's largest scale (taken as its power of two, 2^-30 at most); a
+    weight by 2^-11."""
+    lens = [1, 700, 1100]
+    s, seqs = _batch(lens, seed=4)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    pool, scales, val = _spread_blocks(s.phys_rows, spread, zeros, g)
+    q = torch.zeros((3, H, 576), device="cuda")
+    q[:, :, 512:] = torch.randn((3, H, 64), generator=g, device="cuda") * 4
+    q8 = _e4m3(q).view(torch.uint8)
+    ref, _ = _reference(q8, val, scales, lens, seqs.page_table, 64, "block")
+    tol = torch.zeros_like(ref)
+    q64 = q8.view(torch.float8_e4m3fn).double()
+    for b, n in enumerate(lens):
+        key = torch.arange(n, device="cuda")
+        rows = seqs.page_table[b].long()[key // 64] * 64 + key % 64
+        p = torch.softmax(SCALE * q64[b] @ val[rows].T, 1)
+        mass = SCALE * (q64[b].abs() @ val[rows].abs().T).amax(1, keepdim=True)
+        rel = 3 * 2.0 ** -11 + 2 * 64 * 2.0 ** -23 * mass + 2.0 ** -18 + n * 2.0 ** -24
+        tol[b] = rel * (p @ val[rows, :512].abs()) + 2.0 ** -30 * (p @ scales[rows].double().amax(1))[:, None]
+    tol += 2.0 ** -8 * ref.abs()
+    for most in (1, 1100):
+        _close(_decode(q8, pool, scales, 32, seqs, most), ref, tol)
