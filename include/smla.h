@@ -321,7 +321,8 @@ smla_status_t smla_rope(const void* x, int32_t x_dtype, int64_t x_token_stride, 
  * scale, values beyond +-448 become +-448), >= D (one scale per row) or 32
  * (D / 32 block scales per row), where scale = largest finite magnitude /
  * 448 (1 when that is 0; at least the smallest normal f32), byte = e4m3(r /
- * scale).  NaN stays NaN and infinities saturate.
+ * scale), of the f32 quotient (below a scale of 2^-100, of one that may be off in
+ * its last place).  NaN stays NaN and infinities saturate.
  *   x            bf16 [T, D], rows x_stride elements apart
  *   norm_weight  bf16 [norm_dim], or NULL for no norm (norm_dim is then ignored)
  *   rope         dim = 0 for none; its columns may overlap the normalised ones
