@@ -379,8 +379,12 @@ smla_status_t smla_cache_gather(const void* pool, int32_t pool_dtype, int64_t ph
  * current device (16-byte aligned; NULL when that is 0), used when the
  * queries alone are too few to fill the GPU; contents on entry do not matter,
  * unspecified on return; not shared by calls that may overlap.  The products
- * run as tcgen05 kind::f16 (bf16) MMAs with f32 TMEM accumulation; P is
- * rounded to bf16 (kept as two bf16 terms where T * H <= 64). */
+ * run as tcgen05 kind::f16 (bf16) MMAs with f32 TMEM accumulation.  The weights P
+ * are carried as one bf16 term (rounded by up to 2^-8 of themselves, as the output
+ * is) or two (2^-16).  smla_expanded_prefill takes two in calls of up to 64 rows
+ * (T * H), where they cost little, and one in others; smla_expanded_prefill_terms
+ * takes the caller's p_terms, 1 or 2, so that a row's accuracy does not depend on
+ * how many others share its call (0: as smla_expanded_prefill). */
 size_t smla_expanded_prefill_workspace_size(int32_t T, int32_t S, int32_t B, int32_t H);
 smla_status_t smla_expanded_prefill(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
                                     const uint16_t* k_nope, int64_t k_token_stride, int64_t k_head_stride,
@@ -389,6 +393,13 @@ smla_status_t smla_expanded_prefill(const uint16_t* q, int64_t q_token_stride, i
                                     const int32_t* cu_kv, int32_t B, int32_t T, int32_t S, int32_t H,
                                     float softmax_scale, const float* attn_sink, uint16_t* out, float* lse,
                                     void* workspace, size_t workspace_bytes, cudaStream_t stream);
+smla_status_t smla_expanded_prefill_terms(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                                          const uint16_t* k_nope, int64_t k_token_stride, int64_t k_head_stride,
+                                          const uint16_t* k_rope, int64_t k_rope_stride, const uint16_t* v,
+                                          int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_q,
+                                          const int32_t* cu_kv, int32_t B, int32_t T, int32_t S, int32_t H,
+                                          float softmax_scale, int32_t p_terms, const float* attn_sink, uint16_t* out,
+                                          float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Dense MLA decode (latent attention, absorbed form) for few query tokens over
  * the whole cache of their sequence: out[t,h] as for smla_dense_prefill, with

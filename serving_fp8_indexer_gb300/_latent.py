@@ -195,12 +195,14 @@ def expanded_prefill_workspace_size(T: int, S: int, B: int, H: int) -> int:
 def expanded_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
                      cu_kv: torch.Tensor, softmax_scale: float, out: torch.Tensor,
                      workspace: Optional[torch.Tensor], attn_sink: Optional[torch.Tensor] = None,
-                     lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                     lse: Optional[torch.Tensor] = None, stream=None, p_terms: int = 0) -> torch.Tensor:
     """out bf16 [T, H, 128] = causal attention of q bf16 [T, H, 192] over keys
     [k_nope [S, H, 128] | k_rope [S, 64]] and values v [S, H, 128] (bf16,
     strided views with dense rows); cu_q, cu_kv int32 [B+1]; workspace a uint8
     CUDA tensor of at least expanded_prefill_workspace_size() bytes (None when
-    that is 0); attn_sink f32 [H], lse f32 [T, H] (output)."""
+    that is 0); attn_sink f32 [H], lse f32 [T, H] (output).  p_terms: the bf16
+    terms that the softmax weights are carried in, 1 or 2 (more exact, slower);
+    0 leaves it to the library, which takes 2 in calls of up to 64 rows (T * H)."""
     lib, dev = _lib._lib or _lib.load(), _device()
     bf, f32, i32 = (torch.bfloat16,), torch.float32, torch.int32
     qp, q_shape, qs = _rows(q, "q", bf, dev, 3)
@@ -213,12 +215,12 @@ def expanded_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor
             (attn_sink is not None and attn_sink.shape != (H,)) or (lse is not None and lse.shape != (T, H))):
         raise ValueError("q [T, H, 192], k_nope [S, H, 128], k_rope [S, 64], v [S, H, 128], out [T, H, 128], cu_q and "
                          "cu_kv [B + 1], attn_sink [H], lse [T, H] do not fit each other")
-    st = lib.smla_expanded_prefill(qp, qs[0], qs[1], kp, ks[0], ks[1], rp, rs[0], vp, vs[0], vs[1],
-                                   _flat(cu_q, "cu_q", i32, dev, 1), _flat(cu_kv, "cu_kv", i32, dev, 1), B, T, S, H,
-                                   softmax_scale, _flat(attn_sink, "attn_sink", f32, dev, 1),
-                                   _flat(out, "out", torch.bfloat16, dev, 3), _flat(lse, "lse", f32, dev, 2),
-                                   _flat(workspace, "workspace", torch.uint8, dev, 1),
-                                   0 if workspace is None else workspace.numel(), _on(stream, dev))
+    st = lib.smla_expanded_prefill_terms(qp, qs[0], qs[1], kp, ks[0], ks[1], rp, rs[0], vp, vs[0], vs[1],
+                                         _flat(cu_q, "cu_q", i32, dev, 1), _flat(cu_kv, "cu_kv", i32, dev, 1), B, T, S,
+                                         H, softmax_scale, p_terms, _flat(attn_sink, "attn_sink", f32, dev, 1),
+                                         _flat(out, "out", torch.bfloat16, dev, 3), _flat(lse, "lse", f32, dev, 2),
+                                         _flat(workspace, "workspace", torch.uint8, dev, 1),
+                                         0 if workspace is None else workspace.numel(), _on(stream, dev))
     if st:
         _check(lib, st)
     return out

@@ -29,7 +29,7 @@ EXPORTED = ("smla_indexer_scores", "smla_topk_workspace_size", "smla_topk", "sml
             "smla_indexer_topk", "smla_sparse_prefill",
             "smla_sparse_prefill_bf16_cache", "smla_dense_prefill", "smla_sparse_decode_workspace_size", "smla_sparse_decode",
             "smla_sparse_decode_noalloc", "smla_rope_frequencies", "smla_rope", "smla_cache_append", "smla_cache_gather",
-            "smla_expanded_prefill_workspace_size", "smla_expanded_prefill",
+            "smla_expanded_prefill_workspace_size", "smla_expanded_prefill", "smla_expanded_prefill_terms",
             "smla_dense_decode_workspace_size", "smla_dense_decode",
             "smla_check_device_errors", "smla_selftest_wait_timeout", "smla_last_error", "smla_version")
 
@@ -94,6 +94,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.smla_expanded_prefill_workspace_size.restype = sz
         lib.smla_expanded_prefill.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, i32, i32, i32, i32,
                                               f32, vp, vp, vp, vp, sz, vp]
+        at = lib.smla_expanded_prefill.argtypes
+        lib.smla_expanded_prefill_terms.argtypes = at[:18] + [i32] + at[18:]
         lib.smla_dense_decode_workspace_size.argtypes = [i32, i32, i32]
         lib.smla_dense_decode_workspace_size.restype = sz
         lib.smla_dense_decode.argtypes = [vp, i32, vp, i32, i64, vp, i32, SeqsT, i32, i32, i32, f32, vp, vp, vp, sz, vp]
@@ -105,7 +107,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                      "smla_sparse_prefill_bf16_cache",
                      "smla_dense_prefill",
                      "smla_sparse_decode", "smla_sparse_decode_noalloc", "smla_rope_frequencies", "smla_rope",
-                     "smla_cache_append", "smla_cache_gather", "smla_expanded_prefill", "smla_dense_decode", "smla_check_device_errors",
+                     "smla_cache_append", "smla_cache_gather", "smla_expanded_prefill",
+                     "smla_expanded_prefill_terms", "smla_dense_decode", "smla_check_device_errors",
                      "smla_selftest_wait_timeout"):
             getattr(lib, name).restype = ctypes.c_int
         if path is None:

@@ -196,7 +196,20 @@ smla_status_t smla_expanded_prefill(const uint16_t* q, int64_t q_token_stride, i
                                     const int32_t* cu_kv, int32_t B, int32_t T, int32_t S, int32_t H,
                                     float softmax_scale, const float* attn_sink, uint16_t* out, float* lse,
                                     void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return smla_expanded_prefill_terms(q, q_token_stride, q_head_stride, k_nope, k_token_stride, k_head_stride, k_rope,
+                                     k_rope_stride, v, v_token_stride, v_head_stride, cu_q, cu_kv, B, T, S, H,
+                                     softmax_scale, 0, attn_sink, out, lse, workspace, workspace_bytes, stream);
+}
+
+smla_status_t smla_expanded_prefill_terms(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                                          const uint16_t* k_nope, int64_t k_token_stride, int64_t k_head_stride,
+                                          const uint16_t* k_rope, int64_t k_rope_stride, const uint16_t* v,
+                                          int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_q,
+                                          const int32_t* cu_kv, int32_t B, int32_t T, int32_t S, int32_t H,
+                                          float softmax_scale, int32_t p_terms, const float* attn_sink, uint16_t* out,
+                                          float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   clear_last_error();
+  if (p_terms < 0 || p_terms > 2) return fail(SMLA_ERR_INVALID_ARG, "p_terms=%d must be 0, 1 or 2", p_terms);
   if (T < 0 || S < 0 || B < 0) return fail(SMLA_ERR_INVALID_ARG, "T=%d S=%d B=%d must be >= 0", T, S, B);
   if (H < 1 || H > 65535) return fail(SMLA_ERR_UNSUPPORTED, "H=%d must be in [1, 65535]", H);
   if (!(softmax_scale > 0.f) || softmax_scale < 1.0e-30f || softmax_scale > 1.0e30f)
@@ -226,7 +239,7 @@ smla_status_t smla_expanded_prefill(const uint16_t* q, int64_t q_token_stride, i
   const ExpandedArgs a{q,    q_token_stride, q_head_stride,  k_nope,        k_token_stride, k_head_stride, k_rope,
                        k_rope_stride,        v,              v_token_stride, v_head_stride, cu_q,          cu_kv,
                        B,    T,              S,              H,             softmax_scale,  attn_sink,     out,
-                       lse,  nsplit,         workspace};
+                       lse,  nsplit,         workspace,     p_terms};
   return launch_expanded(a, err, stream);
 }
 

@@ -28,7 +28,8 @@
 // 2^8 (P <= 256; bf16 P keeps its relative precision), so O is rescaled
 // rarely.  l sums the f32 weights before their rounding to bf16; that
 // rounding (2^-8 relative at most, random) is the only one beside the output's,
-// and as large; calls of a few rows carry P as two terms instead.
+// and as large at every length.  P in two bf16 terms does without it, for 20
+// -> 28 MMAs a block; the caller may ask for either (launch_expanded).
 //
 // Warps: 0-3 softmax of tile A, 4-7 of tile B (thread = row = TMEM lane, no
 // exchange between threads), 8 TMA, 9 MMA issue and TMEM, 10 the V tail.  One
@@ -71,7 +72,7 @@ constexpr uint32_t kTmemO = 256;          // O_A, O_B after S_A, S_B
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTau = 8.f;
-constexpr int kTwoTermRows = 64;
+constexpr int kTwoTermRows = 64;  // rows of a call that take two terms unasked
 constexpr int kLaunchRegs = 168, kSoftRegs = 208, kOtherRegs = 80;
 static_assert(kSoftThreads * kSoftRegs + (kThreads - kSoftThreads) * kOtherRegs <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
@@ -655,12 +656,13 @@ smla_status_t launch_expanded(const ExpandedArgs& a, unsigned* err, cudaStream_t
   const size_t smem = sizeof(Smem);
   static_assert(sizeof(Smem) <= 232448, "shared memory exceeds a CTA's 227 KB");
   static_assert(offsetof(Smem, k) % 1024 == 0 && offsetof(Smem, v) % 1024 == 0, "swizzled tiles need 1024-byte alignment");
-  // A call of a few rows in all takes P as two terms: its rounding would show
-  // beside the output's (1.4 times the error against 64 bits, and up to 1.5 in
-  // single rows, where it averages over few elements), and the time is mostly
-  // the launch (1 row of 4000 keys 14 -> 17 us).  With many rows it would cost a
-  // third (32 tokens x 128 heads over 4 x 8000 keys 334 -> 450 us).
-  const bool two = static_cast<int64_t>(a.T) * a.H <= kTwoTermRows;
+  // One term or two: the error against 64 bits is 1.4 or 1.0 times that of the
+  // output's own rounding, in every row and at every size.  Two cost little where
+  // a call is mostly its launch (1 row of 4000 keys 14 -> 17 us) and 40 % where it
+  // is not (4096 tokens x 128 heads 441 -> 614 us, 32 tokens x 128 heads over 4 x
+  // 8000 keys 333 -> 467).  So, where the caller does not say: two for a call of
+  // up to kTwoTermRows rows, one for others.
+  const bool two = a.p_terms ? a.p_terms == 2 : static_cast<int64_t>(a.T) * a.H <= kTwoTermRows;
   const auto kernel = two ? expanded_kernel<true> : expanded_kernel<false>;
   static std::atomic<unsigned long long> ready[2];
   const smla_status_t st = prepare_kernel(reinterpret_cast<const void*>(kernel), smem, kLaunchRegs, ready[two],

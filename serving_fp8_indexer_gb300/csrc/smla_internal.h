@@ -151,6 +151,7 @@ struct ExpandedArgs {
   float* lse;
   int nsplit;
   void* workspace;
+  int p_terms;  // of the weights: 1, 2 or 0 (by the call's size)
 };
 // Splits of the keys for these sizes, the workspace they need, the launch.
 int expanded_splits(int T, int S, int B, int H);
