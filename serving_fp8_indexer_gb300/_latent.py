@@ -66,10 +66,16 @@ def _rows(t, name, dtypes, dev, ndim):
     return t.data_ptr(), shape, strides
 
 
-def _seqs(s: Seqs, dev: int) -> SeqsT:
-    i32 = torch.int32
-    return SeqsT(_flat(s.cu_q, "cu_q", i32, dev, 1), _flat(s.kv_len, "kv_len", i32, dev, 1),
-                 _flat(s.page_table, "page_table", i32, dev, 2), s.B, s.max_pages, s.page_size, s.T)
+def _seqs(s: Seqs, dev: int, paged: bool = True) -> SeqsT:
+    """The C struct of a batch whose arrays hold what the kernels read: B + 1
+    entries, B, and (`paged`: where pages are looked up) B rows of max_pages."""
+    i32, table, B = torch.int32, s.page_table, s.B
+    c = SeqsT(_flat(s.cu_q, "cu_q", i32, dev, 1), _flat(s.kv_len, "kv_len", i32, dev, 1),
+              _flat(table, "page_table", i32, dev, 2), B, s.max_pages, s.page_size, s.T)
+    if s.cu_q.shape[0] <= B or s.kv_len.shape[0] < B or paged and (table.shape[0] < B or table.shape[1] != s.max_pages):
+        raise ValueError(f"seqs: cu_q {tuple(s.cu_q.shape)}, kv_len {tuple(s.kv_len.shape)} and page_table "
+                         f"{tuple(table.shape)} do not hold B={B} sequences of max_pages={s.max_pages}")
+    return c
 
 
 def _on(stream, dev: int) -> int:
@@ -136,7 +142,7 @@ def rope(x: torch.Tensor, seqs: Seqs, rope: Rope, out: torch.Tensor, stream=None
     op, out_shape, os_ = _rows(out, "out", (torch.bfloat16, torch.float32, torch.uint8), dev, 3)
     if shape != out_shape or shape[0] != seqs.T:
         raise ValueError(f"x {tuple(shape)} and out {tuple(out_shape)} must both be [T={seqs.T}, H, D]")
-    st = lib.smla_rope(xp, _DTYPES[x.dtype], xs[0], xs[1], _seqs(seqs, dev), shape[1], shape[2], rope.as_c(dev), op,
+    st = lib.smla_rope(xp, _DTYPES[x.dtype], xs[0], xs[1], _seqs(seqs, dev, False), shape[1], shape[2], rope.as_c(dev), op,
                        _DTYPES[out.dtype], os_[0], os_[1], _on(stream, dev))
     if st:
         _check(lib, st)
