@@ -20,6 +20,7 @@ import pytest
 import torch
 
 import serving_fp8_indexer_gb300 as smla
+import test_gpu_dense_decode as dense
 from serving_fp8_indexer_gb300 import workloads as wl
 
 pytestmark = pytest.mark.gpu
@@ -210,3 +211,21 @@ def test_blocks_of_very_different_scales(H, spread, zeros):
     tol += 2.0 ** -8 * ref.abs()
     for most in (1, 1100):
         _close(_decode(q8, pool, scales, 32, seqs, most), ref, tol)
+
+
+@pytest.mark.parametrize("qd,mode", MODES)
+@pytest.mark.parametrize("q_lens,kv_lens,H", [([1, 2], [3000, 1100], 16), ([2], [5000], 32), ([1, 1], [777, 2500], 128)])
+def test_error_beside_the_rounding_of_the_output(qd, mode, q_lens, kv_lens, H):
+    """Root mean square, in units of the output's own rounding r (2^-8 / sqrt(3) of
+    an element where that is largest, as for every rounding below).  Unit and row
+    scales: q and K are exact and a weight is off by half of r (2^-9): sqrt(1 +
+    1/4) = 1.12.  Block scales: scale and product off by r / 8 each, in the logits
+    and in the values, the weight by r / 8: sqrt(1 + 5 / 64) = 1.04.  bf16: the
+    weight by r: 1.42.  A tenth more for the sums in float32 and the sample."""
+    s, seqs, q, pool, scales, sbs, val = dense._case(q_lens, kv_lens, H, qd, mode, seed=41)
+    ref, _ = dense._reference(s, q, val, **dense._carried(scales, pool))
+    most = {"bf16": 1.42, "block": 1.04}.get(mode, 1.12) * 1.1
+    rounding = float((ref.bfloat16().double() - ref).norm())
+    for bound in (1, max(kv_lens)):
+        got = _decode(q, pool, scales, sbs, seqs, bound)
+        assert float((got.double() - ref).norm()) <= most * rounding
