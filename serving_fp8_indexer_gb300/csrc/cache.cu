@@ -12,9 +12,12 @@
 // cache_gather: the inverse, token t's cached row dequantised to bf16.
 //
 // A few rows (a decode step) cost a launch and the chain cu_q -> page -> row:
-// 16 rows of 576 are written in 3.3 us, 257 read in 2.6.  For many rows the
-// append comes to 2.6 TB/s (12 117 rows of 576 with block scales and rows_out:
-// 13.75 us against 5.3 of HBM time, unit scales 10.6), the gather by HBM (8 sequences, 49 K rows: 16.8 us,
+// 16 rows of 576 are written in 3.5 us, 257 read in 2.4.  For many rows the
+// append takes 2.5 times its HBM time (12 117 rows of 576 with rows_out: block
+// scales 13.8 us against 5.3, row scales 12.6, unit 10.7, bf16 12.0): 876 warp
+// instructions a row in block mode keep the issue slots 65 % busy, and half the
+// warps that fit wait for the row's loads and shuffles beside it.  The gather is
+// bound by HBM (8 sequences, 49 K rows: 16.8 us,
 // 5.0 TB/s).  The angles come from integer phases: in float64 they were the
 // append's bound (27 us).
 #include <algorithm>

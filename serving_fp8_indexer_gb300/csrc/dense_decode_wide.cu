@@ -36,9 +36,9 @@
 // chain of a block, about 6.5 k cycles, of which raw chunks awaited 1.5 k, read
 // 0.6 k, converted and stored 1.7 k, fenced and handed on 1.2 k, softmax 1.4 k.
 //
-// Measured: 16 heads over 4 x <= 120 K keys, bf16 cache 85 us (5.3 TB/s), block
-// scales 77 us (3.3 TB/s); 8 x 2 tokens x 128 heads over <= 8192 keys, bf16 60 us
-// (527 TFLOP/s), block scales 87 us.  (The prefill kernel's form with one block
+// Measured: 16 heads over 4 x <= 120 K keys, bf16 cache 83 us (5.4 TB/s), block
+// scales 79 us (3.2 TB/s); 8 x 2 tokens x 128 heads over <= 8192 keys, bf16 60 us
+// (528 TFLOP/s), block scales 94 us.  (The prefill kernel's form with one block
 // in flight: 142, 179, 85 and 115 us.)
 //
 // Warps: 0-7 conversion, softmax and epilogue (thread = one key x NR/2 rows),
