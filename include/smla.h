@@ -410,8 +410,8 @@ smla_status_t smla_expanded_prefill_terms(const uint16_t* q, int64_t q_token_str
  *     (of p_j s_j, s_j the row's scale), so that the many keys far below a
  *     dominant one keep their weight.  (smla_dense_prefill and the sparse calls
  *     round P to one e4m3 term for e4m3 q, and to two, which end 2^-14 below a
- *     row's largest, for bf16 q.)  bf16 q is exact down to 2^-9 of its row's
- *     largest element over an e4m3 cache, smaller elements are off by up to 2^-17
+ *     row's largest, for bf16 q.)  bf16 q is exact down to 2^-14 of its row's
+ *     largest element over an e4m3 cache, smaller elements are off by up to 2^-22
  *     of that, and exact over a bf16 cache;
  *   - e4m3 caches in every scale mode, or a bf16 cache.
  *   q            [T, H, 576], bf16 or e4m3 (q_dtype)

@@ -4,7 +4,7 @@
 // Orientation and precision are those of the prefill attention kernel: keys
 // are the MMA M dimension and query rows the N dimension,
 //   S^T[128 keys x NR rows] = K . Q^T,   O^T[512 x NR] += V^T . P^T,
-// all on the FP8 pipe, with bf16 q as two e4m3 terms (hi + lo), so that the e4m3
+// all on the FP8 pipe, with bf16 q as two e4m3 terms (hi + lo / 32), so that the e4m3
 // cache rows are used as they lie in memory.  What is different here:
 //
 // * Weights.  A cache is long: thousands of keys far below one that dominates
@@ -87,13 +87,18 @@ struct Smem {
   uint32_t tmem_base;
 };
 
-// Two floats -> e4m3 hi and lo pairs, through f16 (|x| <= 448): hi = e4m3(x),
-// lo = e4m3(x - hi), the difference exact in f16.  A bf16 query's eight bits fit
-// both, down to 2^-9 of its row's largest value.
+// Two floats -> e4m3 hi and lo pairs, through f16 (|x| <= 256): hi = e4m3(x),
+// lo = e4m3(32 (x - hi)), the difference exact in f16 and at most 8.  A bf16
+// query's eight bits fit both, down to 2^-14 of its row's largest value (its lo
+// products have accumulators of their own, which are divided by 32; with lo as it
+// is they would fit to 2^-9 only, and a query with one very large element lost
+// bits of all others).
+constexpr uint32_t kLoF16x2 = 0x50005000u;  // 32
+constexpr float kLoDown = 1.f / 32.f;
 __device__ __forceinline__ void split2(float a, float b, uint16_t& hi, uint16_t& lo) {
   const uint32_t h = f32x2_to_f16x2(a, b);
   hi = f16x2_to_e4m3x2(h);
-  lo = f16x2_to_e4m3x2(hsub2(h, e4m3x2_to_f16x2(hi)));
+  lo = f16x2_to_e4m3x2(hmul2(hsub2(h, e4m3x2_to_f16x2(hi)), kLoF16x2));
 }
 // Two weights (0 .. 2^15) -> three e5m2 terms each, through f16, every difference
 // exact there: off by 2^-3 of 2^-3 of 2^-3, and 2^-11 for the f16, of the weight,
@@ -331,7 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           after_wait(v0);
           if (QP == 2) after_wait(v1);
 #pragma unroll
-          for (int h = 0; h < NC; ++h) y[h] = QP == 2 ? __uint_as_float(v0[h]) + __uint_as_float(v1[h]) : __uint_as_float(v0[h]);
+          for (int h = 0; h < NC; ++h)
+            y[h] = QP == 2 ? fmaf(__uint_as_float(v1[h]), kLoDown, __uint_as_float(v0[h])) : __uint_as_float(v0[h]);
         }
         tc_fence_before();
         warp_arrive(smem_u32(&s.bar_s_free[buf]), lane);

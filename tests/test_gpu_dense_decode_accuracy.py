@@ -229,3 +229,25 @@ def test_error_beside_the_rounding_of_the_output(qd, mode, q_lens, kv_lens, H):
     for bound in (1, max(kv_lens)):
         got = _decode(q, pool, scales, sbs, seqs, bound)
         assert float((got.double() - ref).norm()) <= most * rounding
+
+
+@pytest.mark.parametrize("mode", ["unit", "row", "bf16"])
+@pytest.mark.parametrize("large", [30.0, 3000.0])
+@pytest.mark.parametrize("H", [16, 64])
+def test_one_large_query_element_leaves_the_others_their_bits(mode, large, H):
+    """A query element far above the others, in a column where the keys are 0: the
+    logits come from the others alone.  Over an e4m3 cache bf16 elements are exact
+    down to 2^-14 of the largest and off by 2^-22 of it below (3000: 0.0007 beside
+    elements of size 1), which moves a logit by less than 0.0007 and a weight by
+    0.07 %, a fifth of the output's rounding; the rest as in the test above."""
+    s, seqs, q, pool, scales, sbs, val = dense._case([1, 2], [2000, 700], H, "bf16", mode, seed=43)
+    q[:, :, 300] = large
+    q[:, ::2, 300] = -large
+    pool[:, 300] = 0
+    val[:, 300] = 0
+    ref, _ = dense._reference(s, q, val, **dense._carried(scales, pool))
+    most = ({"bf16": 1.42}.get(mode, 1.12) + 0.02) * 1.1
+    rounding = float((ref.bfloat16().double() - ref).norm())
+    for bound in (1, 2000):
+        got = _decode(q, pool, scales, sbs, seqs, bound)
+        assert float((got.double() - ref).norm()) <= most * rounding
