@@ -75,13 +75,12 @@ SMLA_DEVICE_INLINE unsigned long long rope_step(double f) {
 // cos and sin of pos * inv_freq, times `amplitude`: the integer product step *
 // pos wraps modulo one turn exactly, so far positions lose nothing to the
 // reduction (a 32-bit product pos * inv_freq is off by 2^-24 of the whole
-// angle: 0.008 radians at position 130 000).  What is left is the cut of the
-// reduced angle to 2^-32 of a turn (1.5e-9 radians: beside an element of size 1 in
-// f32, whose own rounding is 6e-8, nothing; of a sine that is itself below 1e-5 its
-// last digits) and its rounding to a float, at most 2^-25 half turns.
+// angle: 0.008 radians at position 130 000).  What is left is the rounding of the
+// reduced angle to a float, 2^-24 of itself (of all 64 bits: its upper 32 alone
+// are off by 2^-32 of a turn, a thousandth of the slowest pairs' first steps).
 SMLA_DEVICE_INLINE void rope_cos_sin(double inv_freq, int pos, float amplitude, float& c, float& s) {
   const unsigned long long phase = rope_step(inv_freq) * static_cast<unsigned long long>(static_cast<long long>(pos));
-  const float half_turns = static_cast<float>(static_cast<int>(phase >> 32)) * (1.f / 2147483648.f);
+  const float half_turns = __ll2float_rn(static_cast<long long>(phase)) * 0x1p-63f;
   sincospif(half_turns, &s, &c);
   c *= amplitude;
   s *= amplitude;
