@@ -32,19 +32,20 @@
 //   rotary part in a 64-byte-swizzled one, which P^T reuses after QK.
 // * For NR < 64, P's three terms are one operand of 3 NR columns with an
 //   accumulator each (summed at the end): a third of the MMAs.  With NR = 64
-//   there is no TMEM for that, and PV runs three times into one accumulator; the
-//   second and third product of a tile keep its V operand in the tensor core
-//   (55.7 -> 54.2 us).
+//   there is no TMEM for that, and PV runs three times into one accumulator.
+//   (Keeping a tile's V operand in the tensor core's buffer for its third product
+//   took 54.2 us instead of 55.5, but nothing promises that it is still there: QK's
+//   products come from another warp and may fall between the two.)
 //
 // Bound: HBM for few rows (a block of 73.7 KB is 3140 cycles of an SM's share
 // of 6.8 TB/s; its MMAs about 1430 cycles at NR = 16, 1760 at 32), at NR = 64 the
-// chain load -> QK -> softmax -> PV over two slots (tensor time about 3200 cycles
+// chain load -> QK -> softmax -> PV over two slots (tensor time about 3460 cycles
 // a block, where the shared-memory reads of N = 64 operands set the rate: 48
-// cycles an MMA, 32 with A kept).
+// cycles an MMA).
 //
 // Measured: 16 heads over 4 x <= 120 K keys 49 us (4.6 TB/s; 6.2 while the line
 // runs, then 6 us of start and 5.7 of join), 32 heads 54; 8 x 2 tokens x 128 heads
-// over <= 8192 keys 54 us (580 TFLOP/s).
+// over <= 8192 keys 55.6 us (566 TFLOP/s).
 //
 // Warps: 0-7 softmax and epilogue (thread = one key x NR/2 rows), 8 TMA, 9 QK,
 // 10 PV.
@@ -756,13 +757,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (leader) {
 #pragma unroll
-              for (int kk = 0; kk < 2; ++kk)
+              for (int term = 0; term < 2; ++term)
 #pragma unroll
-                for (int tile = 0; tile < 4; ++tile)
-                  mma_f8f6f4_ss_pair(tmem + tile * kPN,
-                                     vs + static_cast<uint64_t>((tile * kChunk + (h * kHalf + kk * 32) * 128) >> 4),
-                                     pm + static_cast<uint64_t>((kk * 32 * 64) >> 4),
-                                     pm + static_cast<uint64_t>((kPRow / 2 + kk * 32 * 64) >> 4), IDESC, 1u);
+                for (int kk = 0; kk < 2; ++kk)
+                  pv(h, kk, pm + static_cast<uint64_t>((term * (kPRow / 2) + kk * 32 * 64) >> 4), true);
             }
           }
           if (leader) {

@@ -242,17 +242,6 @@ SMLA_DEVICE_INLINE void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// kind::f8f6f4 products of one A with two B's in turn: the first keeps A in the
-// tensor core's operand buffer, the second takes it from there.
-SMLA_DEVICE_INLINE void mma_f8f6f4_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b0, uint64_t b1, uint32_t idesc,
-                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::fill [%0], %1, %2, %4, p;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::lastuse [%0], %1, %3, %4, 1;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b0), "l"(b1), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 // D[tmem] (+)= A[tmem] * B[smem]^T, kind::f16 (bf16 x bf16), issued by one
 // thread: A row r is TMEM lane r, two consecutive K elements per column.
 SMLA_DEVICE_INLINE void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
