@@ -439,6 +439,94 @@ smla_status_t smla_dense_decode(const void* q, int32_t q_dtype, const void* late
                                 const float* attn_sink, uint16_t* out, void* workspace, size_t workspace_bytes,
                                 cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The latent cache in 4 bits.  A row of 576 values takes 320 bytes:
+ *   bytes   0..287  e2m1 codes (sign, two exponent bits, one mantissa bit: 0, 0.5,
+ *                   1, 1.5, 2, 3, 4, 6), the even column in the low four bits
+ *   bytes 288..305  shifts, four bits for each block of 16 columns, the even
+ *                   block in the low four; 0..14, and 15 for a block of zeros
+ *   bytes 306..307  0
+ *   bytes 308..311  scale, f32
+ *   bytes 312..319  0
+ *   value = e2m1 * 2^(6 - shift) * scale
+ * e2m1 * 2^(6 - shift) is an e4m3 number for every code and shift, so that
+ * attention reads a row exactly, on the FP8 pipe.
+ * ------------------------------------------------------------------------ */
+
+/* smla_cache_append into a 4-bit cache (D = 576): each finished row r is written as
+ *   scale = largest finite magnitude of r / 384 (1 when that is 0; at least the
+ *           smallest normal f32)
+ *   shift = the largest k in 0..14 for which the block's largest finite magnitude
+ *           times 2^k is at most the row's
+ *   code  = e2m1(r / scale * 2^(shift - 6)), to nearest even, of the f32 quotient
+ * Infinities become the block's +-6; a row with a NaN gets the scale NaN.
+ *   pool  [phys_rows, 320] (output), 16-byte aligned
+ * The other arguments, the order of the steps and the rules as for smla_cache_append. */
+smla_status_t smla_cache_append_fp4(const uint16_t* x, int64_t x_stride, smla_seqs_t seqs, const uint16_t* norm_weight,
+                                    int32_t norm_dim, float norm_eps, smla_rope_t rope, uint8_t* pool,
+                                    int64_t phys_rows, uint16_t* rows_out, int64_t rows_stride, cudaStream_t stream);
+
+/* Reads 4-bit rows back, token by token as smla_cache_gather:
+ *   rows_dtype SMLA_BF16  rows bf16 [T, 576] = bf16(value); row_scales NULL
+ *   rows_dtype SMLA_E4M3  rows e4m3 [T, 576] = e2m1 * 2^(6 - shift) and row_scales f32
+ *                         [T] = the rows' scales: the same values, exactly, in the form
+ *                         that the calls over e4m3 caches read (one scale per row)
+ * rows_stride: elements, >= 576, a multiple of 8 (e4m3: 16).  Alignment: pool
+ * and rows 16 bytes, row_scales 4. */
+smla_status_t smla_cache_gather_fp4(const uint8_t* pool, int64_t phys_rows, smla_seqs_t seqs, void* rows,
+                                    int32_t rows_dtype, int64_t rows_stride, float* row_scales, cudaStream_t stream);
+
+/* smla_dense_decode over a 4-bit cache (latent_pool [phys_rows, 320]); q bf16 or
+ * e4m3.  Accuracy, arguments, workspace and rules as for smla_dense_decode over an
+ * e4m3 cache with one scale per row. */
+smla_status_t smla_dense_decode_fp4(const void* q, int32_t q_dtype, const uint8_t* latent_pool, int64_t phys_rows,
+                                    smla_seqs_t seqs, int32_t max_kv_len, int32_t H, int32_t v_depth,
+                                    float softmax_scale, const float* attn_sink, uint16_t* out, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The projections around the attention calls, in 8 bits: activations with a
+ * scale for each row and 128 columns, weights with one for each 128 x 128
+ * block.
+ * ------------------------------------------------------------------------ */
+
+/* Rows x [M, K] quantised to e4m3: optionally r = x * rsqrt(mean(x^2) + norm_eps) *
+ * norm_weight (else r = x), then for each 128 columns (the last ones may be
+ * fewer)
+ *   scale = largest finite magnitude / 448 (1 when that is 0; at least the smallest
+ *           normal f32),  byte = e4m3(r / scale), of the f32 quotient (below a scale
+ *           of 2^-100, of one that may be off in its last place)
+ * NaN stays NaN and infinities saturate.
+ *   x            bf16, rows x_stride elements apart (a multiple of 8, >= 0)
+ *   norm_weight  bf16 [K], or NULL for no norm
+ *   out          e4m3 [M, K], dense;  scales f32 [M, ceil(K / 128)], dense
+ * K: a multiple of 16, up to 2^20 (16384 with a norm).  Alignment: x,
+ * norm_weight, out 16 bytes; scales 4. */
+smla_status_t smla_quantize_blocks(const uint16_t* x, int64_t x_stride, int32_t M, int32_t K, const uint16_t* norm_weight,
+                                   float norm_eps, uint8_t* out, float* scales, cudaStream_t stream);
+
+/* Batched matrix product of such operands: for g < G, m < M, n < N
+ *   out[g,m,n] = sum_kb a_scales[g,m,kb] * b_scales[g,n/128,kb] *
+ *                sum_{k in block kb of 128} a[g,m,k] * b[g,n,k]
+ * with every sum in f32 (FP8 MMAs, f32 accumulation) and one rounding to out's type.
+ * The product of two scales has to be a normal f32 (or 0).
+ *   a         e4m3 [G, M, K]: element (g, m, k) at a[g * a_group_stride + m * a_row_stride + k]
+ *   a_scales  f32 [G, M, ceil(K / 128)], likewise strided
+ *   b         e4m3 [G, N, K], dense;  b_scales f32 [G, ceil(N / 128), ceil(K / 128)], dense
+ *   out       bf16 or f32 (out_dtype) [G, M, N], strided
+ * A batch of heads is G = heads with the token stride as the row stride: the
+ * projections of queries into the latent space and of attention outputs out of it
+ * need no transposition.  Rows of a past M, and columns of b past K, are not read.
+ * K: a multiple of 16, 16 .. 2^20; N a multiple of 8.  Strides: a's multiples
+ * of 16, out's of 8, at least the row's width; out's rows may not share
+ * memory (its larger stride spans the other dimension).  A stride of a
+ * dimension of one element does not matter.  Alignment: a, b, out 16 bytes; the
+ * scales 4. */
+smla_status_t smla_block_matmul(const uint8_t* a, int64_t a_group_stride, int64_t a_row_stride, const float* a_scales,
+                                int64_t as_group_stride, int64_t as_row_stride, const uint8_t* b, const float* b_scales,
+                                int32_t G, int32_t M, int32_t N, int32_t K, void* out, int32_t out_dtype,
+                                int64_t out_group_stride, int64_t out_row_stride, cudaStream_t stream);
+
 /* Synchronises `stream`, then reads and clears the current device's error
  * word.  Returns SMLA_OK, SMLA_ERR_DEVICE_CHECK (out-of-range index or page
  * id), SMLA_ERR_TIMEOUT (a pipeline wait gave up) or SMLA_ERR_CUDA. */

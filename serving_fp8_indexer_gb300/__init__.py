@@ -29,12 +29,17 @@ from ._latent import (  # noqa: F401
     ROPE_HALF,
     ROPE_INTERLEAVED,
     Rope,
+    block_matmul,
     cache_append,
+    cache_append_fp4,
     cache_gather,
+    cache_gather_fp4,
     dense_decode,
+    dense_decode_fp4,
     dense_decode_workspace_size,
     expanded_prefill,
     expanded_prefill_workspace_size,
+    quantize_blocks,
     rope,
     rope_frequencies,
 )

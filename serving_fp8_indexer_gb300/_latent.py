@@ -1,5 +1,6 @@
 """ctypes binding of the operators around the attention calls (include/smla.h):
-rotary positions and the write and read side of the paged caches.
+rotary positions, the write and read side of the paged caches, attention over
+whole caches and in the expanded form, the 4-bit cache, and the 8-bit projections.
 
 As in ``_lib``: argument marshalling only.  Every function checks its
 tensors' types, layouts, sizes and device before the call, runs on the
@@ -261,6 +262,127 @@ def dense_decode(q: torch.Tensor, latent: torch.Tensor, scales: Optional[torch.T
                                _flat(out, "out", torch.bfloat16, dev, 3),
                                _flat(workspace, "workspace", torch.uint8, dev, 1),
                                0 if workspace is None else workspace.numel(), _on(stream, dev))
+    if st:
+        _check(lib, st)
+    return out
+
+
+FP4_ROW = 320  # bytes of a 4-bit cache row
+
+
+def _fp4_pool(pool, dev: int):
+    """(pointer, rows) of a 4-bit cache."""
+    ptr = _flat(pool, "pool", torch.uint8, dev, 2)
+    if pool.shape[1] != FP4_ROW:
+        raise ValueError(f"a 4-bit pool must be [phys_rows, {FP4_ROW}], got {tuple(pool.shape)}")
+    return ptr, pool.shape[0]
+
+
+def cache_append_fp4(x: torch.Tensor, seqs: Seqs, pool: torch.Tensor, rope: Optional[Rope] = None,
+                     norm_weight: Optional[torch.Tensor] = None, norm_eps: float = 1e-6,
+                     rows_out: Optional[torch.Tensor] = None, stream=None):
+    """cache_append into a 4-bit latent cache: x bf16 [T, 576], pool uint8
+    [phys_rows, 320] (codes, block shifts and the row's scale; include/smla.h)."""
+    lib, dev = _lib._lib or _lib.load(), _device()
+    xp, (T, D), xs = _rows(x, "x", (torch.bfloat16,), dev, 2)
+    rp, rs = None, D
+    if rows_out is not None:
+        rp, rows_shape, rs = _rows(rows_out, "rows_out", (torch.bfloat16,), dev, 2)
+        rs = rs[0]
+        if rows_shape != x.shape:
+            raise ValueError("rows_out must have x's shape")
+    pp, phys_rows = _fp4_pool(pool, dev)
+    if T != seqs.T or D != 576:
+        raise ValueError(f"x {tuple(x.shape)} must be [T={seqs.T}, 576]")
+    st = lib.smla_cache_append_fp4(xp, xs[0], _seqs(seqs, dev), _flat(norm_weight, "norm_weight", torch.bfloat16, dev, 1),
+                                   0 if norm_weight is None else norm_weight.shape[0], norm_eps,
+                                   rope.as_c(dev) if rope is not None else RopeT(), pp, phys_rows, rp, rs, _on(stream, dev))
+    if st:
+        _check(lib, st)
+
+
+def cache_gather_fp4(pool: torch.Tensor, seqs: Seqs, rows: torch.Tensor, row_scales: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """rows[t] = the 4-bit cached row of seqs' token t: bf16 [T, 576], or, with
+    row_scales f32 [T, 1], uint8 (e4m3 bytes) [T, 576], which hold the same
+    values exactly and serve as a pool of the calls over e4m3 caches
+    (scale_block_size 576)."""
+    lib, dev = _lib._lib or _lib.load(), _device()
+    dtype = torch.bfloat16 if row_scales is None else torch.uint8
+    rp, (T, D), rs = _rows(rows, "rows", (dtype,), dev, 2)
+    pp, phys_rows = _fp4_pool(pool, dev)
+    if T != seqs.T or D != 576 or (row_scales is not None and row_scales.shape != (T, 1)):
+        raise ValueError(f"rows {tuple(rows.shape)} must be [T={seqs.T}, 576], row_scales [T, 1]")
+    st = lib.smla_cache_gather_fp4(pp, phys_rows, _seqs(seqs, dev), rp, SMLA_BF16 if row_scales is None else SMLA_E4M3, rs[0],
+                                   _flat(row_scales, "row_scales", torch.float32, dev, 2), _on(stream, dev))
+    if st:
+        _check(lib, st)
+    return rows
+
+
+def dense_decode_fp4(q: torch.Tensor, pool: torch.Tensor, seqs: Seqs, max_kv_len: int, softmax_scale: float,
+                     out: torch.Tensor, workspace: Optional[torch.Tensor], attn_sink: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """dense_decode over a 4-bit latent cache, pool uint8 [phys_rows, 320];
+    workspace of dense_decode_workspace_size() bytes."""
+    lib, dev = _lib._lib or _lib.load(), _device()
+    bf16 = q.dtype is torch.bfloat16
+    qp = _flat(q, "q", torch.bfloat16 if bf16 else torch.uint8, dev, 3)
+    pp, phys_rows = _fp4_pool(pool, dev)
+    T, H, D = q.shape
+    if T != seqs.T or D != 576 or out.shape[:2] != (T, H) or (attn_sink is not None and attn_sink.shape != (H,)):
+        raise ValueError(f"q must be [T={seqs.T}, H, 576], out [T, H, 512], attn_sink [H]")
+    st = lib.smla_dense_decode_fp4(qp, SMLA_BF16 if bf16 else SMLA_E4M3, pp, phys_rows, _seqs(seqs, dev), max_kv_len, H,
+                                   out.shape[2], softmax_scale, _flat(attn_sink, "attn_sink", torch.float32, dev, 1),
+                                   _flat(out, "out", torch.bfloat16, dev, 3),
+                                   _flat(workspace, "workspace", torch.uint8, dev, 1),
+                                   0 if workspace is None else workspace.numel(), _on(stream, dev))
+    if st:
+        _check(lib, st)
+    return out
+
+
+def quantize_blocks(x: torch.Tensor, out: torch.Tensor, scales: torch.Tensor, norm_weight: Optional[torch.Tensor] = None,
+                    norm_eps: float = 1e-6, stream=None):
+    """out uint8 (e4m3 bytes) [M, K] and scales f32 [M, ceil(K / 128)] of x bf16
+    [M, K] (rows may be strided): a scale for each 128 columns, after an RMS norm
+    over the row when its weight bf16 [K] is given."""
+    lib, dev = _lib._lib or _lib.load(), _device()
+    xp, (M, K), xs = _rows(x, "x", (torch.bfloat16,), dev, 2)
+    if out.shape != (M, K) or scales.shape != (M, -(-K // 128)) or (norm_weight is not None and norm_weight.shape != (K,)):
+        raise ValueError(f"out must be [M={M}, K={K}], scales [M, {-(-K // 128)}], norm_weight [K]")
+    st = lib.smla_quantize_blocks(xp, xs[0], M, K, _flat(norm_weight, "norm_weight", torch.bfloat16, dev, 1), norm_eps,
+                                  _flat(out, "out", torch.uint8, dev, 2), _flat(scales, "scales", torch.float32, dev, 2),
+                                  _on(stream, dev))
+    if st:
+        _check(lib, st)
+
+
+def block_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor, out: torch.Tensor,
+                 stream=None) -> torch.Tensor:
+    """out[g] bf16 or f32 [M, N] = a[g] b[g]^T of e4m3 operands with a scale for
+    each block of 128: a uint8 [G, M, K] with a_scales f32 [G, M, ceil(K / 128)]
+    (both may be strided, as heads of a token-major tensor are; out too), b uint8
+    [G, N, K] with b_scales f32 [G, ceil(N / 128), ceil(K / 128)] (contiguous).
+    Without a batch all five are 2-D."""
+    lib, dev = _lib._lib or _lib.load(), _device()
+    n = a.dim()
+    if n == 2:
+        if not (a_scales.dim() == b.dim() == b_scales.dim() == out.dim() == 2):
+            raise ValueError("a, a_scales, b, b_scales and out must all be 2-D or all 3-D")
+        a, a_scales, b, b_scales, out_g = a[None], a_scales[None], b[None], b_scales[None], out[None]
+    else:
+        out_g = out
+    ap, (G, M, K), a_st = _rows(a, "a", (torch.uint8,), dev, 3)
+    sp, s_shape, s_st = _rows(a_scales, "a_scales", (torch.float32,), dev, 3)
+    op, (og, om, N), o_st = _rows(out_g, "out", (torch.bfloat16, torch.float32), dev, 3)
+    kb = -(-K // 128)
+    if (og != G or om != M or s_shape != (G, M, kb) or b.shape != (G, N, K) or b_scales.shape != (G, -(-N // 128), kb)):
+        raise ValueError("a [G, M, K], a_scales [G, M, ceil(K / 128)], b [G, N, K], b_scales [G, ceil(N / 128), ceil(K / "
+                         "128)] and out [G, M, N] do not fit each other")
+    st = lib.smla_block_matmul(ap, a_st[0], a_st[1], sp, s_st[0], s_st[1], _flat(b, "b", torch.uint8, dev, 3),
+                               _flat(b_scales, "b_scales", torch.float32, dev, 3), G, M, N, K, op, _DTYPES[out.dtype], o_st[0],
+                               o_st[1], _on(stream, dev))
     if st:
         _check(lib, st)
     return out

@@ -31,6 +31,8 @@ EXPORTED = ("smla_indexer_scores", "smla_topk_workspace_size", "smla_topk", "sml
             "smla_sparse_decode_noalloc", "smla_rope_frequencies", "smla_rope", "smla_cache_append", "smla_cache_gather",
             "smla_expanded_prefill_workspace_size", "smla_expanded_prefill", "smla_expanded_prefill_terms",
             "smla_dense_decode_workspace_size", "smla_dense_decode",
+            "smla_cache_append_fp4", "smla_cache_gather_fp4", "smla_dense_decode_fp4", "smla_quantize_blocks",
+            "smla_block_matmul",
             "smla_check_device_errors", "smla_selftest_wait_timeout", "smla_last_error", "smla_version")
 
 
@@ -99,6 +101,11 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.smla_dense_decode_workspace_size.argtypes = [i32, i32, i32]
         lib.smla_dense_decode_workspace_size.restype = sz
         lib.smla_dense_decode.argtypes = [vp, i32, vp, i32, i64, vp, i32, SeqsT, i32, i32, i32, f32, vp, vp, vp, sz, vp]
+        lib.smla_cache_append_fp4.argtypes = [vp, i64, SeqsT, vp, i32, f32, RopeT, vp, i64, vp, i64, vp]
+        lib.smla_cache_gather_fp4.argtypes = [vp, i64, SeqsT, vp, i32, i64, vp, vp]
+        lib.smla_dense_decode_fp4.argtypes = [vp, i32, vp, i64, SeqsT, i32, i32, i32, f32, vp, vp, vp, sz, vp]
+        lib.smla_quantize_blocks.argtypes = [vp, i64, i32, i32, vp, f32, vp, vp, vp]
+        lib.smla_block_matmul.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, i32, i32, i32, i32, vp, i32, i64, i64, vp]
         lib.smla_check_device_errors.argtypes = [vp]
         lib.smla_last_error.argtypes = [ctypes.c_char_p, ctypes.c_size_t]
         lib.smla_last_error.restype = ctypes.c_size_t
@@ -108,8 +115,9 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                      "smla_dense_prefill",
                      "smla_sparse_decode", "smla_sparse_decode_noalloc", "smla_rope_frequencies", "smla_rope",
                      "smla_cache_append", "smla_cache_gather", "smla_expanded_prefill",
-                     "smla_expanded_prefill_terms", "smla_dense_decode", "smla_check_device_errors",
-                     "smla_selftest_wait_timeout"):
+                     "smla_expanded_prefill_terms", "smla_dense_decode", "smla_cache_append_fp4",
+                     "smla_cache_gather_fp4", "smla_dense_decode_fp4", "smla_quantize_blocks", "smla_block_matmul",
+                     "smla_check_device_errors", "smla_selftest_wait_timeout"):
             getattr(lib, name).restype = ctypes.c_int
         if path is None:
             _lib = lib

@@ -15,8 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsmla.so")
 SOURCES = ["abi.cu", "indexer.cu", "topk.cu", "indexer_topk.cu", "prefill.cu", "decode.cu", "abi_latent.cu",
            "rope.cu", "cache.cu", "expanded.cu", "dense_decode.cu",
-           "dense_decode_wide.cu"]
-HEADERS = ["ptx.cuh", "rope.cuh", "decode_line.cuh", "smla_internal.h"]
+           "dense_decode_wide.cu", "quantize.cu", "block_matmul.cu"]
+HEADERS = ["ptx.cuh", "rope.cuh", "quantize.cuh", "decode_line.cuh", "smla_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -49,6 +49,29 @@ static smla_status_t check_cache(const void* pool, int32_t pool_dtype, int64_t p
 
 static bool stride8(int64_t s) { return (s & 7) == 0; }
 
+// What both appends check of a row and its way into the cache.
+static smla_status_t check_append(const uint16_t* x, int64_t x_stride, const smla_seqs_t& seqs, int32_t D,
+                                  const uint16_t* norm_weight, int32_t norm_dim, float norm_eps, const smla_rope_t& rope,
+                                  const uint16_t* rows_out, int64_t rows_stride) {
+  const smla_status_t st = check_rope(rope, D);
+  if (st != SMLA_OK) return st;
+  if (norm_weight) {
+    if (norm_dim < 8 || norm_dim > D || norm_dim % 8)
+      return fail(SMLA_ERR_UNSUPPORTED, "norm_dim=%d must be a multiple of 8 in [8, D]", norm_dim);
+    if (!(norm_eps >= 0.f) || !std::isfinite(norm_eps))
+      return fail(SMLA_ERR_INVALID_ARG, "norm_eps must be finite and >= 0");
+    if (!aligned16(norm_weight)) return fail(SMLA_ERR_INVALID_ARG, "norm_weight must be 16-byte aligned");
+  }
+  if (x_stride < D || !stride8(x_stride) || (rows_out && (rows_stride < D || !stride8(rows_stride))))
+    return fail(SMLA_ERR_INVALID_ARG, "x_stride and rows_stride must be multiples of 8, >= D");
+  if (seqs.T == 0) return SMLA_OK;
+  if (!x) return fail(SMLA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || (rows_out && !aligned16(rows_out)))
+    return fail(SMLA_ERR_INVALID_ARG, "x and rows_out must be 16-byte aligned");
+  if (rows_out == x) return fail(SMLA_ERR_INVALID_ARG, "rows_out must not be x");
+  return SMLA_OK;
+}
+
 }  // namespace smla
 
 using namespace smla;
@@ -132,22 +155,8 @@ smla_status_t smla_cache_append(const uint16_t* x, int64_t x_stride, smla_seqs_t
   if (st != SMLA_OK) return st;
   st = check_cache(pool, pool_dtype, phys_rows, scales, scale_block_size, D, seqs.T > 0);
   if (st != SMLA_OK) return st;
-  st = check_rope(rope, D);
-  if (st != SMLA_OK) return st;
-  if (norm_weight) {
-    if (norm_dim < 8 || norm_dim > D || norm_dim % 8)
-      return fail(SMLA_ERR_UNSUPPORTED, "norm_dim=%d must be a multiple of 8 in [8, D]", norm_dim);
-    if (!(norm_eps >= 0.f) || !std::isfinite(norm_eps))
-      return fail(SMLA_ERR_INVALID_ARG, "norm_eps must be finite and >= 0");
-    if (!aligned16(norm_weight)) return fail(SMLA_ERR_INVALID_ARG, "norm_weight must be 16-byte aligned");
-  }
-  if (x_stride < D || !stride8(x_stride) || (rows_out && (rows_stride < D || !stride8(rows_stride))))
-    return fail(SMLA_ERR_INVALID_ARG, "x_stride and rows_stride must be multiples of 8, >= D");
-  if (seqs.T == 0) return SMLA_OK;
-  if (!x) return fail(SMLA_ERR_INVALID_ARG, "null pointer");
-  if (!aligned16(x) || (rows_out && !aligned16(rows_out)))
-    return fail(SMLA_ERR_INVALID_ARG, "x and rows_out must be 16-byte aligned");
-  if (rows_out == x) return fail(SMLA_ERR_INVALID_ARG, "rows_out must not be x");
+  st = check_append(x, x_stride, seqs, D, norm_weight, norm_dim, norm_eps, rope, rows_out, rows_stride);
+  if (st != SMLA_OK || seqs.T == 0) return st;
   unsigned* err = nullptr;
   st = device_err_ptr(&err);
   if (st != SMLA_OK) return st;
@@ -182,6 +191,123 @@ smla_status_t smla_cache_gather(const void* pool, int32_t pool_dtype, int64_t ph
   a.rows = rows;
   a.rows_stride = rows_stride;
   return launch_cache_gather(a, seqs, err, stream);
+}
+
+smla_status_t smla_cache_append_fp4(const uint16_t* x, int64_t x_stride, smla_seqs_t seqs, const uint16_t* norm_weight,
+                                    int32_t norm_dim, float norm_eps, smla_rope_t rope, uint8_t* pool,
+                                    int64_t phys_rows, uint16_t* rows_out, int64_t rows_stride, cudaStream_t stream) {
+  clear_last_error();
+  constexpr int32_t D = 576;
+  smla_status_t st = check_seqs(seqs);
+  if (st != SMLA_OK) return st;
+  st = check_cache(pool, SMLA_E4M3, phys_rows, nullptr, 0, D, seqs.T > 0);
+  if (st != SMLA_OK) return st;
+  st = check_append(x, x_stride, seqs, D, norm_weight, norm_dim, norm_eps, rope, rows_out, rows_stride);
+  if (st != SMLA_OK || seqs.T == 0) return st;
+  unsigned* err = nullptr;
+  st = device_err_ptr(&err);
+  if (st != SMLA_OK) return st;
+  CacheArgs a{x, x_stride, D, norm_weight, norm_dim, norm_eps, rope, pool, SMLA_E4M3, phys_rows, nullptr, 0, rows_out, rows_stride};
+  a.fp4 = true;
+  return launch_cache_append(a, seqs, err, stream);
+}
+
+smla_status_t smla_cache_gather_fp4(const uint8_t* pool, int64_t phys_rows, smla_seqs_t seqs, void* rows,
+                                    int32_t rows_dtype, int64_t rows_stride, float* row_scales, cudaStream_t stream) {
+  clear_last_error();
+  constexpr int32_t D = 576;
+  smla_status_t st = check_seqs(seqs);
+  if (st != SMLA_OK) return st;
+  if (rows_dtype != SMLA_BF16 && rows_dtype != SMLA_E4M3)
+    return fail(SMLA_ERR_INVALID_ARG, "rows_dtype=%d must be bf16 or e4m3", rows_dtype);
+  st = check_cache(pool, SMLA_E4M3, phys_rows, nullptr, 0, D, seqs.T > 0);
+  if (st != SMLA_OK) return st;
+  const bool e4m3 = rows_dtype == SMLA_E4M3;
+  if (rows_stride < D || rows_stride % (e4m3 ? 16 : 8))
+    return fail(SMLA_ERR_INVALID_ARG, "rows_stride must be a multiple of 8 (e4m3: 16), >= 576");
+  if (seqs.T == 0) return SMLA_OK;
+  if (!rows || e4m3 != (row_scales != nullptr))
+    return fail(SMLA_ERR_INVALID_ARG, "rows must be non-null; row_scales non-null for e4m3 rows, and for them alone");
+  if (!aligned16(rows) || !aligned4(row_scales))
+    return fail(SMLA_ERR_INVALID_ARG, "rows must be 16-byte aligned; row_scales 4-byte aligned");
+  unsigned* err = nullptr;
+  st = device_err_ptr(&err);
+  if (st != SMLA_OK) return st;
+  CacheArgs a{};
+  a.D = D;
+  a.pool = const_cast<uint8_t*>(pool);
+  a.phys_rows = phys_rows;
+  a.rows = rows;
+  a.rows_stride = rows_stride;
+  a.fp4 = true;
+  a.row_scales = row_scales;
+  return launch_cache_gather(a, seqs, err, stream);
+}
+
+smla_status_t smla_quantize_blocks(const uint16_t* x, int64_t x_stride, int32_t M, int32_t K, const uint16_t* norm_weight,
+                                   float norm_eps, uint8_t* out, float* scales, cudaStream_t stream) {
+  clear_last_error();
+  if (M < 0) return fail(SMLA_ERR_INVALID_ARG, "M=%d must be >= 0", M);
+  if (K < 16 || K > (1 << 20) || K % 16)
+    return fail(SMLA_ERR_UNSUPPORTED, "K=%d must be a multiple of 16 in [16, 2^20]", K);
+  if (norm_weight) {
+    if (K > 16384) return fail(SMLA_ERR_UNSUPPORTED, "K=%d: at most 16384 with a norm", K);
+    if (!(norm_eps >= 0.f) || !std::isfinite(norm_eps))
+      return fail(SMLA_ERR_INVALID_ARG, "norm_eps must be finite and >= 0");
+    if (!aligned16(norm_weight)) return fail(SMLA_ERR_INVALID_ARG, "norm_weight must be 16-byte aligned");
+  }
+  if (x_stride < 0 || !stride8(x_stride)) return fail(SMLA_ERR_INVALID_ARG, "x_stride must be a multiple of 8, >= 0");
+  if (M == 0) return SMLA_OK;
+  if (!x || !out || !scales) return fail(SMLA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || !aligned16(out) || !aligned4(scales))
+    return fail(SMLA_ERR_INVALID_ARG, "x and out must be 16-byte aligned; scales 4-byte aligned");
+  if (static_cast<int64_t>(M) * ((K + 255) / 256) >= (int64_t(1) << 31))
+    return fail(SMLA_ERR_UNSUPPORTED, "M=%d rows of K=%d columns are too much for one call", M, K);
+  const QuantizeArgs a{x, x_stride, M, K, norm_weight, norm_eps, out, scales};
+  return launch_quantize(a, stream);
+}
+
+smla_status_t smla_block_matmul(const uint8_t* a, int64_t a_group_stride, int64_t a_row_stride, const float* a_scales,
+                                int64_t as_group_stride, int64_t as_row_stride, const uint8_t* b, const float* b_scales,
+                                int32_t G, int32_t M, int32_t N, int32_t K, void* out, int32_t out_dtype,
+                                int64_t out_group_stride, int64_t out_row_stride, cudaStream_t stream) {
+  clear_last_error();
+  if (G < 0 || M < 0 || N < 0) return fail(SMLA_ERR_INVALID_ARG, "G=%d M=%d N=%d must be >= 0", G, M, N);
+  if (K < 16 || K > (1 << 20) || K % 16)
+    return fail(SMLA_ERR_UNSUPPORTED, "K=%d must be a multiple of 16 in [16, 2^20]", K);
+  if (N % 8) return fail(SMLA_ERR_UNSUPPORTED, "N=%d must be a multiple of 8", N);
+  constexpr int32_t kMost = 1 << 30;
+  if (M > kMost || N > kMost || G > kMost) return fail(SMLA_ERR_UNSUPPORTED, "G, M and N must be at most 2^30");
+  if (out_dtype != SMLA_BF16 && out_dtype != SMLA_F32)
+    return fail(SMLA_ERR_INVALID_ARG, "out_dtype=%d must be bf16 or f32", out_dtype);
+  const auto wide_enough = [](int64_t n, int64_t s, int64_t width) { return n <= 1 || s >= width; };
+  constexpr int64_t kFar = int64_t(1) << 38;
+  if (!wide_enough(M, a_row_stride, K) || !wide_enough(G, a_group_stride, K) || a_row_stride % 16 || a_group_stride % 16 ||
+      a_row_stride >= kFar || a_group_stride >= kFar)
+    return fail(SMLA_ERR_INVALID_ARG, "a's strides must be multiples of 16 below 2^38, at least K");
+  if (as_group_stride < 0 || as_row_stride < 0) return fail(SMLA_ERR_INVALID_ARG, "a_scales' strides must be >= 0");
+  if (!wide_enough(M, out_row_stride, N) || !wide_enough(G, out_group_stride, N) || !stride8(out_row_stride) ||
+      !stride8(out_group_stride) || out_row_stride >= kFar || out_group_stride >= kFar)
+    return fail(SMLA_ERR_INVALID_ARG, "out's strides must be multiples of 8 below 2^38, at least N");
+  if (G == 0 || M == 0 || N == 0) return SMLA_OK;
+  // rows of different batches share no memory: one of the two strides spans the other's range
+  const __int128 rows_span = static_cast<__int128>(M - 1) * out_row_stride + N;
+  const __int128 groups_span = static_cast<__int128>(G - 1) * out_group_stride + N;
+  if (G > 1 && M > 1 && out_group_stride < rows_span && out_row_stride < groups_span)
+    return fail(SMLA_ERR_INVALID_ARG, "out's rows must not share memory");
+  if (!a || !a_scales || !b || !b_scales || !out) return fail(SMLA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(a) || !aligned16(b) || !aligned16(out) || !aligned4(a_scales) || !aligned4(b_scales))
+    return fail(SMLA_ERR_INVALID_ARG, "a, b and out must be 16-byte aligned; a_scales and b_scales 4-byte aligned");
+  if (static_cast<__int128>(N) * K >= kFar)
+    return fail(SMLA_ERR_UNSUPPORTED, "N=%d K=%d: b's matrices must be smaller than 2^38 bytes", N, K);
+  if (static_cast<__int128>(G) * ((M + 15) / 16) * ((N + 127) / 128) >= (1 << 28))
+    return fail(SMLA_ERR_UNSUPPORTED, "G=%d M=%d N=%d are too much for one call", G, M, N);
+  unsigned* err = nullptr;
+  const smla_status_t st = device_err_ptr(&err);
+  if (st != SMLA_OK) return st;
+  const MatmulArgs args{a, a_group_stride, a_row_stride, a_scales, as_group_stride, as_row_stride, b, b_scales, G, M, N, K,
+                        out, out_dtype, out_group_stride, out_row_stride};
+  return launch_block_matmul(args, err, stream);
 }
 
 size_t smla_expanded_prefill_workspace_size(int32_t T, int32_t S, int32_t B, int32_t H) {
@@ -248,12 +374,11 @@ size_t smla_dense_decode_workspace_size(int32_t T, int32_t H, int32_t max_kv_len
   return dense_decode_workspace_bytes(T, H, max_kv_len);
 }
 
-smla_status_t smla_dense_decode(const void* q, int32_t q_dtype, const void* latent_pool, int32_t pool_dtype,
-                                int64_t phys_rows, const float* scales, int32_t scale_block_size, smla_seqs_t seqs,
-                                int32_t max_kv_len, int32_t H, int32_t v_depth, float softmax_scale,
-                                const float* attn_sink, uint16_t* out, void* workspace, size_t workspace_bytes,
-                                cudaStream_t stream) {
-  clear_last_error();
+static smla_status_t dense_decode(const void* q, int32_t q_dtype, const void* latent_pool, int32_t pool_dtype,
+                                  int64_t phys_rows, const float* scales, int32_t scale_block_size, bool fp4,
+                                  smla_seqs_t seqs, int32_t max_kv_len, int32_t H, int32_t v_depth, float softmax_scale,
+                                  const float* attn_sink, uint16_t* out, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream) {
   smla_status_t st = check_seqs(seqs);
   if (st != SMLA_OK) return st;
   if (pool_dtype != SMLA_BF16 && pool_dtype != SMLA_E4M3)
@@ -275,11 +400,30 @@ smla_status_t smla_dense_decode(const void* q, int32_t q_dtype, const void* late
   if (st != SMLA_OK) return st;
   const DenseDecodeArgs d{q,    q_dtype, latent_pool, phys_rows,     scale_block_size == 0 ? nullptr : scales,
                           &seqs, T,       H,           max_kv_len,    softmax_scale,
-                          attn_sink, out, workspace};
+                          attn_sink, out, workspace, fp4};
   // scales by the row (or none) leave the bytes as MMA operands; the others
   // take 16-bit ones
   const bool wide = pool_dtype == SMLA_BF16 || scale_block_size == 32;
   return wide ? launch_dense_decode_wide(d, err, stream) : launch_dense_decode(d, err, stream);
+}
+
+smla_status_t smla_dense_decode(const void* q, int32_t q_dtype, const void* latent_pool, int32_t pool_dtype,
+                                int64_t phys_rows, const float* scales, int32_t scale_block_size, smla_seqs_t seqs,
+                                int32_t max_kv_len, int32_t H, int32_t v_depth, float softmax_scale,
+                                const float* attn_sink, uint16_t* out, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream) {
+  clear_last_error();
+  return dense_decode(q, q_dtype, latent_pool, pool_dtype, phys_rows, scales, scale_block_size, false, seqs, max_kv_len, H,
+                      v_depth, softmax_scale, attn_sink, out, workspace, workspace_bytes, stream);
+}
+
+smla_status_t smla_dense_decode_fp4(const void* q, int32_t q_dtype, const uint8_t* latent_pool, int64_t phys_rows,
+                                    smla_seqs_t seqs, int32_t max_kv_len, int32_t H, int32_t v_depth,
+                                    float softmax_scale, const float* attn_sink, uint16_t* out, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream) {
+  clear_last_error();
+  return dense_decode(q, q_dtype, latent_pool, SMLA_E4M3, phys_rows, nullptr, 0, true, seqs, max_kv_len, H, v_depth,
+                      softmax_scale, attn_sink, out, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -23,14 +23,13 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "quantize.cuh"
 #include "rope.cuh"
 
 namespace smla {
 namespace ca {
 
 constexpr int kWarps = 4;
-
-constexpr float kE4m3Max = 448.f;
 
 struct AppendParams {
   const __nv_bfloat16* x;
@@ -51,30 +50,7 @@ struct AppendParams {
   unsigned* err;
 };
 
-enum Mode { kBf16 = 0, kUnit = 1, kRow = 2, kBlock = 3 };
-
-__device__ __forceinline__ float finite_abs(float v) {
-  const float a = fabsf(v);
-  return a < INFINITY ? a : 0.f;  // false for NaN
-}
-// The scale that maps `amax` to e4m3's largest value; 1 for an all-zero
-// block, and never below the smallest normal number (so that x / scale and
-// byte * scale stay finite).
-__device__ __forceinline__ float scale_of(float amax) {
-  return amax > 0.f ? fmaxf(amax / kE4m3Max, 1.17549435e-38f) : 1.f;
-}
-
-// v / scale, rounded once: the product with the rounded reciprocal is off by up to
-// 1.5 units in the last place, and a quotient on the border between two bytes then
-// fell to the wrong side.  One step with the exact remainder mends that (Markstein,
-// IBM J. Res. Dev. 34, 1990): 12 117 block-scaled rows 13.0 -> 13.75 us, by a
-// division each 15.3.  (The remainder is exact while scale >= 2^-100.)  Without one
-// to speak of, as for infinities, NaN and zeros, the product stands.
-__device__ __forceinline__ float quotient(float v, float scale, float inv) {
-  const float q = v * inv;
-  const float r = fmaf(-q, scale, v);
-  return fabsf(r) > 0.f ? fmaf(r, inv, q) : q;
-}
+enum Mode { kBf16 = 0, kUnit = 1, kRow = 2, kBlock = 3, kFp4 = 4 };
 
 // kSlots: 8-element chunks a lane holds.  Ten CTAs an SM (48 registers instead
 // of 64) hide more of the rows' latency, 13.5 -> 13.0 us; four slots would spill.
@@ -175,6 +151,49 @@ __global__ void __launch_bounds__(32 * kWarps, kSlots <= 3 ? 10 : 1) append_kern
     return;
   }
   float scale = 1.f, inv = 1.f;
+  if constexpr (MODE == kFp4) {
+    // (chunks past the row's 72 hold zeros)
+    float top[kSlots], most = 0.f;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      top[i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        top[i] = fmaxf(top[i], finite_abs(v[i][k]));
+        nan |= v[i][k] != v[i][k];
+      }
+      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));  // two lanes hold a block
+      most = fmaxf(most, top[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 1; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    scale = scale_of(most, kFp4Top);
+    inv = 1.f / scale;
+    uint8_t* dst = static_cast<uint8_t*>(p.pool) + row * kFp4Row;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      const int c = lane + 32 * i;
+      const int k = fp4_shift(top[i], most);
+      const float unit = __uint_as_float(static_cast<uint32_t>(127 + k - 6) << 23);
+      float q[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = quotient(v[i][e], scale, inv) * unit;
+      const int odd = __shfl_down_sync(0xffffffffu, k, 2);  // the next block's
+      if (c < p.chunks) {
+        *reinterpret_cast<uint32_t*>(dst + c * 4) = pack_e2m1x8(q);
+        if ((c & 3) == 0) dst[kFp4Shifts + (c >> 2)] = static_cast<uint8_t>(k | odd << 4);
+      }
+    }
+    if (__any_sync(0xffffffffu, nan)) scale = NAN;  // e2m1 has none: the whole row's values are
+    if (lane == 0) {
+      *reinterpret_cast<uint16_t*>(dst + kFp4Scale - 2) = 0;
+      *reinterpret_cast<float*>(dst + kFp4Scale) = scale;
+      *reinterpret_cast<uint32_t*>(dst + kFp4Scale + 4) = 0;
+      *reinterpret_cast<uint32_t*>(dst + kFp4Scale + 8) = 0;
+    }
+    return;
+  }
   if (MODE == kRow) {
     float amax = 0.f;
 #pragma unroll
@@ -222,12 +241,26 @@ struct GatherParams {
   int T, chunks;
   uint32_t magic;  // ceil(2^32 / chunks)
   int rows_per_cta;
-  __nv_bfloat16* rows;
+  __nv_bfloat16* rows;  // (4-bit cache: or e4m3 bytes)
   int64_t rows_stride;
+  float* row_scales;  // of e4m3 rows
   unsigned* err;
 };
 
 constexpr int kMaxGatherRows = 32;
+
+// Physical rows of the nr tokens from t0 on (-1: none), by one warp.
+__device__ __forceinline__ void find_rows(const GatherParams& p, int t0, int nr, int64_t* s_row) {
+  const int lane = threadIdx.x, t = t0 + lane;
+  int b = warp_seq_of(p.seqs.cu_q, p.seqs.B, t0, lane);
+  if (lane < nr) {
+    if (b < 0) b = p.seqs.cu_q[0] > t0 ? 0 : p.seqs.B;  // before the first sequence, or behind the last
+    while (b < p.seqs.B && p.seqs.cu_q[b + 1] <= t) ++b;
+    s_row[lane] = b >= p.seqs.B || p.seqs.cu_q[b] > t
+                      ? -1
+                      : key_phys_row(p.seqs, b, token_pos(p.seqs, b, t), p.phys_rows, p.err);
+  }
+}
 
 // A CTA takes up to 32 consecutive tokens: a warp finds the first one's
 // sequence, then each lane steps to its own token's (few steps, mostly none)
@@ -239,17 +272,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
   __shared__ int64_t s_row[kMaxGatherRows];
   const int t0 = blockIdx.x * p.rows_per_cta;
   const int nr = min(p.rows_per_cta, p.T - t0);
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x, t = t0 + lane;
-    int b = warp_seq_of(p.seqs.cu_q, p.seqs.B, t0, lane);
-    if (lane < nr) {
-      if (b < 0) b = p.seqs.cu_q[0] > t0 ? 0 : p.seqs.B;  // before the first sequence, or behind the last
-      while (b < p.seqs.B && p.seqs.cu_q[b + 1] <= t) ++b;
-      s_row[lane] = b >= p.seqs.B || p.seqs.cu_q[b] > t
-                        ? -1
-                        : key_phys_row(p.seqs, b, token_pos(p.seqs, b, t), p.phys_rows, p.err);
-    }
-  }
+  if (threadIdx.x < 32) find_rows(p, t0, nr, s_row);
   __syncthreads();
   const int n = nr * p.chunks;
   constexpr int kBatch = 5;  // loads of a thread in flight (a full CTA of 576-wide rows has nine)
@@ -291,7 +314,65 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
   }
 }
 
+// The same for a 4-bit cache, by blocks of 16 columns: 8 bytes of codes and a
+// shift become 16 e4m3 bytes by a table, stored as they are (with the row's
+// scale) or times the scale in bf16.
+template <bool E4M3>
+__global__ void __launch_bounds__(kGatherThreads) gather_fp4_kernel(const GatherParams p) {
+  __shared__ int64_t s_row[kMaxGatherRows];
+  __shared__ uint2 s_table[16];
+  const int t0 = blockIdx.x * p.rows_per_cta;
+  const int nr = min(p.rows_per_cta, p.T - t0);
+  if (threadIdx.x < 32) find_rows(p, t0, nr, s_row);
+  if (threadIdx.x >= 32 && threadIdx.x < 48) s_table[threadIdx.x - 32] = fp4_table_entry(threadIdx.x - 32);
+  __syncthreads();
+  const int n = nr * kFp4Blocks;
+  constexpr int kBatch = 5;
+  for (int i0 = threadIdx.x; i0 < n; i0 += kBatch * kGatherThreads) {
+    uint2 raw[kBatch];
+    float sc[kBatch];
+    int sh[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kGatherThreads, r = i / kFp4Blocks, c = i - r * kFp4Blocks;
+      const int64_t row = i < n ? s_row[r] : -1;
+      raw[k] = make_uint2(0u, 0u);
+      sc[k] = 1.f;
+      sh[k] = 0;
+      if (row < 0) continue;
+      const uint8_t* at = static_cast<const uint8_t*>(p.pool) + row * kFp4Row;
+      raw[k] = __ldcs(reinterpret_cast<const uint2*>(at + c * 8));
+      sh[k] = at[kFp4Shifts + (c >> 1)] >> (4 * (c & 1)) & 15;
+      sc[k] = *reinterpret_cast<const float*>(at + kFp4Scale);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kGatherThreads, r = i / kFp4Blocks, c = i - r * kFp4Blocks;
+      if (i >= n || s_row[r] < 0) continue;
+      const uint2 t = s_table[sh[k]];
+      const uint2 a = fp4x8_to_e4m3x8(raw[k].x, t), b = fp4x8_to_e4m3x8(raw[k].y, t);
+      if constexpr (E4M3) {
+        uint8_t* dst = reinterpret_cast<uint8_t*>(p.rows) + (t0 + r) * p.rows_stride + c * 16;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(a.x, a.y, b.x, b.y);
+        if (c == 0) p.row_scales[t0 + r] = sc[k];
+      } else {
+        uint4* dst = reinterpret_cast<uint4*>(p.rows + (t0 + r) * p.rows_stride + c * 16);
+        float v[8];
+        unpack_e4m3x8(a, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= sc[k];
+        dst[0] = pack_bf16x8(v);
+        unpack_e4m3x8(b, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= sc[k];
+        dst[1] = pack_bf16x8(v);
+      }
+    }
+  }
+}
+
 static Mode mode_of(const CacheArgs& a) {
+  if (a.fp4) return kFp4;
   if (a.pool_dtype == SMLA_BF16) return kBf16;
   return a.sbs == 0 ? kUnit : a.sbs >= a.D ? kRow : kBlock;
 }
@@ -330,6 +411,9 @@ smla_status_t launch_cache_append(const CacheArgs& a, const smla_seqs_t& seqs, u
       case kUnit: append_kernel<kUnit, N><<<grid, 32 * kWarps, smem, stream>>>(p); break;
       case kRow: append_kernel<kRow, N><<<grid, 32 * kWarps, smem, stream>>>(p); break;
       case kBlock: append_kernel<kBlock, N><<<grid, 32 * kWarps, smem, stream>>>(p); break;
+      case kFp4:
+        if constexpr (N == 3) append_kernel<kFp4, 3><<<grid, 32 * kWarps, smem, stream>>>(p);  // (its rows are 576 wide)
+        break;
     }
   };
   switch ((p.chunks + 31) / 32) {
@@ -357,6 +441,7 @@ smla_status_t launch_cache_gather(const CacheArgs& a, const smla_seqs_t& seqs, u
   p.rows_per_cta = seqs.T >= 2 * device_sm_count() * kMaxGatherRows ? kMaxGatherRows : 8;
   p.rows = static_cast<__nv_bfloat16*>(a.rows);
   p.rows_stride = a.rows_stride;
+  p.row_scales = a.row_scales;
   p.err = err;
   const unsigned grid = (static_cast<unsigned>(seqs.T) + p.rows_per_cta - 1) / p.rows_per_cta;
   switch (mode_of(a)) {
@@ -364,6 +449,12 @@ smla_status_t launch_cache_gather(const CacheArgs& a, const smla_seqs_t& seqs, u
     case kUnit: gather_kernel<kUnit><<<grid, kGatherThreads, 0, stream>>>(p); break;
     case kRow: gather_kernel<kRow><<<grid, kGatherThreads, 0, stream>>>(p); break;
     case kBlock: gather_kernel<kBlock><<<grid, kGatherThreads, 0, stream>>>(p); break;
+    case kFp4:
+      if (a.row_scales)
+        gather_fp4_kernel<true><<<grid, kGatherThreads, 0, stream>>>(p);
+      else
+        gather_fp4_kernel<false><<<grid, kGatherThreads, 0, stream>>>(p);
+      break;
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "cache gather launch");

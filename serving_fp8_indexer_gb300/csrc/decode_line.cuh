@@ -31,6 +31,7 @@ struct Params {
   SeqsDev seqs;
   int64_t phys_rows;
   const float* scales;  // [phys_rows] or null
+  const uint8_t* pool;  // 4-bit cache: its rows
   int T, H;
   int tok_per_item;     // tokens of an item, 1 where a token's heads fill one
   int groups, group_rows;  // head groups of a token, and their heads
@@ -377,6 +378,7 @@ inline Params decode_params(const DenseDecodeArgs& a, int tok_per_item, int grou
   p.seqs = seqs_dev(*a.seqs);
   p.phys_rows = a.phys_rows;
   p.scales = a.scales;
+  p.pool = static_cast<const uint8_t*>(a.latent);
   p.T = a.T;
   p.H = a.H;
   p.tok_per_item = tok_per_item;

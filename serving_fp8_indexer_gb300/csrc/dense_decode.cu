@@ -54,6 +54,7 @@
 #include <type_traits>
 
 #include "decode_line.cuh"
+#include "quantize.cuh"
 
 namespace smla {
 namespace dd {
@@ -69,6 +70,18 @@ constexpr int kPRow = kBK * 64;          // a term of P^T, 64 bytes a key
 // this many blocks.
 constexpr int kItemCost = 5;
 
+enum Cache { kUnitScale, kRowScale, kFourBit };
+// Over a 4-bit cache: further warps, which fetch the rows and turn them into e4m3
+// ones, and a register split.  Up to 32 rows eight of them, four for each half of a
+// block's keys (the launch's 640 x 96 registers are 128 x (2 x 112 + 64 + 2 x 96));
+// the 64-row softmax leaves registers for four, which take the halves in turn (512
+// x 128 are 128 x (2 x 168 + 72 + 104)).
+constexpr int kConvWarp = 12;
+constexpr int kConvPer = kHalf * 18 / 128;  // 16-byte pieces of half a block for each of 128 threads
+__host__ __device__ constexpr int conv_groups(int nr) { return nr == 64 ? 1 : 2; }
+constexpr int threads_of(Cache c, int nr) { return c == kFourBit ? kThreads + 128 * conv_groups(nr) : kThreads; }
+constexpr int fp4_regs(int nr) { return nr == 64 ? 128 : 96; }
+
 template <int NR, int QP>
 struct Smem {
   uint8_t q[QP * NR * kD];  // [4][QP * NR rows][128] then [QP * NR][64]: hi rows, then lo rows
@@ -83,6 +96,7 @@ struct Smem {
   int mx[NR];
   float sums[4][NR];           // row sums of each quarter of the key lanes
   int nk[NR];                  // keys each row sees
+  uint2 table[16];             // 4-bit cache: e4m3 bytes by shift
   unsigned long long bar_qraw, bar_q, bar_full[kNST], bar_empty[kNST][2];
   unsigned long long bar_s[2], bar_s_free[2], bar_p[2][2], bar_more[2], bar_pv[2], bar_drain[2];
   uint32_t tmem_base;
@@ -112,11 +126,12 @@ __device__ __forceinline__ void split3(float a, float b, uint16_t& t1, uint16_t&
   t3 = f16x2_to_e5m2x2(hsub2(h, e5m2x2_to_f16x2(t2)));
 }
 
-template <int NR, int QP, bool ROWSCALE>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int NR, int QP, Cache CACHE>
+__global__ void __launch_bounds__(threads_of(CACHE, NR), 1)
     decode_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tqr,
                   const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tr, const Params p) {
   using S = Smem<NR, QP>;
+  constexpr bool ROWSCALE = CACHE != kUnitScale;
   constexpr int kQN = QP * NR;                 // QK's N
   constexpr int kQChunk = kQN * 128;           // a 128-column chunk of Q
   constexpr int kParts = NR == 64 ? 1 : 3;     // accumulators of a V tile: one for each term, or one for all
@@ -137,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&s.bar_qraw), 1);
     mbar_init(smem_u32(&s.bar_q), kSoftThreads);
     for (int i = 0; i < kNST; ++i) {
-      mbar_init(smem_u32(&s.bar_full[i]), 1);
+      mbar_init(smem_u32(&s.bar_full[i]), CACHE == kFourBit ? 8 : 1);
       mbar_init(smem_u32(&s.bar_empty[i][0]), 1);
       mbar_init(smem_u32(&s.bar_empty[i][1]), 1);
     }
@@ -160,10 +175,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (the descriptors' and the line's cold reads overlap)
   if (threadIdx.x == kTmaWarp * 32) {
     tma_prefetch_desc(&tq);
-    tma_prefetch_desc(&tk);
-    tma_prefetch_desc(&tr);
+    if (CACHE != kFourBit) {
+      tma_prefetch_desc(&tk);
+      tma_prefetch_desc(&tr);
+    }
     if (QP == 1) tma_prefetch_desc(&tqr);
   }
+  if (CACHE == kFourBit && warp == kConvWarp && lane < 16) s.table[lane] = fp4_table_entry(lane);
   const Cursor start = find_part(p, lane);  // this CTA's part of the line
   tc_fence_before();
   __syncthreads();
@@ -188,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // nothing left of the line for this CTA
   } else if (warp < 8) {
     // ===================================================== softmax, epilogue
+    if constexpr (CACHE == kFourBit) setmaxnreg_inc<(NR == 64 ? 168 : 112)>();
     const int r = threadIdx.x & 127;    // key lane
     const int hb = (warp >> 2) * NC;    // rows [hb, hb + NC)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -285,7 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto key_scale = [&](const Seg& g, int j, int pid) -> float {
       const int key = (g.j0 + j) * kBK + r;
       const int64_t row = (static_cast<int64_t>(pid) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
-      return !ROWSCALE || pid < 0 || row >= p.phys_rows ? 1.f : p.scales[row];
+      if (!ROWSCALE || pid < 0 || row >= p.phys_rows) return 1.f;
+      return CACHE == kFourBit ? *reinterpret_cast<const float*>(p.pool + row * kFp4Row + kFp4Scale) : p.scales[row];
     };
     Cursor cur = start;
     Seg g;
@@ -444,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint2*>(p_row + sw64(r, 1) + hb) = make_uint2(pack(t2), pack(t2 + 2));
           *reinterpret_cast<uint2*>(p_row + sw64(r, 2) + hb) = make_uint2(pack(t3), pack(t3 + 2));
         }
-        if (edge && key >= n_item) {
+        if (CACHE != kFourBit && edge && key >= n_item) {
           // nobody's key: whatever lies there must not meet a weight of 0
           for (int c = (warp >> 2); c < 32; c += 2)
             *reinterpret_cast<uint4*>(s.kv[slot] + (c >> 3) * kChunk + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -564,7 +584,115 @@ __global__ void __launch_bounds__(kThreads, 1)
       cur = cn;
       g = gn;
     }
-  } else if (warp == kTmaWarp) {
+  } else if (CACHE == kFourBit && warp >= kConvWarp) {
+    // ================================================== key blocks, 4-bit rows
+    // Four warps take half a block's keys at a time.  A thread holds nine 16-byte
+    // pieces (32 columns) of its next half in registers, fetched as it spends
+    // those of the one before: rows are read as they lie in memory, 320 bytes
+    // a key, whatever the page size.  A piece becomes 32 e4m3 bytes, of which the
+    // lanes of odd 128-column chunks store the second sixteen first: eight
+    // neighbouring lanes then meet all banks.
+    setmaxnreg_dec<(NR == 64 ? 104 : 96)>();
+    const int ct = (warp - kConvWarp) % 4 * 32 + lane;
+    int half = (warp - kConvWarp) >> 2;  // of the keys that are fetched next
+    Cursor cur = start;
+    Seg g;
+    int j = 0;
+    bool live = next_seg(p, cur, g);
+    // Page of eight keys of the half for each of the first eight lanes (-1:
+    // none).  A bad one is reported, and its keys read as zeros.
+    const auto read_page = [&]() -> int {
+      const int key = (g.j0 + j) * kBK + half * kHalf + lane * 8;
+      if (lane >= kHalf / 8 || key >= seg_keys(g)) return -1;
+      const int pid = p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)];
+      const int64_t row = (static_cast<int64_t>(pid) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
+      if (pid < 0 || row + min(8, seg_keys(g) - key) > p.phys_rows) {
+        atomicOr(p.err, kErrPage);
+        if (pid < 0) return -1;
+      }
+      return pid;
+    };
+    uint4 v[kConvPer];
+    uint32_t sh[kConvPer];
+    // Passes 0..7: eight rows of sixteen pieces, the row's place in the swizzle the
+    // same in each; pass 8: the two rotary pieces of all 64 rows.
+    const int r0 = ct >> 4, c0 = ct & 15, r8 = ct >> 1, c8 = 16 + (ct & 1);
+    const auto fetch = [&](int k, int pid_l) {
+      const int r = k < 8 ? 8 * k + r0 : r8, c = k < 8 ? c0 : c8;
+      const int key = (g.j0 + j) * kBK + half * kHalf + r;
+      const int pid = __shfl_sync(0xffffffffu, pid_l, k < 8 ? k : r8 >> 3);
+      const int64_t row = (static_cast<int64_t>(pid) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
+      v[k] = make_uint4(0u, 0u, 0u, 0u);
+      sh[k] = 0;
+      if (pid >= 0 && key < seg_keys(g) && row < p.phys_rows) {
+        const uint8_t* at = p.pool + row * kFp4Row;
+        v[k] = *reinterpret_cast<const uint4*>(at + c * 16);
+        sh[k] = at[kFp4Shifts + c];
+      }
+    };
+    // where a pass's two sixteens go: in the odd 128-column chunks the second first
+    const int odd = (c0 >> 2) & 1, piece = 2 * (c0 & 3);
+    const uint32_t first = (c0 >> 2) * kChunk + sw128(r0, piece + odd);
+    const uint32_t second = (c0 >> 2) * kChunk + sw128(r0, piece + 1 - odd);
+    const uint32_t rope0 = kRopeOff + sw64(r8, 2 * (ct & 1)), rope1 = kRopeOff + sw64(r8, 2 * (ct & 1) + 1);
+    const auto advance = [&] {
+      if (conv_groups(NR) == 1) {
+        half ^= 1;
+        if (half) return;  // the same block's second half
+      }
+      if (++j == g.nb) {
+        j = 0;
+        live = next_seg(p, cur, g);
+      }
+    };
+    bool have = live;
+    int pid = live ? read_page() : -1;
+    if (live) {
+#pragma unroll
+      for (int k = 0; k < kConvPer; ++k) fetch(k, pid);
+      advance();
+      if (live) pid = read_page();
+    }
+    for (int n = 0; have; ++n) {
+      const int i = conv_groups(NR) == 1 ? n >> 1 : n, slot = i % kNST;
+      const int h = conv_groups(NR) == 1 ? n & 1 : (warp - kConvWarp) >> 2;  // of the keys that are converted
+      const bool next = live;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_empty[slot][h]), ((i / kNST) & 1) ^ 1, p.err))) break;
+      uint8_t* kv = s.kv[slot] + h * (kHalf * 128);
+      uint8_t* kv_rope = s.kv[slot] + h * (kHalf * 64);
+#pragma unroll
+      for (int k = 0; k < kConvPer; ++k) {
+        const uint2 t0 = s.table[sh[k] & 15], t1 = s.table[sh[k] >> 4];
+        const uint2 a = fp4x8_to_e4m3x8(v[k].x, t0), b = fp4x8_to_e4m3x8(v[k].y, t0);
+        const uint2 d = fp4x8_to_e4m3x8(v[k].z, t1), e = fp4x8_to_e4m3x8(v[k].w, t1);
+        const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
+        if (next) fetch(k, pid);
+        if (k < 8) {
+          *reinterpret_cast<uint4*>(kv + first + k * 1024) = odd ? hi : lo;
+          *reinterpret_cast<uint4*>(kv + second + k * 1024) = odd ? lo : hi;
+        } else {
+          *reinterpret_cast<uint4*>(kv_rope + rope0) = lo;
+          *reinterpret_cast<uint4*>(kv_rope + rope1) = hi;
+        }
+      }
+      fence_proxy_async_smem();
+      warp_arrive(smem_u32(&s.bar_full[slot]), lane);
+      have = next;
+      if (next) {
+        advance();
+        if (live) pid = read_page();
+      }
+    }
+  } else {
+    if constexpr (CACHE == kFourBit) setmaxnreg_dec<(NR == 64 ? 72 : 64)>();
+  if (CACHE == kFourBit && warp == kTmaWarp) {
+    // the first segment's q (the QK warp requests the others)
+    Cursor cur = start;
+    Seg g;
+    const bool leader = elect_one();
+    if (next_seg(p, cur, g) && leader) load_q(g);
+    __syncwarp();
+  } else if (CACHE != kFourBit && warp == kTmaWarp) {
     // ============================================================= key blocks
     // A block's keys come in parts of a page, up to 64 keys each: five boxes a
     // part (four 128-byte columns, one of 64), all issued by one lane with the
@@ -775,30 +903,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     mbar_wait(smem_u32(&s.bar_drain[1]), 0, p.err);
   }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == kQkWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int NR, int QP, bool ROWSCALE>
+template <int NR, int QP, Cache CACHE>
 static smla_status_t launch(const DenseDecodeArgs& a, const Params& p, cudaStream_t stream) {
   CUtensorMap tq, tqr, tk, tr;
   const uint64_t q_rows = static_cast<uint64_t>(a.T) * a.H;
   const uint32_t box = std::min(a.seqs->page_size, kBK / 2);
-  bool enc = encode_tma_2d_u8(&tk, a.latent, kD, a.phys_rows, 128, box, 128) &&
-             encode_tma_2d_u8(&tr, a.latent, kD, a.phys_rows, 64, box, 64) &&
-             encode_tma_2d_u8(&tq, a.q, kD * QP, q_rows, 128, NR, 128);
-  tqr = tq;
+  bool enc = encode_tma_2d_u8(&tq, a.q, kD * QP, q_rows, 128, NR, 128);
+  tqr = tk = tr = tq;
+  if (CACHE != kFourBit)
+    enc = enc && encode_tma_2d_u8(&tk, a.latent, kD, a.phys_rows, 128, box, 128) &&
+          encode_tma_2d_u8(&tr, a.latent, kD, a.phys_rows, 64, box, 64);
   if (QP == 1) enc = enc && encode_tma_2d_u8(&tqr, a.q, kD, q_rows, 64, NR, 64);
   if (!enc) return fail(SMLA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the dense-decode tensor maps");
   constexpr size_t smem = sizeof(Smem<NR, QP>);
   static_assert(smem <= 232448, "shared memory exceeds a CTA's 227 KB");
   static std::atomic<unsigned long long> ready{0};
-  const smla_status_t st = prepare_kernel(reinterpret_cast<const void*>(decode_kernel<NR, QP, ROWSCALE>), smem, 0, ready,
-                                          "dense decode kernel");
+  const smla_status_t st = prepare_kernel(reinterpret_cast<const void*>(decode_kernel<NR, QP, CACHE>), smem,
+                                          CACHE == kFourBit ? fp4_regs(NR) : 0, ready, "dense decode kernel");
   if (st != SMLA_OK) return st;
-  decode_kernel<NR, QP, ROWSCALE><<<p.grid, kThreads, smem, stream>>>(tq, tqr, tk, tr, p);
+  decode_kernel<NR, QP, CACHE><<<p.grid, threads_of(CACHE, NR), smem, stream>>>(tq, tqr, tk, tr, p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e, "dense decode launch");
   return launch_join<NR>(p, stream);
@@ -826,8 +956,9 @@ smla_status_t launch_dense_decode(const DenseDecodeArgs& a, unsigned* err, cudaS
   const bool bf16 = a.q_dtype == SMLA_BF16, rows = a.scales != nullptr;
   const auto go = [&](auto nr_c) {
     constexpr int NR = decltype(nr_c)::value;
-    if (bf16) return rows ? launch<NR, 2, true>(a, p, stream) : launch<NR, 2, false>(a, p, stream);
-    return rows ? launch<NR, 1, true>(a, p, stream) : launch<NR, 1, false>(a, p, stream);
+    if (a.fp4) return bf16 ? launch<NR, 2, kFourBit>(a, p, stream) : launch<NR, 1, kFourBit>(a, p, stream);
+    if (bf16) return rows ? launch<NR, 2, kRowScale>(a, p, stream) : launch<NR, 2, kUnitScale>(a, p, stream);
+    return rows ? launch<NR, 1, kRowScale>(a, p, stream) : launch<NR, 1, kUnitScale>(a, p, stream);
   };
   if (nr == 64) return go(std::integral_constant<int, 64>{});
   if (nr == 32) return go(std::integral_constant<int, 32>{});

@@ -128,6 +128,8 @@ struct CacheArgs {
   int sbs;
   void* rows;
   int64_t rows_stride;
+  bool fp4;           // a 4-bit cache (D = 576; pool_dtype, scales and sbs unused)
+  float* row_scales;  // gather from one: rows are e4m3 with these scales (null: bf16)
 };
 smla_status_t launch_cache_append(const CacheArgs& a, const smla_seqs_t& seqs, unsigned* err, cudaStream_t stream);
 smla_status_t launch_cache_gather(const CacheArgs& a, const smla_seqs_t& seqs, unsigned* err, cudaStream_t stream);
@@ -172,9 +174,37 @@ struct DenseDecodeArgs {
   const float* sink;
   uint16_t* out;
   void* workspace;
+  bool fp4;  // latent: a 4-bit cache's rows, their scales in them
 };
 size_t dense_decode_workspace_bytes(int T, int H, int max_kv_len);
 smla_status_t launch_dense_decode(const DenseDecodeArgs& a, unsigned* err, cudaStream_t stream);
 smla_status_t launch_dense_decode_wide(const DenseDecodeArgs& a, unsigned* err, cudaStream_t stream);
+
+// Rows quantised to e4m3 with a scale for each 128 columns.
+struct QuantizeArgs {
+  const void* x;  // bf16 [M, K], rows x_stride elements apart
+  int64_t x_stride;
+  int M, K;
+  const void* norm_weight;  // bf16 [K], null: no norm
+  float norm_eps;
+  uint8_t* out;   // [M, K]
+  float* scales;  // [M, ceil(K / 128)]
+};
+smla_status_t launch_quantize(const QuantizeArgs& a, cudaStream_t stream);
+
+// Batched product of block-scaled e4m3 operands.  Strides in elements.
+struct MatmulArgs {
+  const uint8_t* a;  // [G, M, K]
+  int64_t a_gs, a_ms;
+  const float* a_scales;  // [G, M, ceil(K / 128)]
+  int64_t as_gs, as_ms;
+  const uint8_t* b;       // [G, N, K]
+  const float* b_scales;  // [G, ceil(N / 128), ceil(K / 128)]
+  int G, M, N, K;
+  void* out;  // [G, M, N]
+  int out_dtype;
+  int64_t o_gs, o_ms;
+};
+smla_status_t launch_block_matmul(const MatmulArgs& a, unsigned* err, cudaStream_t stream);
 
 }  // namespace smla
