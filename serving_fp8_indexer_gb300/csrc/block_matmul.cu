@@ -36,7 +36,7 @@ struct Params {
   void* out;
   int64_t o_gs, o_ms;
   bool out_f32;
-  bool a_flip;  // a's tensor map has the batch before the rows
+  bool a_flip, o_flip;  // a's (out's) tensor map has the batch before the rows
   int G, M, N;
   int m_tiles, n_tiles;
   int64_t tiles;
@@ -49,70 +49,126 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 
 // ------------------------------------------------------------------------ wide
-// (the launch's 384 x 168 registers are 128 x (2 x 216 + 72))
-constexpr int kWideThreads = 384, kWideRegs = 168, kWideSoft = 8, kGroupM = 16;
+// A pair of CTAs takes 256 rows of a and BN of b: each loads 128 rows of a and BN / 2
+// of b a block, and the first one's MMAs (cta_group::2) read both shared memories,
+// where a CTA by itself, which stages all of b, is bound by them (48 KB in and 48
+// KB out a block of 512 MMA cycles: 712 cycles).  Each CTA's TMEM holds its own
+// 128 rows' sums.
+// Warps: 0-7 epilogue (32 rows x BN / 2 columns each), 8 TMA loads, 9 MMAs (in the
+// second CTA: tells the first that a stage has landed), 10-11 a's and b's scales.
+// (The launch's 384 x 168 registers are 128 x (2 x 216 + 72).)
+constexpr int kWideThreads = 384, kWideRegs = 168, kWideSoft = 8, kGroupM = 8;
+constexpr int kScaleBlocks = 8;  // blocks whose scales are fetched together
+constexpr int kScaleRow = 132;   // padded: the fetching warps' transposed stores meet all banks
 
-template <int BN>
+constexpr int BN = 256;
+
 struct WideSmem {
-  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kStages = 4;  // a stage's way round takes 1.5 us: what is in flight sets the rate
+  // places for 64 bytes of an epilogue warp's 32 rows on their way out
+  static constexpr int kPlaces = 4;
   uint8_t a[kStages][128 * kBK];
-  uint8_t b[kStages][BN * kBK];
-  unsigned long long full[kStages], empty[kStages], sum_full[2], sum_empty[2], drain;
+  uint8_t b[kStages][BN / 2 * kBK];
+  uint8_t out[kWideSoft][kPlaces][32 * 64];
+  float as[2][kScaleBlocks][kScaleRow], bs[2][2][kScaleBlocks];
+  unsigned long long full[kStages], empty[kStages];
+  unsigned long long sum_full[2], sum_empty[2], scale_full[2], scale_empty[2], drain;
   uint32_t tmem_base;
 };
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// An address of this CTA's shared memory in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// (No release beyond the CTA's: what it tells of are finished TMEM reads and TMA
+// writes, and a cluster-wide one waits for the warp's every store: 765 us at 4096^2 x
+// 16384.)
+__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The tcgen05 operations of a pair of CTAs.
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void pair_mma_f8f6f4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at this address in both CTAs when the MMAs so far complete.
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+               "h"(static_cast<uint16_t>(3))
+               : "memory");
+}
 
 struct Tile {
   int g, m0, n0;
 };
-// Tile t of the walk: batch after batch; in each, groups of kGroupM row tiles,
-// column after column, so that the CTAs of a moment share few rows of a and b.
-template <int BN>
-__device__ __forceinline__ Tile tile_at(const Params& p, int64_t t) {
-  const int64_t per = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-  const int g = static_cast<int>(t / per);
-  const int64_t r = t - g * per;
-  const int64_t group = static_cast<int64_t>(kGroupM) * p.n_tiles;
-  const int gr = static_cast<int>(r / group), first = gr * kGroupM;
-  const int rows = min(kGroupM, p.m_tiles - first);
-  const int in = static_cast<int>(r - gr * group);
-  const int n = in / rows, m = in - n * rows;
-  return {g, (first + m) * 128, n * BN};
+// Tile t of the walk (below 2^31: the entry checks it): batch after batch; in
+// each, groups of kGroupM row tiles, column after column, so that the CTAs of a
+// moment share few rows of a and b.
+__device__ __forceinline__ Tile tile_at(const Params& p, unsigned t) {
+  const unsigned per = static_cast<unsigned>(p.m_tiles) * p.n_tiles;
+  const unsigned g = p.G == 1 ? 0 : t / per, r = t - g * per;
+  const unsigned group = static_cast<unsigned>(kGroupM) * p.n_tiles;
+  const unsigned gr = r / group, in = r - gr * group, first = gr * kGroupM;
+  const unsigned rows = min(static_cast<unsigned>(kGroupM), p.m_tiles - first);
+  const unsigned n = in / rows, m = in - n * rows;
+  return {static_cast<int>(g), static_cast<int>(first + m) * 256, static_cast<int>(n) * BN};
 }
 
-template <int BN>
 __global__ void __launch_bounds__(kWideThreads, 1)
-    wide_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const Params p) {
-  using S = WideSmem<BN>;
+    wide_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                const __grid_constant__ CUtensorMap to, const Params p) {
+  using S = WideSmem;
   constexpr int kStages = S::kStages, kCols = BN / 2;  // columns of a thread
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  if (smem_u32(smem_raw) & 1023u) {
+  if (smem_u32(smem_raw) & 1023u) {  // (the same for every CTA)
     if (threadIdx.x == 0) atomicOr(p.err, kErrShape);
     return;
   }
   S& s = *reinterpret_cast<S*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(blockIdx.x & 1), m_of = rank * 128;  // this CTA's rows of a tile
+  const unsigned tiles = static_cast<unsigned>(p.tiles), pairs = gridDim.x >> 1;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&s.full[i]), 1);
+      mbar_init(smem_u32(&s.full[i]), 2 - rank);  // the first CTA's counts the second's landing too
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s.sum_full[i]), 1);
-      mbar_init(smem_u32(&s.sum_empty[i]), kWideSoft);
+      mbar_init(smem_u32(&s.sum_empty[i]), 2 * kWideSoft);  // (the first CTA's counts)
+      mbar_init(smem_u32(&s.scale_full[i]), 2);
+      mbar_init(smem_u32(&s.scale_empty[i]), kWideSoft);
     }
     mbar_init(smem_u32(&s.drain), 1);
     fence_mbar_init();
   }
   if (warp == 9) {
-    tmem_alloc(smem_u32(&s.tmem_base), 2 * BN);
-    tmem_relinquish();
+    pair_tmem_alloc(smem_u32(&s.tmem_base), 2 * BN);
   }
   if (threadIdx.x == 8 * 32) {
     tma_prefetch_desc(&ta);
     tma_prefetch_desc(&tb);
+    tma_prefetch_desc(&to);
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // both CTAs' barriers are there
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
 
@@ -121,160 +177,247 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     setmaxnreg_inc<216>();
     const int half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    int i = 0;
+    const uint32_t from = tmem + lanes + half * kCols;
+    const uint32_t full0 = smem_u32(s.sum_full), empty0 = cluster_addr(smem_u32(s.sum_empty), 0);
+    int buf = 0, q = 0;            // accumulator, group of scales
+    uint32_t phase = 0, q_phase = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
-      const Tile tile = tile_at<BN>(p, t);
-      const int m = tile.m0 + (warp & 3) * 32 + lane, n0 = tile.n0 + half * kCols;
-      const bool in_m = m < p.M;
-      const float* as = p.as + tile.g * p.as_gs + (in_m ? m : 0) * p.as_ms;
-      const float* bs = p.bs + (static_cast<int64_t>(tile.g) * p.nb + min(n0 / 128, p.nb - 1)) * p.kb;
+    for (unsigned t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
+      const Tile tile = tile_at(p, t);
       float acc[kCols];
 #pragma unroll
       for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
-      float sa = as[0], sb = bs[0];
-      for (int kb = 0; kb < p.kb; ++kb, ++i) {
-        const float scale = sa * sb;
-        if (kb + 1 < p.kb) {
-          sa = as[kb + 1];
-          sb = bs[kb + 1];
-        }
-        const int buf = i & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.sum_full[buf]), (i >> 1) & 1, p.err));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t a = tmem + lanes + buf * BN + half * kCols;
-#pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(a + c, v);
-          tmem_wait_ld_regs(v);
-          if (c + 32 == kCols) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s.sum_empty[buf]));
-          }
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            const float2 r = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), make_float2(scale, scale),
-                                  make_float2(acc[c + k], acc[c + k + 1]));
-            acc[c + k] = r.x;
-            acc[c + k + 1] = r.y;
-          }
-        }
-      }
-      if (ok && in_m) {
-        const int64_t at = tile.g * p.o_gs + m * p.o_ms + n0;
-        const int left = p.N - n0;
-        if (p.out_f32) {
-          float* o = static_cast<float*>(p.out) + at;
-#pragma unroll
-          for (int c = 0; c < kCols; c += 4)
-            if (c < left) *reinterpret_cast<float4*>(o + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
-        } else {
-          uint16_t* o = static_cast<uint16_t*>(p.out) + at;
-#pragma unroll
-          for (int c = 0; c < kCols; c += 8)
-            if (c < left)
-              *reinterpret_cast<uint4*>(o + c) = make_uint4(pack2(acc[c], acc[c + 1]), pack2(acc[c + 2], acc[c + 3]),
-                                                            pack2(acc[c + 4], acc[c + 5]), pack2(acc[c + 6], acc[c + 7]));
-        }
-      }
-    }
-  } else {
-    setmaxnreg_dec<72>();
-  if (warp == 8) {
-    // ==================================================================== loads
-    int i = 0;
-    if (elect_one()) {
-      bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
-        const Tile tile = tile_at<BN>(p, t);
-        for (int kb = 0; kb < p.kb; ++kb, ++i) {
-          const int st = i % kStages;
-          ok = mbar_wait(smem_u32(&s.empty[st]), ((i / kStages) & 1) ^ 1, p.err);
-          if (!ok) break;
-          const uint32_t bar = smem_u32(&s.full[st]);
-          mbar_arrive_expect_tx(bar, (128 + BN) * kBK);
-          tma_load_3d(smem_u32(s.a[st]), &ta, kb * kBK, p.a_flip ? tile.g : tile.m0, p.a_flip ? tile.m0 : tile.g, bar);
-          tma_load_3d(smem_u32(s.b[st]), &tb, kb * kBK, tile.n0, tile.g, bar);
-        }
-      }
-      // nothing is still landing when the CTA ends
-      for (int st = 0; st < kStages; ++st) {
-        const int loads = (i + kStages - 1 - st) / kStages;
-        if (loads > 0) mbar_wait(smem_u32(&s.full[st]), (loads - 1) & 1, p.err);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 9) {
-    // ===================================================================== MMAs
-    if (elect_one()) {
-      constexpr uint32_t IDESC = idesc_e4m3_f32(128, BN, 0, 0);
-      const uint64_t da = make_sdesc(smem_u32(s.a[0]), 16, 1024, kSwizzle128B);
-      const uint64_t db = make_sdesc(smem_u32(s.b[0]), 16, 1024, kSwizzle128B);
-      int i = 0;
-      bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
-        for (int kb = 0; kb < p.kb; ++kb, ++i) {
-          const int st = i % kStages, buf = i & 1;
-          ok = mbar_wait(smem_u32(&s.sum_empty[buf]), ((i >> 1) & 1) ^ 1, p.err) &&
-               mbar_wait(smem_u32(&s.full[st]), (i / kStages) & 1, p.err);
-          if (!ok) break;
+      for (int kb0 = 0; ok && kb0 < p.kb; kb0 += kScaleBlocks) {
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.scale_full[q]), q_phase, p.err));
+        const float* sa = &s.as[q][0][(warp & 3) * 32 + lane];
+        const float* sb = s.bs[q][half];
+#pragma unroll 1
+        for (int left = min(kScaleBlocks, p.kb - kb0); ok && left > 0; --left, sa += kScaleRow, ++sb) {
+          const float scale = *sa * *sb;
+          ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * buf, phase, p.err));
           tc_fence_after();
+          const uint32_t a = from + buf * BN;
+          // 32 columns at a time, two loads in flight.  (Paired multiply-adds had a move
+          // beside each, for their register pairs: 252 us for 213 at 4096^2 x 16384.)
+          const auto add = [&](const uint32_t (&v)[32], int c) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) acc[c + k] = fmaf(__uint_as_float(v[k]), scale, acc[c + k]);
+          };
+          uint32_t v0[32], v1[32];
+          tmem_ld32(a, v0);
+          tmem_ld32(a + 32, v1);
+          tmem_wait_ld_regs(v0);
+          tmem_wait_ld_regs(v1);
+          add(v0, 0);
+          tmem_ld32(a + 64, v0);
+          add(v1, 32);
+          tmem_ld32(a + 96, v1);
+          tmem_wait_ld_regs(v0);
+          tmem_wait_ld_regs(v1);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) cluster_arrive(empty0 + 8 * buf);
+          add(v0, 64);
+          add(v1, 96);
+          buf ^= 1;
+          phase ^= buf ^ 1;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.scale_empty[q]));
+        q ^= 1;
+        q_phase ^= q ^ 1;
+      }
+      const int row0 = tile.m0 + m_of + (warp & 3) * 32, n0 = tile.n0 + half * kCols;
+      if (ok && row0 < p.M) {
+        // 64 bytes of the warp's 32 rows at a time, through shared memory: stores of a
+        // row by each thread took a sector of their own each (K = 512, 4101 x 32768:
+        // 166 us).  The tensor's ends are the store's to mind.
+        const int per = p.out_f32 ? 16 : 32;
+        const auto put = [&](int c, int place, auto&& piece) {  // columns [c, c + per)
+          uint8_t* stage = s.out[warp][place];
+          if (lane == 0) tma_store_wait_read<S::kPlaces - 1>();
+          __syncwarp();
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_f8f6f4_ss(tmem + buf * BN, da + static_cast<uint64_t>((st * 128 * kBK + k * 32) >> 4),
-                          db + static_cast<uint64_t>((st * BN * kBK + k * 32) >> 4), IDESC, k ? 1u : 0u);
-          mma_commit(smem_u32(&s.empty[st]));
-          mma_commit(smem_u32(&s.sum_full[buf]));
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = piece(k);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const int x = (n0 + c) * (64 / per);
+            tma_store_3d(&to, smem_u32(stage), x, p.o_flip ? tile.g : row0, p.o_flip ? row0 : tile.g);
+            tma_store_commit();
+          }
+        };
+        if (p.out_f32) {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 16)
+            if (n0 + c < p.N)
+              put(c, c / 16 % S::kPlaces, [&](int k) {
+                const float* f = acc + c + 4 * k;
+                return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+              });
+        } else {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32)
+            if (n0 + c < p.N)
+              put(c, c / 32 % S::kPlaces, [&](int k) {
+                const float* f = acc + c + 8 * k;
+                return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+              });
         }
       }
-      mma_commit(smem_u32(&s.drain));
-      mbar_wait(smem_u32(&s.drain), 0, p.err);
     }
+    if (lane == 0) tma_store_wait_all();
     __syncwarp();
-  }
+  } else {
+    setmaxnreg_dec<72>();
+    if (warp == 8) {
+      // ================================================================== loads
+      if (elect_one()) {
+        int st = 0;
+        uint32_t phase = 0, used = 0;
+        bool ok = true;
+        for (unsigned t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
+          const Tile tile = tile_at(p, t);
+          const int m = tile.m0 + m_of, n = tile.n0 + rank * (BN / 2);
+          const int y = p.a_flip ? tile.g : m, z = p.a_flip ? m : tile.g;
+          for (int kb = 0; kb < p.kb; ++kb) {
+            ok = mbar_wait(smem_u32(&s.empty[st]), phase ^ 1, p.err);
+            if (!ok) break;
+            const uint32_t bar = smem_u32(&s.full[st]);
+            mbar_arrive_expect_tx(bar, (128 + BN / 2) * kBK);
+            tma_load_3d(smem_u32(s.a[st]), &ta, kb * kBK, y, z, bar);
+            tma_load_3d(smem_u32(s.b[st]), &tb, kb * kBK, n, tile.g, bar);
+            used |= 1u << st;
+            if (++st == kStages) {
+              st = 0;
+              phase ^= 1;
+            }
+          }
+        }
+        // nothing is still landing when the CTA ends: the last load of each stage
+        for (int k = 0; k < kStages; ++k)
+          if (used >> k & 1) mbar_wait(smem_u32(&s.full[k]), k < st ? phase : phase ^ 1, p.err);
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      // =================================================================== MMAs
+      if (elect_one()) {
+        constexpr uint32_t IDESC = idesc_e4m3_f32(256, BN, 0, 0);
+        const uint64_t da = make_sdesc(smem_u32(s.a[0]), 16, 1024, kSwizzle128B);
+        const uint64_t db = make_sdesc(smem_u32(s.b[0]), 16, 1024, kSwizzle128B);
+        // (One thread, whose every instruction the MMAs wait for: nothing is computed
+        // that can be carried along.)
+        const uint32_t full0 = smem_u32(s.full), empty0 = smem_u32(s.empty), peer0 = cluster_addr(full0, 0);
+        const uint32_t sum_full0 = smem_u32(s.sum_full), sum_empty0 = smem_u32(s.sum_empty);
+        int st = 0, buf = 0;
+        uint32_t phase = 0, buf_phase = 1;
+        bool ok = true;
+        for (unsigned t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
+          for (int kb = 0; kb < p.kb; ++kb) {
+            ok = mbar_wait(full0 + 8 * st, phase, p.err);
+            if (!ok) break;
+            if (rank == 1) {
+              cluster_arrive(peer0 + 8 * st);
+            } else {
+              ok = mbar_wait(sum_empty0 + 8 * buf, buf_phase, p.err);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t a = da + static_cast<uint64_t>(st * (128 * kBK >> 4));
+              const uint64_t b = db + static_cast<uint64_t>(st * (BN / 2 * kBK >> 4));
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                pair_mma_f8f6f4(tmem + buf * BN, a + static_cast<uint64_t>(2 * k), b + static_cast<uint64_t>(2 * k), IDESC,
+                                k ? 1u : 0u);
+              pair_commit(sum_full0 + 8 * buf);
+              pair_commit(empty0 + 8 * st);
+              buf ^= 1;
+              buf_phase ^= buf ^ 1;
+            }
+            if (++st == kStages) {
+              st = 0;
+              phase ^= 1;
+            }
+          }
+        }
+        if (rank == 0) {
+          pair_commit(smem_u32(&s.drain));
+          mbar_wait(smem_u32(&s.drain), 0, p.err);
+        }
+      }
+      __syncwarp();
+    } else {
+      // ================================================================= scales
+      // Eight blocks' at a time, turned round: a warp reads four rows' eight numbers
+      // at once, and the epilogue 32 rows' of one block.  (Read by the epilogue's
+      // threads, a row each, they took a third of the kernel: 297 us for 208 at 4096^2
+      // x 16384.)
+      const int rows0 = (warp - 10) * 64 + (lane >> 3), b = lane & 7;
+      int q = 0;
+      bool ok = true;
+      for (unsigned t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
+        const Tile tile = tile_at(p, t);
+        const float* as = p.as + tile.g * p.as_gs;
+        const float* bs = p.bs + static_cast<int64_t>(tile.g) * p.nb * p.kb;
+        for (int kb0 = 0; kb0 < p.kb; kb0 += kScaleBlocks, ++q) {
+          const int kb = min(kb0 + b, p.kb - 1);
+          float v[16], w = 0.f;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = as[min(tile.m0 + m_of + rows0 + 4 * k, p.M - 1) * p.as_ms + kb];
+          const int n = lane >> 3;  // half of the tile's columns
+          if (n < 2) w = bs[static_cast<int64_t>(min((tile.n0 + n * kCols) / 128, p.nb - 1)) * p.kb + kb];
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.scale_empty[q & 1]), ((q >> 1) & 1) ^ 1, p.err));
+          if (!ok) break;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) s.as[q & 1][b][rows0 + 4 * k] = v[k];
+          if (warp == 10 && n < 2) s.bs[q & 1][n][b] = w;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s.scale_full[q & 1]));
+        }
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // neither CTA's memory is touched any more
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 2 * BN);
+  if (warp == 9) pair_tmem_dealloc(tmem, 2 * BN);
 }
 
 // ---------------------------------------------------------------------- narrow
 constexpr int kNarrowThreads = 192;
 
+constexpr int kNarrowStages = 5, kNarrowChunk = 32;
+// (two CTAs an SM)
+constexpr int most_stages(int mt) { return mt == 64 ? 4 : kNarrowStages; }
+// Behind the stages (weights, then rows of a, each 1024-byte aligned).
 template <int MT>
 struct NarrowSmem {
-  static constexpr int kStages = MT <= 32 ? 5 : 4;  // two CTAs an SM up to MT = 64
-  uint8_t b[kStages][128 * kBK];
-  uint8_t a[kStages][MT * kBK];
-  alignas(16) float scale[4][2][MT];  // of each epilogue warp
-  unsigned long long full[kStages], empty[kStages], sum_full[2], sum_empty[2], drain;
+  alignas(16) float scale[kNarrowChunk][MT + 4];  // of a chunk of blocks: a's times b's
+  unsigned long long full[kNarrowStages], empty[kNarrowStages], sum_full[2], sum_empty[2], drain;
   uint32_t tmem_base;
 };
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+template <int MT>
+constexpr int stage_bytes() {
+  return (128 + MT) * kBK;
 }
+
 // The word at this CTA's shared-memory address in CTA `rank` of the cluster.
 __device__ __forceinline__ float cluster_ld(uint32_t addr, uint32_t rank) {
-  uint32_t r;
   float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(addr, rank)) : "memory");
   return v;
 }
 
 template <int MT, int CS>
-__global__ void __launch_bounds__(kNarrowThreads)
-    narrow_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const Params p) {
-  using S = NarrowSmem<MT>;
-  constexpr int kStages = S::kStages;
+__global__ void __launch_bounds__(kNarrowThreads, 2)
+    narrow_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const Params p,
+                  const int stages) {
   constexpr int kTmemCols = 2 * MT < 32 ? 32 : 2 * MT;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  S& s = *reinterpret_cast<S*>(smem_raw);
+  uint8_t* const s_b = smem_raw;                        // [stages][128][kBK]
+  uint8_t* const s_a = smem_raw + stages * 128 * kBK;   // [stages][MT][kBK]
+  auto& s = *reinterpret_cast<NarrowSmem<MT>*>(smem_raw + stages * (128 + MT) * kBK);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CS > 1 ? static_cast<int>(blockIdx.x % CS) : 0;
   const int64_t t = blockIdx.x / CS;
@@ -283,14 +426,20 @@ __global__ void __launch_bounds__(kNarrowThreads)
   const int n0 = r / p.m_tiles * 128, m0 = r % p.m_tiles * MT;
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.kb) * rank / CS);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.kb) * (rank + 1) / CS);
-  // (an unaligned base would be the same for every CTA)
-  const bool aligned = (smem_u32(smem_raw) & 1023u) == 0;
-  if (!aligned) {
+  if (smem_u32(smem_raw) & 1023u) {  // (the same for every CTA)
     if (threadIdx.x == 0) atomicOr(p.err, kErrShape);
     return;
   }
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+  const auto load = [&](int i) {  // block kb0 + i into its stage
+    const int st = i % stages, kb = kb0 + i;
+    const uint32_t bar = smem_u32(&s.full[st]);
+    mbar_arrive_expect_tx(bar, (128 + MT) * kBK);
+    tma_load_3d(smem_u32(s_b + st * 128 * kBK), &tb, kb * kBK, n0, g, bar);
+    tma_load_3d(smem_u32(s_a + st * MT * kBK), &ta, kb * kBK, p.a_flip ? g : m0, p.a_flip ? m0 : g, bar);
+  };
+  // (the first loads go out ahead of the rest of the set-up)
+  if (threadIdx.x == 4 * 32) {
+    for (int i = 0; i < stages; ++i) {
       mbar_init(smem_u32(&s.full[i]), 1);
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
@@ -300,14 +449,11 @@ __global__ void __launch_bounds__(kNarrowThreads)
     }
     mbar_init(smem_u32(&s.drain), 1);
     fence_mbar_init();
+    for (int i = 0; i < min(stages, kb1 - kb0); ++i) load(i);
   }
   if (warp == 5) {
     tmem_alloc(smem_u32(&s.tmem_base), kTmemCols);
     tmem_relinquish();
-  }
-  if (threadIdx.x == 4 * 32) {
-    tma_prefetch_desc(&ta);
-    tma_prefetch_desc(&tb);
   }
   tc_fence_before();
   __syncthreads();
@@ -320,66 +466,73 @@ __global__ void __launch_bounds__(kNarrowThreads)
 #pragma unroll
     for (int c = 0; c < MT; ++c) acc[c] = 0.f;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    constexpr int kPer = (MT + 31) / 32;  // rows whose scales a lane fetches
-    const float* as[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) as[j] = p.as + g * p.as_gs + min(m0 + lane + 32 * j, p.M - 1) * p.as_ms;
+    // Scales come 32 blocks at a time, each warp reading a quarter of the rows with a
+    // lane for each block, and wait in registers while the chunk before is used.
+    // (Read a block at a time they were late: 14.7 us for 16 x 4096 x 16384.)
+    constexpr int kPer = MT / 4;
+    const float* as = p.as + g * p.as_gs;
     const float* bs = p.bs + (static_cast<int64_t>(g) * p.nb + n0 / 128) * p.kb;
-    float na[kPer], nbs = 0.f;
+    float next[kPer];
     const auto fetch = [&](int kb) {
-      nbs = bs[kb];
+      const int at = min(kb + lane, p.kb - 1);
+      const float w = bs[at];
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) na[j] = as[j][kb];
+      for (int j = 0; j < kPer; ++j) next[j] = as[min(m0 + warp * kPer + j, p.M - 1) * p.as_ms + at] * w;
     };
     if (kb0 < kb1) fetch(kb0);
-    for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
-      const int buf = i & 1;
-      float* sc = s.scale[warp][buf];
+    int buf = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int kc = kb0; ok && kc < kb1; kc += kNarrowChunk) {
+      if (kc > kb0) named_bar_sync(1, 128);  // the chunk before has been used
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (lane + 32 * j < MT) sc[lane + 32 * j] = na[j] * nbs;
-      if (kb + 1 < kb1) fetch(kb + 1);
-      const bool ok = mbar_wait(smem_u32(&s.sum_full[buf]), (i >> 1) & 1, p.err);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      __syncwarp();
-      tc_fence_after();
-      const uint32_t a = tmem + lanes + buf * MT;
+      for (int j = 0; j < kPer; ++j) s.scale[lane][warp * kPer + j] = next[j];
+      named_bar_sync(1, 128);
+      if (kc + kNarrowChunk < kb1) fetch(kc + kNarrowChunk);
+      const int n = min(kNarrowChunk, kb1 - kc);
+#pragma unroll 1
+      for (int k = 0; k < n; ++k) {
+        // (a wait that gives up lets the others run into their own limits)
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.sum_full[buf]), phase, p.err))) ok = false;
+        tc_fence_after();
+        const uint32_t a = tmem + lanes + buf * MT;
+        const float* sc = s.scale[k];
+        uint32_t v[MT];
+        if constexpr (MT == 16) {
+          tmem_ld16(a, v);
+        } else {
 #pragma unroll
-      for (int c = 0; c < MT; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(a + c, v);
+          for (int c = 0; c < MT; c += 32) tmem_ld32(a + c, reinterpret_cast<uint32_t(&)[32]>(v[c]));
+        }
         tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) asm volatile("" : "+r"(v[k]));
-        if (c + 16 == MT) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&s.sum_empty[buf]));
-        }
+        for (int c = 0; c < MT; ++c) asm volatile("" : "+r"(v[c]));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.sum_empty[buf]));
 #pragma unroll
-        for (int k = 0; k < 16; k += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(sc + c + k);
-          acc[c + k] = fmaf(__uint_as_float(v[k]), f.x, acc[c + k]);
-          acc[c + k + 1] = fmaf(__uint_as_float(v[k + 1]), f.y, acc[c + k + 1]);
-          acc[c + k + 2] = fmaf(__uint_as_float(v[k + 2]), f.z, acc[c + k + 2]);
-          acc[c + k + 3] = fmaf(__uint_as_float(v[k + 3]), f.w, acc[c + k + 3]);
+        for (int c = 0; c < MT; c += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(sc + c);
+          acc[c] = fmaf(__uint_as_float(v[c]), f.x, acc[c]);
+          acc[c + 1] = fmaf(__uint_as_float(v[c + 1]), f.y, acc[c + 1]);
+          acc[c + 2] = fmaf(__uint_as_float(v[c + 2]), f.z, acc[c + 2]);
+          acc[c + 3] = fmaf(__uint_as_float(v[c + 3]), f.w, acc[c + 3]);
         }
+        buf ^= 1;
+        phase ^= buf ^ 1;
       }
     }
   } else if (warp == 4) {
     // ==================================================================== loads
-    if (elect_one()) {
-      int i = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++i) {
-        const int st = i % kStages;
-        if (!mbar_wait(smem_u32(&s.empty[st]), ((i / kStages) & 1) ^ 1, p.err)) break;
-        const uint32_t bar = smem_u32(&s.full[st]);
-        mbar_arrive_expect_tx(bar, (128 + MT) * kBK);
-        tma_load_3d(smem_u32(s.b[st]), &tb, kb * kBK, n0, g, bar);
-        tma_load_3d(smem_u32(s.a[st]), &ta, kb * kBK, p.a_flip ? g : m0, p.a_flip ? m0 : g, bar);
+    if (lane == 0) {
+      int i = min(stages, kb1 - kb0);
+      for (; i < kb1 - kb0; ++i) {
+        if (!mbar_wait(smem_u32(&s.empty[i % stages]), ((i / stages) & 1) ^ 1, p.err)) break;
+        load(i);
       }
-      for (int st = 0; st < kStages; ++st) {
-        const int loads = (i + kStages - 1 - st) / kStages;
+      // nothing is still landing when the CTA ends
+      for (int st = 0; st < stages; ++st) {
+        const int loads = (i + stages - 1 - st) / stages;
         if (loads > 0) mbar_wait(smem_u32(&s.full[st]), (loads - 1) & 1, p.err);
       }
     }
@@ -388,20 +541,27 @@ __global__ void __launch_bounds__(kNarrowThreads)
     // ===================================================================== MMAs
     if (elect_one()) {
       constexpr uint32_t IDESC = idesc_e4m3_f32(128, MT, 0, 0);
-      const uint64_t da = make_sdesc(smem_u32(s.b[0]), 16, 1024, kSwizzle128B);
-      const uint64_t db = make_sdesc(smem_u32(s.a[0]), 16, 1024, kSwizzle128B);
-      for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
-        const int st = i % kStages, buf = i & 1;
-        if (!(mbar_wait(smem_u32(&s.sum_empty[buf]), ((i >> 1) & 1) ^ 1, p.err) &&
-              mbar_wait(smem_u32(&s.full[st]), (i / kStages) & 1, p.err)))
-          break;
+      const uint64_t da = make_sdesc(smem_u32(s_b), 16, 1024, kSwizzle128B);
+      const uint64_t db = make_sdesc(smem_u32(s_a), 16, 1024, kSwizzle128B);
+      const uint32_t full0 = smem_u32(s.full), empty0 = smem_u32(s.empty);
+      const uint32_t sum_full0 = smem_u32(s.sum_full), sum_empty0 = smem_u32(s.sum_empty);
+      int st = 0, buf = 0;
+      uint32_t phase = 0, buf_phase = 1;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(mbar_wait(sum_empty0 + 8 * buf, buf_phase, p.err) && mbar_wait(full0 + 8 * st, phase, p.err))) break;
         tc_fence_after();
+        const uint64_t a = da + static_cast<uint64_t>(st * (128 * kBK >> 4)), b = db + static_cast<uint64_t>(st * (MT * kBK >> 4));
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_f8f6f4_ss(tmem + buf * MT, da + static_cast<uint64_t>((st * 128 * kBK + k * 32) >> 4),
-                        db + static_cast<uint64_t>((st * MT * kBK + k * 32) >> 4), IDESC, k ? 1u : 0u);
-        mma_commit(smem_u32(&s.empty[st]));
-        mma_commit(smem_u32(&s.sum_full[buf]));
+          mma_f8f6f4_ss(tmem + buf * MT, a + static_cast<uint64_t>(2 * k), b + static_cast<uint64_t>(2 * k), IDESC, k ? 1u : 0u);
+        mma_commit(sum_full0 + 8 * buf);
+        mma_commit(empty0 + 8 * st);
+        buf ^= 1;
+        buf_phase ^= buf ^ 1;
+        if (++st == stages) {
+          st = 0;
+          phase ^= 1;
+        }
       }
       mma_commit(smem_u32(&s.drain));
       mbar_wait(smem_u32(&s.drain), 0, p.err);
@@ -417,8 +577,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
   constexpr int kOwn = MT / CS;  // rows of a that this CTA finishes
   float sum[kOwn];
   if constexpr (CS > 1) {
-    float* part = reinterpret_cast<float*>(s.b);  // [MT][128], in place of the stages (all read)
-    static_assert(sizeof(s.b) >= MT * 128 * sizeof(float), "");
+    float* part = reinterpret_cast<float*>(smem_raw);  // [MT][128], in place of the stages (all read)
     if (warp < 4) {
 #pragma unroll
       for (int c = 0; c < MT; ++c) part[c * 128 + threadIdx.x] = acc[c];
@@ -456,23 +615,23 @@ __global__ void __launch_bounds__(kNarrowThreads)
   }
 }
 
-// A [G][rows][K] byte operand in boxes of 128 columns x box_rows, its dimensions in
+// A [G][rows][width] byte tensor in boxes of box_bytes x box_rows, its dimensions in
 // the order of their strides; *flip: the batch's comes before the rows'.
-static bool operand_map(CUtensorMap* map, const uint8_t* x, int64_t gs, int64_t rs, int G, int rows, int K, int box_rows,
-                        bool* flip) {
+static bool byte_map(CUtensorMap* map, const void* x, int64_t gs, int64_t rs, int G, int rows, int64_t width, int box_rows,
+                     bool* flip, int box_bytes = 128) {
   if (G == 1) gs = rs * rows;
   if (rows == 1) rs = gs;
   *flip = gs < rs;
   const int r = *flip ? 2 : 1, b = 3 - r;
-  uint64_t dims[3] = {static_cast<uint64_t>(K)}, strides[2];
-  uint32_t box[3] = {kBK};
+  uint64_t dims[3] = {static_cast<uint64_t>(width)}, strides[2];
+  uint32_t box[3] = {static_cast<uint32_t>(box_bytes)};
   dims[r] = static_cast<uint64_t>(rows);
   dims[b] = static_cast<uint64_t>(G);
   strides[r - 1] = static_cast<uint64_t>(rs);
   strides[b - 1] = static_cast<uint64_t>(gs);
   box[r] = static_cast<uint32_t>(box_rows);
   box[b] = 1;
-  return encode_tma_u8(map, x, 3, dims, strides, box, 128);
+  return encode_tma_u8(map, x, 3, dims, strides, box, box_bytes);
 }
 
 static Params params(const MatmulArgs& a, int rows, int cols, unsigned* err) {
@@ -499,27 +658,45 @@ static Params params(const MatmulArgs& a, int rows, int cols, unsigned* err) {
 
 static smla_status_t maps(const MatmulArgs& a, int a_rows, int b_rows, CUtensorMap* ta, CUtensorMap* tb, Params* p) {
   bool b_flip;
-  if (operand_map(ta, a.a, a.a_gs, a.a_ms, a.G, a.M, a.K, a_rows, &p->a_flip) &&
-      operand_map(tb, a.b, static_cast<int64_t>(a.N) * a.K, a.K, a.G, a.N, a.K, b_rows, &b_flip))
+  if (byte_map(ta, a.a, a.a_gs, a.a_ms, a.G, a.M, a.K, a_rows, &p->a_flip) &&
+      byte_map(tb, a.b, static_cast<int64_t>(a.N) * a.K, a.K, a.G, a.N, a.K, b_rows, &b_flip))
     return SMLA_OK;
   return fail(SMLA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the block matmul's tensor maps");
 }
 
-template <int BN>
+template <typename... Args>
+static smla_status_t launch_cluster(void (*kernel)(Args...), unsigned grid, int threads, size_t smem, int cluster,
+                                    cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = cluster;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e == cudaSuccess ? SMLA_OK : fail_cuda(e, "block matmul launch");
+}
+
 static smla_status_t launch_wide(const MatmulArgs& a, unsigned* err, cudaStream_t stream) {
-  Params p = params(a, 128, BN, err);
-  CUtensorMap ta, tb;
-  smla_status_t st = maps(a, 128, BN, &ta, &tb, &p);
+  Params p = params(a, 256, BN, err);
+  CUtensorMap ta, tb, to;
+  smla_status_t st = maps(a, 128, BN / 2, &ta, &tb, &p);
   if (st != SMLA_OK) return st;
-  constexpr size_t smem = sizeof(WideSmem<BN>);
+  const int es = p.out_f32 ? 4 : 2;
+  if (!byte_map(&to, a.out, a.o_gs * es, a.o_ms * es, a.G, a.M, static_cast<int64_t>(a.N) * es, 32, &p.o_flip, 64))
+    return fail(SMLA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the block matmul's output");
+  constexpr size_t smem = sizeof(WideSmem);
   static_assert(smem <= 232448, "");
   static std::atomic<unsigned long long> ready{0};
-  st = prepare_kernel(reinterpret_cast<const void*>(wide_kernel<BN>), smem, kWideRegs, ready, "block matmul kernel");
+  st = prepare_kernel(reinterpret_cast<const void*>(wide_kernel), smem, kWideRegs, ready, "block matmul kernel");
   if (st != SMLA_OK) return st;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.tiles, device_sm_count()));
-  wide_kernel<BN><<<grid, kWideThreads, smem, stream>>>(ta, tb, p);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? SMLA_OK : fail_cuda(e, "block matmul launch");
+  const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(p.tiles, device_sm_count() / 2));
+  return launch_cluster(wide_kernel, 2 * pairs, kWideThreads, smem, 2, stream, ta, tb, to, p);
 }
 
 template <int MT, int CS>
@@ -528,45 +705,43 @@ static smla_status_t launch_narrow(const MatmulArgs& a, unsigned* err, cudaStrea
   CUtensorMap ta, tb;
   smla_status_t st = maps(a, MT, 128, &ta, &tb, &p);
   if (st != SMLA_OK) return st;
-  constexpr size_t smem = sizeof(NarrowSmem<MT>);
+  // as many stages as a CTA has blocks: with few of them more CTAs fit an SM
+  // (128 heads x 16 rows, K = 128: 6.5 us with five, 5.4)
+  const int least = CS > 1 ? (MT * 128 * 4 + stage_bytes<MT>() - 1) / stage_bytes<MT>() : 1;
+  const int stages = std::min(most_stages(MT), std::max((p.kb + CS - 1) / CS, least));
+  const size_t smem = static_cast<size_t>(stages) * stage_bytes<MT>() + sizeof(NarrowSmem<MT>);
   static std::atomic<unsigned long long> ready{0};
-  st = prepare_kernel(reinterpret_cast<const void*>(narrow_kernel<MT, CS>), smem, 0, ready, "block matmul kernel");
+  st = prepare_kernel(reinterpret_cast<const void*>(narrow_kernel<MT, CS>),
+                      most_stages(MT) * stage_bytes<MT>() + sizeof(NarrowSmem<MT>), 0, ready, "block matmul kernel");
   if (st != SMLA_OK) return st;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.tiles * CS));
-  cfg.blockDim = dim3(kNarrowThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = CS;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, narrow_kernel<MT, CS>, ta, tb, p);
-  return e == cudaSuccess ? SMLA_OK : fail_cuda(e, "block matmul launch");
+  return launch_cluster(narrow_kernel<MT, CS>, static_cast<unsigned>(p.tiles * CS), kNarrowThreads, smem, CS, stream, ta, tb, p,
+                        stages);
 }
 
 }  // namespace bm
 
 smla_status_t launch_block_matmul(const MatmulArgs& a, unsigned* err, cudaStream_t stream) {
   using namespace bm;
-  const int sms = device_sm_count();
+  const int64_t sms = device_sm_count();
   const auto tiles = [&](int rows, int cols) {
     return static_cast<int64_t>(a.G) * ((a.M + rows - 1) / rows) * ((a.N + cols - 1) / cols);
   };
-  if (a.M > 64 && tiles(128, 128) >= sms) {
-    // the tile that wastes less of its last wave
-    const auto waves = [&](int64_t n) { return (n + sms - 1) / sms; };
-    return 2 * waves(tiles(128, 256)) <= waves(tiles(128, 128)) ? launch_wide<256>(a, err, stream)
-                                                                : launch_wide<128>(a, err, stream);
-  }
   const int kb = (a.K + kBK - 1) / kBK;
+  // The wide form where it is the faster one: a wave of its tiles takes about 1.5 us
+  // and 0.42 a block, a 64-row tile of the narrow form an SM 1.5 us and 0.27 a block
+  // (narrow / wide: 256 x 4096 x 4096 13.6 / 17.5 us, 512 rows 19.5 / 18.4; 512 x 4096 x
+  // 16384 62 / 58; 128 x 24576 x 2048 21.2 / 23.0, 256 rows 31.7 / 23.6; 128 heads x 64 x
+  // 512 x 128 9.1 / 11.2, 128 rows 16.1 / 11.9).
+  const int64_t waves = (tiles(256, BN) + sms / 2 - 1) / (sms / 2);
+  if (a.M > 32 && waves * (72 + 20 * kb) * sms < tiles(64, 128) * (72 + 13 * kb)) return launch_wide(a, err, stream);
   const auto go = [&](auto mt) {
     constexpr int MT = decltype(mt)::value;
     const int64_t n = tiles(MT, 128);
+    // a tile's columns divided while all CTAs still run at once (a cluster of eight
+    // leaves some of a GPC's SMs out: 38 tiles of 128 blocks 17.9 us in clusters of four,
+    // 22.5 of eight)
     int cs = 1;
-    while (cs < 8 && n * cs < 2 * sms && kb >= 4 * cs) cs *= 2;
+    while (cs < 8 && 2 * n * cs <= 2 * sms - sms / 4 && kb >= 4 * cs) cs *= 2;
     switch (cs) {
       case 1: return launch_narrow<MT, 1>(a, err, stream);
       case 2: return launch_narrow<MT, 2>(a, err, stream);

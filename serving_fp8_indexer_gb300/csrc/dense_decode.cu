@@ -80,6 +80,7 @@ constexpr int kConvWarp = 12;
 constexpr int kConvPer = kHalf * 18 / 128;  // 16-byte pieces of half a block for each of 128 threads
 __host__ __device__ constexpr int conv_groups(int nr) { return nr == 64 ? 1 : 2; }
 constexpr int threads_of(Cache c, int nr) { return c == kFourBit ? kThreads + 128 * conv_groups(nr) : kThreads; }
+constexpr int kAhead = 4;  // blocks whose rows are requested from HBM ahead of their conversion
 constexpr int fp4_regs(int nr) { return nr == 64 ? 128 : 96; }
 
 template <int NR, int QP>
@@ -97,6 +98,7 @@ struct Smem {
   float sums[4][NR];           // row sums of each quarter of the key lanes
   int nk[NR];                  // keys each row sees
   uint2 table[16];             // 4-bit cache: e4m3 bytes by shift
+  int converted;               // and blocks turned into e4m3
   unsigned long long bar_qraw, bar_q, bar_full[kNST], bar_empty[kNST][2];
   unsigned long long bar_s[2], bar_s_free[2], bar_p[2][2], bar_more[2], bar_pv[2], bar_drain[2];
   uint32_t tmem_base;
@@ -124,6 +126,18 @@ __device__ __forceinline__ void split3(float a, float b, uint16_t& t1, uint16_t&
   h = hsub2(h, e5m2x2_to_f16x2(t1));
   t2 = f16x2_to_e5m2x2(h);
   t3 = f16x2_to_e5m2x2(hsub2(h, e5m2x2_to_f16x2(t2)));
+}
+
+// 16 bytes of codes and their shifts if `in`; else what v and sh held (keys past the
+// end weigh 0, and every code is a finite number).  Volatile: the loads stay
+// where they are among the conversions; gathered ahead of them their addresses
+// took the registers of the pieces.
+__device__ __forceinline__ void load_piece(const uint8_t* at, const uint8_t* shifts, bool in, uint4& v, uint32_t& sh) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %7, 0;\n\t@p ld.global.v4.u32 {%0, %1, %2, %3}, [%5];\n\t"
+      "@p ld.global.u8 %4, [%6];\n\t}"
+      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w), "+r"(sh)
+      : "l"(at), "l"(shifts), "r"(static_cast<uint32_t>(in)));
 }
 
 template <int NR, int QP, Cache CACHE>
@@ -168,6 +182,7 @@ __global__ void __launch_bounds__(threads_of(CACHE, NR), 1)
     fence_mbar_init();
   }
   if (threadIdx.x < NR) s.mx[threadIdx.x] = kOrdMin;
+  if (threadIdx.x == 0) s.converted = 0;
   if (warp == kQkWarp) {
     tmem_alloc(smem_u32(&s.tmem_base), kTmemCols);
     tmem_relinquish();
@@ -589,9 +604,7 @@ __global__ void __launch_bounds__(threads_of(CACHE, NR), 1)
     // Four warps take half a block's keys at a time.  A thread holds nine 16-byte
     // pieces (32 columns) of its next half in registers, fetched as it spends
     // those of the one before: rows are read as they lie in memory, 320 bytes
-    // a key, whatever the page size.  A piece becomes 32 e4m3 bytes, of which the
-    // lanes of odd 128-column chunks store the second sixteen first: eight
-    // neighbouring lanes then meet all banks.
+    // a key, whatever the page size.
     setmaxnreg_dec<(NR == 64 ? 104 : 96)>();
     const int ct = (warp - kConvWarp) % 4 * 32 + lane;
     int half = (warp - kConvWarp) >> 2;  // of the keys that are fetched next
@@ -599,41 +612,40 @@ __global__ void __launch_bounds__(threads_of(CACHE, NR), 1)
     Seg g;
     int j = 0;
     bool live = next_seg(p, cur, g);
-    // Page of eight keys of the half for each of the first eight lanes (-1:
-    // none).  A bad one is reported, and its keys read as zeros.
-    const auto read_page = [&]() -> int {
+    // First physical row of eight keys of the half for each of the first eight
+    // lanes (-1: none).  A bad page is reported.
+    const auto read_rows = [&]() -> int {
       const int key = (g.j0 + j) * kBK + half * kHalf + lane * 8;
       if (lane >= kHalf / 8 || key >= seg_keys(g)) return -1;
       const int pid = p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)];
       const int64_t row = (static_cast<int64_t>(pid) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
       if (pid < 0 || row + min(8, seg_keys(g) - key) > p.phys_rows) {
         atomicOr(p.err, kErrPage);
-        if (pid < 0) return -1;
+        return -1;
       }
-      return pid;
+      return static_cast<int>(row);
     };
     uint4 v[kConvPer];
     uint32_t sh[kConvPer];
-    // Passes 0..7: eight rows of sixteen pieces, the row's place in the swizzle the
-    // same in each; pass 8: the two rotary pieces of all 64 rows.
-    const int r0 = ct >> 4, c0 = ct & 15, r8 = ct >> 1, c8 = 16 + (ct & 1);
-    const auto fetch = [&](int k, int pid_l) {
-      const int r = k < 8 ? 8 * k + r0 : r8, c = k < 8 ? c0 : c8;
-      const int key = (g.j0 + j) * kBK + half * kHalf + r;
-      const int pid = __shfl_sync(0xffffffffu, pid_l, k < 8 ? k : r8 >> 3);
-      const int64_t row = (static_cast<int64_t>(pid) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
+#pragma unroll
+    for (int k = 0; k < kConvPer; ++k) {
       v[k] = make_uint4(0u, 0u, 0u, 0u);
       sh[k] = 0;
-      if (pid >= 0 && key < seg_keys(g) && row < p.phys_rows) {
-        const uint8_t* at = p.pool + row * kFp4Row;
-        v[k] = *reinterpret_cast<const uint4*>(at + c * 16);
-        sh[k] = at[kFp4Shifts + c];
-      }
+    }
+    // Passes 0..7: eight rows of sixteen pieces, the row's place in the swizzle the
+    // same in each; pass 8: the two rotary pieces of all 64 rows.  Eight neighbouring
+    // lanes hold four pieces of two rows: their 16-byte stores meet all banks.
+    const int r0 = (ct >> 2 & 1) | ct >> 5 << 1, c0 = (ct & 3) | (ct >> 3 & 3) << 2, r8 = ct >> 1, c8 = 16 + (ct & 1);
+    const uint8_t* const from = p.pool + r0 * kFp4Row + c0 * 16;
+    const uint8_t* const from8 = p.pool + (r8 & 7) * kFp4Row + c8 * 16;
+    const int shift_at = kFp4Shifts - 15 * c0, shift_at8 = kFp4Shifts - 15 * c8;  // from a piece to its shifts
+    const auto fetch = [&](int k, int rows, int left) {  // left: keys from the half's first on
+      const int row = __shfl_sync(0xffffffffu, rows, k < 8 ? k : r8 >> 3);
+      const uint8_t* at = (k < 8 ? from : from8) + static_cast<int64_t>(row) * kFp4Row;
+      load_piece(at, at + (k < 8 ? shift_at : shift_at8), row >= 0 && (k < 8 ? 8 * k + r0 : r8) < left, v[k], sh[k]);
     };
-    // where a pass's two sixteens go: in the odd 128-column chunks the second first
-    const int odd = (c0 >> 2) & 1, piece = 2 * (c0 & 3);
-    const uint32_t first = (c0 >> 2) * kChunk + sw128(r0, piece + odd);
-    const uint32_t second = (c0 >> 2) * kChunk + sw128(r0, piece + 1 - odd);
+    const auto keys_left = [&] { return seg_keys(g) - ((g.j0 + j) * kBK + half * kHalf); };
+    const uint32_t first = (c0 >> 2) * kChunk + sw128(r0, 2 * (c0 & 3)), second = (c0 >> 2) * kChunk + sw128(r0, 2 * (c0 & 3) + 1);
     const uint32_t rope0 = kRopeOff + sw64(r8, 2 * (ct & 1)), rope1 = kRopeOff + sw64(r8, 2 * (ct & 1) + 1);
     const auto advance = [&] {
       if (conv_groups(NR) == 1) {
@@ -646,17 +658,19 @@ __global__ void __launch_bounds__(threads_of(CACHE, NR), 1)
       }
     };
     bool have = live;
-    int pid = live ? read_page() : -1;
+    int rows = live ? read_rows() : -1, left = 0;
     if (live) {
+      left = keys_left();
 #pragma unroll
-      for (int k = 0; k < kConvPer; ++k) fetch(k, pid);
+      for (int k = 0; k < kConvPer; ++k) fetch(k, rows, left);
       advance();
-      if (live) pid = read_page();
+      if (live) rows = read_rows();
     }
     for (int n = 0; have; ++n) {
       const int i = conv_groups(NR) == 1 ? n >> 1 : n, slot = i % kNST;
       const int h = conv_groups(NR) == 1 ? n & 1 : (warp - kConvWarp) >> 2;  // of the keys that are converted
       const bool next = live;
+      left = next ? keys_left() : 0;
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_empty[slot][h]), ((i / kNST) & 1) ^ 1, p.err))) break;
       uint8_t* kv = s.kv[slot] + h * (kHalf * 128);
       uint8_t* kv_rope = s.kv[slot] + h * (kHalf * 64);
@@ -666,10 +680,10 @@ __global__ void __launch_bounds__(threads_of(CACHE, NR), 1)
         const uint2 a = fp4x8_to_e4m3x8(v[k].x, t0), b = fp4x8_to_e4m3x8(v[k].y, t0);
         const uint2 d = fp4x8_to_e4m3x8(v[k].z, t1), e = fp4x8_to_e4m3x8(v[k].w, t1);
         const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
-        if (next) fetch(k, pid);
+        fetch(k, rows, left);  // (none behind the last block)
         if (k < 8) {
-          *reinterpret_cast<uint4*>(kv + first + k * 1024) = odd ? hi : lo;
-          *reinterpret_cast<uint4*>(kv + second + k * 1024) = odd ? lo : hi;
+          *reinterpret_cast<uint4*>(kv + first + k * 1024) = lo;
+          *reinterpret_cast<uint4*>(kv + second + k * 1024) = hi;
         } else {
           *reinterpret_cast<uint4*>(kv_rope + rope0) = lo;
           *reinterpret_cast<uint4*>(kv_rope + rope1) = hi;
@@ -677,21 +691,38 @@ __global__ void __launch_bounds__(threads_of(CACHE, NR), 1)
       }
       fence_proxy_async_smem();
       warp_arrive(smem_u32(&s.bar_full[slot]), lane);
+      if (threadIdx.x == kConvWarp * 32) *const_cast<volatile int*>(&s.converted) = i + 1;
       have = next;
       if (next) {
         advance();
-        if (live) pid = read_page();
+        if (live) rows = read_rows();
       }
     }
   } else {
     if constexpr (CACHE == kFourBit) setmaxnreg_dec<(NR == 64 ? 72 : 64)>();
   if (CACHE == kFourBit && warp == kTmaWarp) {
-    // the first segment's q (the QK warp requests the others)
+    // The first segment's q (the QK warp requests the others), then the rows of
+    // the blocks ahead into L2: the half a block that the converting warps have in
+    // flight covers L2's latency, but not HBM's.
     Cursor cur = start;
     Seg g;
     const bool leader = elect_one();
-    if (next_seg(p, cur, g) && leader) load_q(g);
+    bool more = next_seg(p, cur, g);
+    if (leader && more) load_q(g);
     __syncwarp();
+    const int box = min(1 << p.seqs.page_shift, kHalf);
+    for (int i = 0; more; more = next_seg(p, cur, g)) {
+      for (int j = 0; j < g.nb; ++j, ++i) {
+        const unsigned long long t0 = global_timer_ns();
+        while (i - *const_cast<volatile int*>(&s.converted) > kAhead && global_timer_ns() - t0 < kWaitLimitNs) __nanosleep(200);
+        const int key = (g.j0 + j) * kBK + lane * box;
+        if (lane * box >= kBK || key >= seg_keys(g)) continue;
+        const int pid = p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)];
+        const int64_t row = (static_cast<int64_t>(pid) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
+        const int n = min(box, seg_keys(g) - key);
+        if (pid >= 0 && row + n <= p.phys_rows) prefetch_l2(p.pool + row * kFp4Row, n * kFp4Row);
+      }
+    }
   } else if (CACHE != kFourBit && warp == kTmaWarp) {
     // ============================================================= key blocks
     // A block's keys come in parts of a page, up to 64 keys each: five boxes a
