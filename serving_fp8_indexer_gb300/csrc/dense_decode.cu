@@ -80,7 +80,7 @@ constexpr int kConvWarp = 12;
 constexpr int kConvPer = kHalf * 18 / 128;  // 16-byte pieces of half a block for each of 128 threads
 __host__ __device__ constexpr int conv_groups(int nr) { return nr == 64 ? 1 : 2; }
 constexpr int threads_of(Cache c, int nr) { return c == kFourBit ? kThreads + 128 * conv_groups(nr) : kThreads; }
-constexpr int kAhead = 4;  // blocks whose rows are requested from HBM ahead of their conversion
+constexpr int kAhead = 2;  // blocks whose rows are requested from HBM ahead of their conversion
 constexpr int fp4_regs(int nr) { return nr == 64 ? 128 : 96; }
 
 template <int NR, int QP>

@@ -3,8 +3,8 @@
 // all in 32 bits with one rounding at the end.
 //
 // Bound: HBM (2 bytes read and 1 written an element).  Without the norm the
-// blocks are independent: sixteen lanes hold a block's 128 columns (16 bytes a
-// lane), find its largest magnitude with four shuffles and store 8 bytes a lane.
+// blocks are independent: eight lanes hold a block's 128 columns (32 bytes a
+// lane), find its largest magnitude with three shuffles and store 16 bytes a lane.
 // With it a row is read once, kept in registers as bf16 and summed first.
 #include <algorithm>
 
@@ -20,31 +20,42 @@ constexpr int kBlock = 128;
 struct Params {
   const __nv_bfloat16* x;
   int64_t x_stride;
-  int M, K, chunks, nblk;  // chunks of 8 columns, blocks of 128
+  int M, K, chunks, nblk;  // chunks of 16 columns, blocks of 128
   const __nv_bfloat16* w;
   float eps;
   uint8_t* out;
   float* scales;
 };
 
-// Chunk c (8 columns) of a row, held by lanes in order: its block's scale and
+// Chunk c (16 columns) of a row, held by lanes in order: its block's scale and
 // its bytes.  All lanes of the warp call; `in`: the chunk exists.
-__device__ __forceinline__ void quantize_chunk(const Params& p, int64_t row, int c, bool in, float (&v)[8], int lane) {
+__device__ __forceinline__ void quantize_chunk(const Params& p, int64_t row, int c, bool in, float (&v)[2][8], int lane) {
   float amax = 0.f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) amax = fmaxf(amax, finite_abs(v[k]));
+  for (int k = 0; k < 8; ++k) amax = max3(amax, finite_abs(v[0][k]), finite_abs(v[1][k]));
 #pragma unroll
-  for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  for (int o = 4; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const float scale = scale_of(amax), inv = 1.f / scale;
   if (!in) return;
-  float q[8];
+  uint2 q[2];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) q[k] = quotient(v[k], scale, inv);
-  *reinterpret_cast<uint2*>(p.out + row * p.K + c * 8) = pack_e4m3x8(q);
-  if ((lane & 15) == 0) p.scales[row * p.nblk + (c >> 4)] = scale;
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[h][k] = quotient(v[h][k], scale, inv);
+    q[h] = pack_e4m3x8(v[h]);
+  }
+  __stcs(reinterpret_cast<uint4*>(p.out + row * p.K + c * 16), make_uint4(q[0].x, q[0].y, q[1].x, q[1].y));
+  if ((lane & 7) == 0) p.scales[row * p.nblk + (c >> 3)] = scale;
+}
+struct Raw {
+  uint4 a, b;
+};
+__device__ __forceinline__ void unpack(const Raw& r, float (&v)[2][8]) {
+  unpack_bf16x8(r.a, v[0]);
+  unpack_bf16x8(r.b, v[1]);
 }
 
-// A warp takes kLoads * 256 columns of a row.
+// A warp takes kLoads * 512 columns of a row.
 template <int kLoads>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const Params p, int units_per_row, int64_t units) {
   const int lane = threadIdx.x & 31;
@@ -52,17 +63,18 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const Params p, int 
   if (u >= units) return;
   const int64_t row = u / units_per_row;
   const int c0 = static_cast<int>(u - row * units_per_row) * (kLoads * 32) + lane;
-  const __nv_bfloat16* x = p.x + row * p.x_stride;
-  uint4 raw[kLoads];
+  const uint4* x = reinterpret_cast<const uint4*>(p.x + row * p.x_stride);
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  Raw raw[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const int c = c0 + 32 * i;
-    raw[i] = c < p.chunks ? __ldcs(reinterpret_cast<const uint4*>(x + c * 8)) : make_uint4(0, 0, 0, 0);
+    raw[i] = c < p.chunks ? Raw{__ldcs(x + 2 * c), __ldcs(x + 2 * c + 1)} : Raw{none, none};
   }
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    float v[8];
-    unpack_bf16x8(raw[i], v);
+    float v[2][8];
+    unpack(raw[i], v);
     quantize_chunk(p, row, c0 + 32 * i, c0 + 32 * i < p.chunks, v, lane);
   }
 }
@@ -76,20 +88,23 @@ __global__ void __launch_bounds__(kThreads) quantize_norm_kernel(const Params p)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rt = threadIdx.x % kRowThreads;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / kRowThreads) + threadIdx.x / kRowThreads;
   const bool live = row < p.M;  // (whole warps; the others only keep the barrier)
-  const __nv_bfloat16* x = p.x + (live ? row : 0) * p.x_stride;
-  uint4 raw[kLoads];
+  const uint4* x = reinterpret_cast<const uint4*>(p.x + (live ? row : 0) * p.x_stride);
+  const uint4* weight = reinterpret_cast<const uint4*>(p.w);
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  Raw raw[kLoads], w0{none, none};
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const int c = rt + kRowThreads * i;
-    raw[i] = live && c < p.chunks ? *reinterpret_cast<const uint4*>(x + c * 8) : make_uint4(0, 0, 0, 0);
+    raw[i] = live && c < p.chunks ? Raw{x[2 * c], x[2 * c + 1]} : Raw{none, none};
   }
+  if (rt < p.chunks) w0 = Raw{weight[2 * rt], weight[2 * rt + 1]};  // beside the row's, not behind its sum
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    float v[8];
-    unpack_bf16x8(raw[i], v);
+    float v[2][8];
+    unpack(raw[i], v);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) ss = fmaf(v[k], v[k], ss);
+    for (int k = 0; k < 8; ++k) ss = fmaf(v[1][k], v[1][k], fmaf(v[0][k], v[0][k], ss));
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -106,11 +121,14 @@ __global__ void __launch_bounds__(kThreads) quantize_norm_kernel(const Params p)
   for (int i = 0; i < kLoads; ++i) {
     const int c = rt + kRowThreads * i;
     const bool in = c < p.chunks;
-    float v[8], w[8];
-    unpack_bf16x8(raw[i], v);
-    unpack_bf16x8(in ? *reinterpret_cast<const uint4*>(p.w + c * 8) : make_uint4(0, 0, 0, 0), w);
+    if (i > 0) w0 = in ? Raw{weight[2 * c], weight[2 * c + 1]} : Raw{none, none};
+    float v[2][8], w[2][8];
+    unpack(raw[i], v);
+    unpack(w0, w);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = v[k] * rstd * w[k];
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[h][k] = v[h][k] * rstd * w[h][k];
     quantize_chunk(p, row, c, in, v, lane);
   }
 }
@@ -124,7 +142,7 @@ smla_status_t launch_quantize(const QuantizeArgs& a, cudaStream_t stream) {
   p.x_stride = a.x_stride;
   p.M = a.M;
   p.K = a.K;
-  p.chunks = a.K / 8;
+  p.chunks = a.K / 16;
   p.nblk = (a.K + kBlock - 1) / kBlock;
   p.w = static_cast<const __nv_bfloat16*>(a.norm_weight);
   p.eps = a.norm_eps;
@@ -132,11 +150,11 @@ smla_status_t launch_quantize(const QuantizeArgs& a, cudaStream_t stream) {
   p.scales = a.scales;
   if (p.w) {
     if (a.K <= 1024)
-      quantize_norm_kernel<32, 4><<<(a.M + 7) / 8, kThreads, 0, stream>>>(p);
+      quantize_norm_kernel<32, 2><<<(a.M + 7) / 8, kThreads, 0, stream>>>(p);
     else if (a.K <= 4096)
-      quantize_norm_kernel<256, 2><<<a.M, kThreads, 0, stream>>>(p);
+      quantize_norm_kernel<256, 1><<<a.M, kThreads, 0, stream>>>(p);
     else
-      quantize_norm_kernel<256, 8><<<a.M, kThreads, 0, stream>>>(p);
+      quantize_norm_kernel<256, 4><<<a.M, kThreads, 0, stream>>>(p);
   } else {
     const auto go = [&](auto kernel, int loads) {
       const int per_row = (p.chunks + 32 * loads - 1) / (32 * loads);
