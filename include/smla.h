@@ -499,7 +499,8 @@ smla_status_t smla_dense_decode_fp4(const void* q, int32_t q_dtype, const uint8_
  * NaN stays NaN and infinities saturate.
  *   x            bf16, rows x_stride elements apart (a multiple of 8, >= 0)
  *   norm_weight  bf16 [K], or NULL for no norm
- *   out          e4m3 [M, K], dense;  scales f32 [M, ceil(K / 128)], dense
+ *   out          e4m3 [M, K], dense;  scales f32 [M, ceil(K / 128)], dense (neither
+ *                overlapping x)
  * K: a multiple of 16, up to 2^20 (16384 with a norm).  Alignment: x,
  * norm_weight, out 16 bytes; scales 4. */
 smla_status_t smla_quantize_blocks(const uint16_t* x, int64_t x_stride, int32_t M, int32_t K, const uint16_t* norm_weight,
@@ -517,11 +518,13 @@ smla_status_t smla_quantize_blocks(const uint16_t* x, int64_t x_stride, int32_t 
  * A batch of heads is G = heads with the token stride as the row stride: the
  * projections of queries into the latent space and of attention outputs out of it
  * need no transposition.  Rows of a past M, and columns of b past K, are not read.
- * K: a multiple of 16, 16 .. 2^20; N a multiple of 8.  Strides: a's multiples
- * of 16, out's of 8, at least the row's width; out's rows may not share
- * memory (its larger stride spans the other dimension).  A stride of a
- * dimension of one element does not matter.  Alignment: a, b, out 16 bytes; the
- * scales 4. */
+ * K: a multiple of 16, 16 .. 2^20; N a multiple of 8, up to 2^28.  Strides: a's
+ * multiples of 16, out's of 8, at least the row's width; out's rows may not share
+ * memory (its larger stride spans the other dimension), nor may out and an operand.
+ * A stride of a dimension of one element does not matter.  Alignment: a, b, out 16
+ * bytes; the scales 4.  A result does not depend on the run, nor on the other rows of a
+ * or b, but may differ in its last bits with the numbers of rows (G, M, N), by which
+ * the order of its sum over k is chosen. */
 smla_status_t smla_block_matmul(const uint8_t* a, int64_t a_group_stride, int64_t a_row_stride, const float* a_scales,
                                 int64_t as_group_stride, int64_t as_row_stride, const uint8_t* b, const float* b_scales,
                                 int32_t G, int32_t M, int32_t N, int32_t K, void* out, int32_t out_dtype,

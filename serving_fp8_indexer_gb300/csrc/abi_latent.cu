@@ -277,7 +277,19 @@ smla_status_t smla_block_matmul(const uint8_t* a, int64_t a_group_stride, int64_
     return fail(SMLA_ERR_UNSUPPORTED, "K=%d must be a multiple of 16 in [16, 2^20]", K);
   if (N % 8) return fail(SMLA_ERR_UNSUPPORTED, "N=%d must be a multiple of 8", N);
   constexpr int32_t kMost = 1 << 30;
-  if (M > kMost || N > kMost || G > kMost) return fail(SMLA_ERR_UNSUPPORTED, "G, M and N must be at most 2^30");
+  if (M > kMost || N > kMost / 4 || G > kMost)
+    return fail(SMLA_ERR_UNSUPPORTED, "G and M must be at most 2^30, N at most 2^28");
+  // (a dimension of one element has no stride to speak of)
+  if (M == 1) {
+    a_row_stride = K;
+    as_row_stride = 0;
+    out_row_stride = N;
+  }
+  if (G == 1) {
+    a_group_stride = K;
+    as_group_stride = 0;
+    out_group_stride = N;
+  }
   if (out_dtype != SMLA_BF16 && out_dtype != SMLA_F32)
     return fail(SMLA_ERR_INVALID_ARG, "out_dtype=%d must be bf16 or f32", out_dtype);
   const auto wide_enough = [](int64_t n, int64_t s, int64_t width) { return n <= 1 || s >= width; };

@@ -234,6 +234,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         // 166 us).  The tensor's ends are the store's to mind.
         const int per = p.out_f32 ? 16 : 32;
         const auto put = [&](int c, int place, auto&& piece) {  // columns [c, c + per)
+          if (n0 + c >= p.N) {  // (an empty group: the wait for a place counts them)
+            if (lane == 0) tma_store_commit();
+            return;
+          }
           uint8_t* stage = s.out[warp][place];
           if (lane == 0) tma_store_wait_read<S::kPlaces - 1>();
           __syncwarp();
@@ -251,19 +255,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (p.out_f32) {
 #pragma unroll
           for (int c = 0; c < kCols; c += 16)
-            if (n0 + c < p.N)
-              put(c, c / 16 % S::kPlaces, [&](int k) {
-                const float* f = acc + c + 4 * k;
-                return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-              });
+            put(c, c / 16 % S::kPlaces, [&](int k) {
+              const float* f = acc + c + 4 * k;
+              return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+            });
         } else {
 #pragma unroll
           for (int c = 0; c < kCols; c += 32)
-            if (n0 + c < p.N)
-              put(c, c / 32 % S::kPlaces, [&](int k) {
-                const float* f = acc + c + 8 * k;
-                return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
-              });
+            put(c, c / 32 % S::kPlaces, [&](int k) {
+              const float* f = acc + c + 8 * k;
+              return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+            });
         }
       }
     }
@@ -483,7 +485,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     int buf = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int kc = kb0; ok && kc < kb1; kc += kNarrowChunk) {
+    // (a warp whose wait gives up still keeps the chunks' barriers)
+    for (int kc = kb0; kc < kb1; kc += kNarrowChunk) {
       if (kc > kb0) named_bar_sync(1, 128);  // the chunk before has been used
 #pragma unroll
       for (int j = 0; j < kPer; ++j) s.scale[lane][warp * kPer + j] = next[j];
@@ -491,9 +494,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
       if (kc + kNarrowChunk < kb1) fetch(kc + kNarrowChunk);
       const int n = min(kNarrowChunk, kb1 - kc);
 #pragma unroll 1
-      for (int k = 0; k < n; ++k) {
-        // (a wait that gives up lets the others run into their own limits)
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.sum_full[buf]), phase, p.err))) ok = false;
+      for (int k = 0; ok && k < n; ++k) {
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.sum_full[buf]), phase, p.err));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t a = tmem + lanes + buf * MT;
         const float* sc = s.scale[k];

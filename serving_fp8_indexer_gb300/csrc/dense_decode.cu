@@ -711,12 +711,17 @@ __global__ void __launch_bounds__(threads_of(CACHE, NR), 1)
     if (leader && more) load_q(g);
     __syncwarp();
     const int box = min(1 << p.seqs.page_shift, kHalf);
-    for (int i = 0; more; more = next_seg(p, cur, g)) {
-      for (int j = 0; j < g.nb; ++j, ++i) {
+    for (int i = 0; more; more = more && next_seg(p, cur, g)) {
+      for (int j = 0; more && j < g.nb; ++j, ++i) {
+        // (nothing depends on these: conversions that have stopped end them)
         const unsigned long long t0 = global_timer_ns();
-        while (i - *const_cast<volatile int*>(&s.converted) > kAhead && global_timer_ns() - t0 < kWaitLimitNs) __nanosleep(200);
+        while (more && i - *const_cast<volatile int*>(&s.converted) > kAhead) {
+          __nanosleep(200);
+          more = global_timer_ns() - t0 < kWaitLimitNs;
+        }
+        more = __all_sync(0xffffffffu, more);
         const int key = (g.j0 + j) * kBK + lane * box;
-        if (lane * box >= kBK || key >= seg_keys(g)) continue;
+        if (!more || lane * box >= kBK || key >= seg_keys(g)) continue;
         const int pid = p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)];
         const int64_t row = (static_cast<int64_t>(pid) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
         const int n = min(box, seg_keys(g) - key);

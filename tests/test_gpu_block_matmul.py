@@ -109,6 +109,45 @@ def test_broadcast_scales_and_one_element_dimensions():
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("G,M", [(1, 1), (1, 300), (5, 1)])
+def test_strides_of_one_element_do_not_matter(G, M):
+    """As the C interface says: whatever stands there, 0 and negative numbers too."""
+    from serving_fp8_indexer_gb300 import _lib
+
+    lib, N, K = _lib.load(), 20000, 256
+    g = _gen(6)
+    a, sa, av = _operand(g, G, M, K, True)
+    b, sb, bv = _operand(g, G, N, K, False)
+    for odd in (0, -32, 1 << 40):
+        out = torch.full((G, M, N), float("nan"), device="cuda")
+        st = lib.smla_block_matmul(a.data_ptr(), odd if G == 1 else M * K, odd if M == 1 else K, sa.data_ptr(),
+                                   odd if G == 1 else M * 2, odd if M == 1 else 2, b.data_ptr(), sb.data_ptr(), G, M, N, K,
+                                   out.data_ptr(), 2, odd if G == 1 else M * N, odd if M == 1 else N, None)
+        assert st == 0, _lib.last_error(lib)
+        smla.check_device_errors()
+        _close(out, av, bv)
+
+
+@pytest.mark.parametrize("N", [8, 40, 264, 2088])
+def test_many_tiles_with_few_columns(N):
+    """Tiles whose last columns lie past N, one after the other on each SM: a
+    place on the way out is not taken again before it has been read."""
+    g = _gen(N)
+    M, K = 60000, 128
+    a, sa, av = _operand(g, 1, M, K, True)
+    b, sb, bv = _operand(g, 1, N, K, False)
+    for dtype in (torch.bfloat16, torch.float32):
+        first = None
+        for _ in range(4):
+            out = torch.full((M, N), float("nan"), dtype=dtype, device="cuda")
+            smla.block_matmul(a[0], sa[0], b[0], sb[0], out)
+            if first is None:
+                first = out
+                _close(out[None], av, bv)
+            assert torch.equal(first, out)
+    smla.check_device_errors()
+
+
 @pytest.mark.parametrize("M", [4, 200])
 def test_special_values_stay_in_their_rows_and_columns(M):
     g = _gen(4)

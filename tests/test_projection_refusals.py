@@ -54,7 +54,7 @@ def test_matmul_refusals(lib):
                    (dict(s=None), INVALID), (dict(b=None), INVALID), (dict(bs=None), INVALID), (dict(out=None), INVALID),
                    (dict(a=P + 8), INVALID), (dict(b=P + 8), INVALID), (dict(out=P + 8), INVALID), (dict(s=P + 2), INVALID),
                    (dict(bs=P + 1), INVALID), (dict(M=1 << 30, N=256, ag=1 << 37, og=256, om=512), UNSUPPORTED),
-                   (dict(M=(1 << 30) + 1), UNSUPPORTED), (dict(N=1 << 30, K=1 << 10, am=1024, ag=4096, om=1 << 30, og=1 << 32), UNSUPPORTED)):
+                   (dict(M=(1 << 30) + 1), UNSUPPORTED), (dict(N=(1 << 28) + 8), UNSUPPORTED), (dict(N=1 << 28, K=1 << 10, am=1024, ag=4096, om=1 << 28, og=1 << 30), UNSUPPORTED)):
         assert call(**kw) == st, (kw, _lib.last_error(lib))
     for kw in (dict(G=0), dict(M=0), dict(N=0)):
         assert call(a=None, s=None, b=None, bs=None, out=None, **kw) == 0, kw
