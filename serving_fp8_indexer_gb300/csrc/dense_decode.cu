@@ -134,7 +134,7 @@ __device__ __forceinline__ void split3(float a, float b, uint16_t& t1, uint16_t&
 // took the registers of the pieces.
 __device__ __forceinline__ void load_piece(const uint8_t* at, const uint8_t* shifts, bool in, uint4& v, uint32_t& sh) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %7, 0;\n\t@p ld.global.v4.u32 {%0, %1, %2, %3}, [%5];\n\t"
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %7, 0;\n\t@p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%5];\n\t"
       "@p ld.global.u8 %4, [%6];\n\t}"
       : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w), "+r"(sh)
       : "l"(at), "l"(shifts), "r"(static_cast<uint32_t>(in)));

@@ -80,13 +80,6 @@ SMLA_DEVICE_INLINE uint2 fp4_table_entry(int shift) {
                     static_cast<uint32_t>(f32x2_to_e4m3x2(2.f * u, 3.f * u)) |
                         static_cast<uint32_t>(f32x2_to_e4m3x2(4.f * u, 6.f * u)) << 16);
 }
-// The same, computed where the bytes are normal numbers (shifts up to 11: a step of
-// the shift takes one from their exponents), and read from `table` elsewhere.
-SMLA_DEVICE_INLINE uint2 fp4_entry(uint32_t shift, const uint2* table) {
-  uint2 t = make_uint2(0x6C686000u - shift * 0x08080800u, 0x7C787470u - shift * 0x08080808u);
-  if (shift > 11) t = table[shift];
-  return t;
-}
 // Eight codes -> eight e4m3 bytes, by the entry t of their block's shift: each
 // code's three magnitude bits select a byte, then the signs are put in.
 SMLA_DEVICE_INLINE uint2 fp4x8_to_e4m3x8(uint32_t w, uint2 t) {
