@@ -25,6 +25,7 @@ _DTYPES = {torch.bfloat16: SMLA_BF16, torch.uint8: SMLA_E4M3, torch.float32: SML
 # These calls take a few microseconds on the GPU, so the checks below keep to
 # the cheapest queries of a tensor, and the message is put together only when
 # one fails.
+_U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
 _device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -70,13 +71,20 @@ def _rows(t, name, dtypes, dev, ndim):
 def _seqs(s: Seqs, dev: int, paged: bool = True) -> SeqsT:
     """The C struct of a batch whose arrays hold what the kernels read: B + 1
     entries, B, and (`paged`: where pages are looked up) B rows of max_pages."""
-    i32, table, B = torch.int32, s.page_table, s.B
-    c = SeqsT(_flat(s.cu_q, "cu_q", i32, dev, 1), _flat(s.kv_len, "kv_len", i32, dev, 1),
-              _flat(table, "page_table", i32, dev, 2), B, s.max_pages, s.page_size, s.T)
-    if s.cu_q.shape[0] <= B or s.kv_len.shape[0] < B or paged and (table.shape[0] < B or table.shape[1] != s.max_pages):
-        raise ValueError(f"seqs: cu_q {tuple(s.cu_q.shape)}, kv_len {tuple(s.kv_len.shape)} and page_table "
-                         f"{tuple(table.shape)} do not hold B={B} sequences of max_pages={s.max_pages}")
-    return c
+    cu, kv, table, B = s.cu_q, s.kv_len, s.page_table, s.B
+    try:  # (all checks at once; which one fails is found out below)
+        nc, nk, nt = cu.shape, kv.shape, table.shape
+        if (cu.dtype is _I32 and kv.dtype is _I32 and table.dtype is _I32 and cu.get_device() == dev and
+                kv.get_device() == dev and table.get_device() == dev and len(nc) == 1 and len(nk) == 1 and len(nt) == 2 and
+                nc[0] > B and nk[0] >= B and (not paged or nt[0] >= B and nt[1] == s.max_pages) and cu.is_contiguous() and
+                kv.is_contiguous() and table.is_contiguous()):
+            return SeqsT(cu.data_ptr(), kv.data_ptr(), table.data_ptr(), B, s.max_pages, s.page_size, s.T)
+    except AttributeError:
+        pass
+    for t, name, ndim in ((cu, "cu_q", 1), (kv, "kv_len", 1), (table, "page_table", 2)):
+        _flat(t, name, _I32, dev, ndim)
+    raise ValueError(f"seqs: cu_q {tuple(cu.shape)}, kv_len {tuple(kv.shape)} and page_table "
+                     f"{tuple(table.shape)} do not hold B={B} sequences of max_pages={s.max_pages}")
 
 
 def _on(stream, dev: int) -> int:
@@ -348,12 +356,12 @@ def quantize_blocks(x: torch.Tensor, out: torch.Tensor, scales: torch.Tensor, no
     [M, K] (rows may be strided): a scale for each 128 columns, after an RMS norm
     over the row when its weight bf16 [K] is given."""
     lib, dev = _lib._lib or _lib.load(), _device()
-    xp, (M, K), xs = _rows(x, "x", (torch.bfloat16,), dev, 2)
-    if out.shape != (M, K) or scales.shape != (M, -(-K // 128)) or (norm_weight is not None and norm_weight.shape != (K,)):
+    xp, shape, xs = _rows(x, "x", (_BF16,), dev, 2)
+    M, K = shape
+    if out.shape != shape or scales.shape != (M, (K + 127) >> 7) or (norm_weight is not None and norm_weight.shape != (K,)):
         raise ValueError(f"out must be [M={M}, K={K}], scales [M, {-(-K // 128)}], norm_weight [K]")
-    st = lib.smla_quantize_blocks(xp, xs[0], M, K, _flat(norm_weight, "norm_weight", torch.bfloat16, dev, 1), norm_eps,
-                                  _flat(out, "out", torch.uint8, dev, 2), _flat(scales, "scales", torch.float32, dev, 2),
-                                  _on(stream, dev))
+    st = lib.smla_quantize_blocks(xp, xs[0], M, K, _flat(norm_weight, "norm_weight", _BF16, dev, 1), norm_eps,
+                                  _flat(out, "out", _U8, dev, 2), _flat(scales, "scales", _F32, dev, 2), _on(stream, dev))
     if st:
         _check(lib, st)
 
@@ -366,23 +374,34 @@ def block_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sca
     [G, N, K] with b_scales f32 [G, ceil(N / 128), ceil(K / 128)] (contiguous).
     Without a batch all five are 2-D."""
     lib, dev = _lib._lib or _lib.load(), _device()
-    n = a.dim()
-    if n == 2:
-        if not (a_scales.dim() == b.dim() == b_scales.dim() == out.dim() == 2):
-            raise ValueError("a, a_scales, b, b_scales and out must all be 2-D or all 3-D")
-        a, a_scales, b, b_scales, out_g = a[None], a_scales[None], b[None], b_scales[None], out[None]
+    shape, o_shape = a.shape, out.shape
+    n = len(shape)
+    if n == 3:
+        G, M, K = shape
+        lead = (G,)
+    elif n == 2:
+        (M, K), G, lead = shape, 1, ()
     else:
-        out_g = out
-    ap, (G, M, K), a_st = _rows(a, "a", (torch.uint8,), dev, 3)
-    sp, s_shape, s_st = _rows(a_scales, "a_scales", (torch.float32,), dev, 3)
-    op, (og, om, N), o_st = _rows(out_g, "out", (torch.bfloat16, torch.float32), dev, 3)
-    kb = -(-K // 128)
-    if (og != G or om != M or s_shape != (G, M, kb) or b.shape != (G, N, K) or b_scales.shape != (G, -(-N // 128), kb)):
+        raise ValueError(f"a must have 2 or 3 dims, got {n}")
+    N, kb = o_shape[-1] if len(o_shape) else 0, (K + 127) >> 7
+    a_st, s_st, o_st, out_type = a.stride(), a_scales.stride(), out.stride(), out.dtype
+    # (all checks at once; which one fails is found out below)
+    if not (o_shape == (*lead, M, N) and a_scales.shape == (*lead, M, kb) and b.shape == (*lead, N, K) and
+            b_scales.shape == (*lead, (N + 127) >> 7, kb) and a.dtype is _U8 and b.dtype is _U8 and a_scales.dtype is _F32 and
+            b_scales.dtype is _F32 and (out_type is _BF16 or out_type is _F32) and a.get_device() == dev and
+            a_scales.get_device() == dev and b.get_device() == dev and b_scales.get_device() == dev and
+            out.get_device() == dev and (a_st[-1] == 1 or K <= 1) and (o_st[-1] == 1 or N <= 1) and
+            (kb == 1 or s_st[-1] == 1) and b.is_contiguous() and b_scales.is_contiguous()):
+        _rows(a, "a", (_U8,), dev, n)
+        _rows(a_scales, "a_scales", (_F32,), dev, n)
+        _rows(out, "out", (_BF16, _F32), dev, n)
+        _flat(b, "b", _U8, dev, n)
+        _flat(b_scales, "b_scales", _F32, dev, n)
         raise ValueError("a [G, M, K], a_scales [G, M, ceil(K / 128)], b [G, N, K], b_scales [G, ceil(N / 128), ceil(K / "
                          "128)] and out [G, M, N] do not fit each other")
-    st = lib.smla_block_matmul(ap, a_st[0], a_st[1], sp, s_st[0], s_st[1], _flat(b, "b", torch.uint8, dev, 3),
-                               _flat(b_scales, "b_scales", torch.float32, dev, 3), G, M, N, K, op, _DTYPES[out.dtype], o_st[0],
-                               o_st[1], _on(stream, dev))
+    st = lib.smla_block_matmul(a.data_ptr(), a_st[0], a_st[-2], a_scales.data_ptr(), s_st[0], s_st[-2], b.data_ptr(),
+                               b_scales.data_ptr(), G, M, N, K, out.data_ptr(), SMLA_BF16 if out_type is _BF16 else SMLA_F32,
+                               o_st[0], o_st[-2], _on(stream, dev))
     if st:
         _check(lib, st)
     return out

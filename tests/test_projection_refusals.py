@@ -120,8 +120,12 @@ def test_binding_refusals(monkeypatch):
     for kw in (dict(a=bf(2, 4, 128)), dict(out=u8(2, 4, 64)), dict(a_scales=bf(2, 4, 1)), dict(b=f(2, 64, 128))):
         with pytest.raises(TypeError):
             _latent.block_matmul(**{**ok, **kw}, stream=0)
-    with pytest.raises(ValueError, match="2-D"):
-        _latent.block_matmul(u8(4, 128), f(4, 1), u8(1, 64, 128), f(1, 1, 1), bf(4, 64), stream=0)
+    for a, rest in ((u8(4, 128), (f(4, 1), u8(1, 64, 128), f(1, 1, 1), bf(4, 64))),
+                    (u8(4, 128), (f(1, 4, 1), u8(64, 128), f(1, 1), bf(4, 64))),
+                    (u8(1, 1, 4, 128), (f(4, 1), u8(64, 128), f(1, 1), bf(4, 64))),
+                    (u8(128), (f(4, 1), u8(64, 128), f(1, 1), bf(4, 64)))):
+        with pytest.raises(ValueError):
+            _latent.block_matmul(a, *rest, stream=0)
     for out, sc, w in ((u8(4, 64), f(4, 1), None), (u8(4, 128), f(4, 2), None), (u8(4, 128), f(4, 1), bf(64))):
         with pytest.raises(ValueError):
             _latent.quantize_blocks(bf(4, 128), out, sc, w, stream=0)
