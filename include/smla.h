@@ -1,7 +1,8 @@
 /*
  * smla.h -- C ABI of libsmla: the FP8 lightning indexer, per-token top-k and
  * MLA attention (sparse, dense, expanded; prefill and decode), with the rotary
- * positions and the cache writes and reads around them, for GB300 (sm_103a).
+ * positions, the cache writes and reads and the 8-bit projections around them, for
+ * GB300 (sm_103a).
  *
  * Every entry point takes plain device pointers and sizes, validates them on
  * the host, enqueues its kernels asynchronously on `stream` and returns an

@@ -9,14 +9,22 @@
 // accumulators in turn, so that one block is read while the next is multiplied.
 //
 // Two forms.
-// * wide: rows of a are the MMA's M (128), rows of b its N (256 or 128).  A thread
-//   of the epilogue owns half a tile's row, so a block's scale is one number for
-//   it.  Persistent CTAs, one an SM, walk the tiles in groups of 16 row tiles.
+// * wide: rows of a are the MMA's M, rows of b its N, a pair of CTAs a tile of 256 x
+//   256.  A thread of the epilogue owns half a tile's row, so a block's scale is one
+//   number for it.  Persistent pairs walk the tiles in groups of eight row tiles.
 // * narrow, for calls whose few rows leave the wide form's tiles too few to fill
 //   the GPU: rows of b (the weights, which are what such a call reads) are the M,
-//   rows of a the N (16..128).  The CTAs of a cluster divide the columns k of a
+//   rows of a the N (16, 32 or 64).  The CTAs of a cluster divide the columns k of a
 //   tile and add their sums through distributed shared memory in a fixed order, so
 //   that a result does not depend on the run.
+//
+// Bound and measured.  Wide: an accumulator's way round (MMAs 512 cycles, the word to the
+// epilogue, its loads and multiply-adds, the word back from the other CTA), about 890
+// cycles a block of two accumulators, which are all of TMEM: 4096 x 4096 x 16384 215 us
+// (2550 TFLOP/s; 168-184 without the multiply-adds), 8192^3 378 us (2910); with four
+// blocks a tile and 269 MB to store, 4101 x 32768 x 512 97 us (a fill of as much 72).
+// Narrow: HBM behind 4 us of start and end, 16 x 4096 x 16384 14.5 us (4.6 TB/s),
+// 128 x (16 x 512 x 128) 5.1 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -58,6 +66,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // second CTA: tells the first that a stage has landed), 10-11 a's and b's scales.
 // (The launch's 384 x 168 registers are 128 x (2 x 216 + 72).)
 constexpr int kWideThreads = 384, kWideRegs = 168, kWideSoft = 8, kGroupM = 8;
+static_assert(128 * (2 * 216 + 72) <= kWideThreads * kWideRegs, "the split draws on the launch's registers");
 constexpr int kScaleBlocks = 8;  // blocks whose scales are fetched together
 constexpr int kScaleRow = 132;   // padded: the fetching warps' transposed stores meet all banks
 

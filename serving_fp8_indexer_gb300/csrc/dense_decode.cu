@@ -1,5 +1,5 @@
-// Dense MLA decode over a paged e4m3 latent cache (unit or per-row scales):
-// attention of a few query tokens over every cached key of their sequence.
+// Dense MLA decode over a paged latent cache, e4m3 (unit or per-row scales) or in 4
+// bits: attention of a few query tokens over every cached key of their sequence.
 //
 // Orientation and precision are those of the prefill attention kernel: keys
 // are the MMA M dimension and query rows the N dimension,
@@ -47,8 +47,14 @@
 // runs, then 6 us of start and 5.7 of join), 32 heads 54; 8 x 2 tokens x 128 heads
 // over <= 8192 keys 55.6 us (566 TFLOP/s).
 //
-// Warps: 0-7 softmax and epilogue (thread = one key x NR/2 rows), 8 TMA, 9 QK,
-// 10 PV.
+// Over a 4-bit cache the rows are turned into e4m3 ones on their way into the slots, by
+// warps of their own; everything behind is the same, and so is the result, bit by
+// bit.  The chain of a block grows by the conversion: 2400 cycles of 3500-4200 a block that two
+// slots leave (QK 1070, softmax 1000, PV 750; byte permutes at half rate, and the pipe of shared memory
+// 73 % busy).  16 heads over 4 x <= 120 K keys 57.5 us (2.4 TB/s), 8 x 2 tokens x 128 heads 66 us.
+//
+// Warps: 0-7 softmax and epilogue (thread = one key x NR/2 rows), 8 TMA (4-bit: q and
+// requests ahead), 9 QK, 10 PV; 4-bit: 12-19 (64 rows: 12-15) conversion.
 #include <algorithm>
 #include <cstddef>
 #include <type_traits>
@@ -82,6 +88,9 @@ __host__ __device__ constexpr int conv_groups(int nr) { return nr == 64 ? 1 : 2;
 constexpr int threads_of(Cache c, int nr) { return c == kFourBit ? kThreads + 128 * conv_groups(nr) : kThreads; }
 constexpr int kAhead = 2;  // blocks whose rows are requested from HBM ahead of their conversion
 constexpr int fp4_regs(int nr) { return nr == 64 ? 128 : 96; }
+static_assert(128 * (2 * 112 + 64 + 2 * 96) <= threads_of(kFourBit, 16) * fp4_regs(16) &&
+                  128 * (2 * 168 + 72 + 104) <= threads_of(kFourBit, 64) * fp4_regs(64),
+              "the split draws on the launch's registers");
 
 template <int NR, int QP>
 struct Smem {
@@ -700,245 +709,245 @@ __global__ void __launch_bounds__(threads_of(CACHE, NR), 1)
     }
   } else {
     if constexpr (CACHE == kFourBit) setmaxnreg_dec<(NR == 64 ? 72 : 64)>();
-  if (CACHE == kFourBit && warp == kTmaWarp) {
-    // The first segment's q (the QK warp requests the others), then the rows of
-    // the blocks ahead into L2: the half a block that the converting warps have in
-    // flight covers L2's latency, but not HBM's.
-    Cursor cur = start;
-    Seg g;
-    const bool leader = elect_one();
-    bool more = next_seg(p, cur, g);
-    if (leader && more) load_q(g);
-    __syncwarp();
-    const int box = min(1 << p.seqs.page_shift, kHalf);
-    for (int i = 0; more; more = more && next_seg(p, cur, g)) {
-      for (int j = 0; more && j < g.nb; ++j, ++i) {
-        // (nothing depends on these: conversions that have stopped end them)
-        const unsigned long long t0 = global_timer_ns();
-        while (more && i - *const_cast<volatile int*>(&s.converted) > kAhead) {
-          __nanosleep(200);
-          more = global_timer_ns() - t0 < kWaitLimitNs;
-        }
-        more = __all_sync(0xffffffffu, more);
-        const int key = (g.j0 + j) * kBK + lane * box;
-        if (!more || lane * box >= kBK || key >= seg_keys(g)) continue;
-        const int pid = p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)];
-        const int64_t row = (static_cast<int64_t>(pid) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
-        const int n = min(box, seg_keys(g) - key);
-        if (pid >= 0 && row + n <= p.phys_rows) prefetch_l2(p.pool + row * kFp4Row, n * kFp4Row);
-      }
-    }
-  } else if (CACHE != kFourBit && warp == kTmaWarp) {
-    // ============================================================= key blocks
-    // A block's keys come in parts of a page, up to 64 keys each: five boxes a
-    // part (four 128-byte columns, one of 64), all issued by one lane with the
-    // part's page handed to it (boxes spread over the lanes are issued one
-    // lane at a time, at 200 cycles a box).  Lane k reads part k's page, one
-    // block ahead.
-    const bool leader = elect_one();
-    const int box = min(1 << p.seqs.page_shift, kBK / 2);
-    const int half_parts = (kBK / 2) / box;
-    const auto parts_of = [&](const Seg& g, int j) {  // parts with keys in them
-      return (min(kBK, max(0, seg_keys(g) - (g.j0 + j) * kBK)) + box - 1) / box;
-    };
-    // the first physical row of the lane's part of block j
-    const auto read_row = [&](const Seg& g, int j) -> int {
-      const int key = (g.j0 + j) * kBK + lane * box;
-      if (lane >= parts_of(g, j)) return 0;
-      const int pg = p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)];
-      const int64_t row = (static_cast<int64_t>(pg) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
-      // (rows past the pool's end, where a page hangs over it, arrive as zeros)
-      if (pg < 0 || row + min(box, seg_keys(g) - key) > p.phys_rows) {
-        atomicOr(p.err, kErrPage);
-        if (pg < 0 || row >= p.phys_rows) return 0;
-      }
-      return static_cast<int>(row);
-    };
-    Cursor cur = start;
-    Seg g, gn;
-    int i = 0;
-    bool ok = true, more = next_seg(p, cur, g);
-    // the first segment's q ahead of the keys (behind the first two blocks of
-    // every CTA it took 3 us); the QK warp requests the others
-    if (leader && more) load_q(g);
-    __syncwarp();
-    int row = more ? read_row(g, 0) : 0, row_n = 0;
-    while (ok && more) {
-      more = next_seg(p, cur, gn);
-      for (int j = 0; ok && j < g.nb; ++j) {
-        if (j + 1 < g.nb)
-          row_n = read_row(g, j + 1);
-        else if (more)
-          row_n = read_row(gn, 0);
-        const int slot = i % kNST, parts = parts_of(g, j);
-        const uint32_t bar = smem_u32(&s.bar_full[slot]);
-        const uint32_t dst = smem_u32(s.kv[slot]);
-        const uint32_t par = ((i / kNST) & 1) ^ 1;
-        const auto load = [&](int k, int y) {  // part k's keys
-          const uint32_t d = dst + k * box * 128;
-          tma_load_2d(d, &tk, 0, y, bar);
-          tma_load_2d(d + kChunk, &tk, 128, y, bar);
-          tma_load_2d(d + 2 * kChunk, &tk, 256, y, bar);
-          tma_load_2d(d + 3 * kChunk, &tk, 384, y, bar);
-          tma_load_2d(dst + kRopeOff + k * box * 64, &tr, 512, y, bar);
-        };
-        const int y0 = __shfl_sync(0xffffffffu, row, 0), y1 = __shfl_sync(0xffffffffu, row, 1);
-        if (parts == 2 && half_parts == 1) {
-          // two pages (the usual case), straight from one thread
-          int done = 0;
-          if (leader) {
-            ok = mbar_wait(smem_u32(&s.bar_empty[slot][0]), par, p.err);
-            if (ok) {
-              done = 1;
-              mbar_arrive_expect_tx(bar, 2 * box * kD);
-              load(0, y0);
-              // the second half of the keys once PV has given it back
-              ok = mbar_wait(smem_u32(&s.bar_empty[slot][1]), par, p.err);
-              if (ok) load(1, y1);
-            }
-          }
-          ok = __all_sync(0xffffffffu, ok);
-          i += __any_sync(0xffffffffu, done) ? 1 : 0;
-          row = row_n;
-          continue;
-        }
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_empty[slot][0]), par, p.err))) { ok = false; break; }
-        if (leader) {
-          if (parts > 0)
-            mbar_arrive_expect_tx(bar, parts * box * kD);
-          else
-            mbar_arrive(bar);
-        }
-        for (int k = 0; k < parts; ++k) {
-          if (k == half_parts &&
-              !__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_empty[slot][1]), par, p.err))) {
-            ok = false;
-            break;
-          }
-          const int y = __shfl_sync(0xffffffffu, row, k);
-          if (leader) load(k, y);
-          __syncwarp();
-        }
-        ++i;
-        row = row_n;
-      }
-      g = gn;
-    }
-    // nothing is still landing when the CTA ends
-    for (int sl = 0; sl < kNST; ++sl) {
-      const int loads = (i + kNST - 1 - sl) / kNST;
-      if (loads > 0) mbar_wait(smem_u32(&s.bar_full[sl]), (loads - 1) & 1, p.err);
-    }
-  } else if (warp == kQkWarp) {
-    // ============================================================== q and QK
-    Cursor cur = start;
-    Seg g;
-    const bool leader = elect_one();
-    constexpr uint32_t IDESC = idesc_e4m3_f32(kBK, kQN, 0, 0);
-    const uint64_t ka = make_sdesc(smem_u32(s.kv[0]), 16, 1024, kSwizzle128B);
-    const uint64_t kr = make_sdesc(smem_u32(s.kv[0]) + kRopeOff, 16, 512, kSwizzle64B);
-    const uint64_t qa = make_sdesc(smem_u32(s.q), 16, 1024, kSwizzle128B);
-    const uint64_t qr = make_sdesc(smem_u32(s.q) + 4 * kQChunk, 16, 512, kSwizzle64B);
-    int i = 0, nq = 0;
-    bool ok = true;
-    while (ok && next_seg(p, cur, g)) {
-      // the segment's q rows: every QK before has completed (waited for below)
-      if (leader && nq > 0) load_q(g);
+    if (CACHE == kFourBit && warp == kTmaWarp) {
+      // The first segment's q (the QK warp requests the others), then the rows of
+      // the blocks ahead into L2: the half a block that the converting warps have in
+      // flight covers L2's latency, but not HBM's.
+      Cursor cur = start;
+      Seg g;
+      const bool leader = elect_one();
+      bool more = next_seg(p, cur, g);
+      if (leader && more) load_q(g);
       __syncwarp();
-      ++nq;
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_q), (nq - 1) & 1, p.err));
-      for (int j = 0; ok && j < g.nb; ++j, ++i) {
-        const int slot = i % kNST, buf = i & 1;
-        const bool w = (i < 2 || mbar_wait(smem_u32(&s.bar_s_free[buf]), ((i >> 1) - 1) & 1, p.err)) &&
-                       mbar_wait(smem_u32(&s.bar_full[slot]), (i / kNST) & 1, p.err);
-        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-        tc_fence_after();
-        if (leader) {
-          const uint64_t so = static_cast<uint64_t>(slot * (kSlot >> 4));
-          const uint32_t d = tmem + kS + buf * kQN;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f8f6f4_ss(d, ka + so + static_cast<uint64_t>((c * kChunk + kk * 32) >> 4),
-                            qa + static_cast<uint64_t>((c * kQChunk + kk * 32) >> 4), IDESC, (c | kk) ? 1u : 0u);
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-            mma_f8f6f4_ss(d, kr + so + static_cast<uint64_t>((kk * 32) >> 4), qr + static_cast<uint64_t>((kk * 32) >> 4),
-                          IDESC, 1u);
-          mma_commit(smem_u32(&s.bar_s[buf]));
+      const int box = min(1 << p.seqs.page_shift, kHalf);
+      for (int i = 0; more; more = more && next_seg(p, cur, g)) {
+        for (int j = 0; more && j < g.nb; ++j, ++i) {
+          // (nothing depends on these: conversions that have stopped end them)
+          const unsigned long long t0 = global_timer_ns();
+          while (more && i - *const_cast<volatile int*>(&s.converted) > kAhead) {
+            __nanosleep(200);
+            more = global_timer_ns() - t0 < kWaitLimitNs;
+          }
+          more = __all_sync(0xffffffffu, more);
+          const int key = (g.j0 + j) * kBK + lane * box;
+          if (!more || lane * box >= kBK || key >= seg_keys(g)) continue;
+          const int pid = p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)];
+          const int64_t row = (static_cast<int64_t>(pid) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
+          const int n = min(box, seg_keys(g) - key);
+          if (pid >= 0 && row + n <= p.phys_rows) prefetch_l2(p.pool + row * kFp4Row, n * kFp4Row);
         }
-        __syncwarp();
       }
-      // q's place is free once the segment's last QK has completed
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_s[(i - 1) & 1]), ((i - 1) >> 1) & 1, p.err));
-    }
-    if (leader) mma_commit(smem_u32(&s.bar_drain[0]));
-    __syncwarp();
-    mbar_wait(smem_u32(&s.bar_drain[0]), 0, p.err);
-    if (nq > 0) mbar_wait(smem_u32(&s.bar_qraw), (nq - 1) & 1, p.err);
-  } else if (warp == kPvWarp) {
-    // ==================================================================== PV
-    Cursor cur = start;
-    Seg g;
-    const bool leader = elect_one();
-    constexpr uint32_t IDESC = idesc_e4m3_e5m2_f32(128, kPN, 1, 1);
-    const uint64_t va = make_sdesc(smem_u32(s.kv[0]), kChunk, 1024, kSwizzle128B);
-    // P^T of each slot.  NR = 32 is 96 columns wide: 64 in the rotary chunk, 32 in
-    // the slot's further place.
-    const auto p_desc = [&](int slot) {
-      const uint32_t a = smem_u32(s.kv[slot]) + kRopeOff;
-      return make_sdesc(a, NR == 32 ? smem_u32(s.pmore) + slot * kPRow - a : kPRow, 512, kSwizzle64B);
-    };
-    const uint64_t p0 = p_desc(0), p1 = p_desc(1);
-    const uint64_t pm = make_sdesc(smem_u32(s.pmore), kPRow, 512, kSwizzle64B);
-    int i = 0;
-    bool ok = true;
-    while (ok && next_seg(p, cur, g)) {
-      for (int j = 0; ok && j < g.nb; ++j, ++i) {
-        const int slot = i % kNST;
-        const uint64_t vs = va + static_cast<uint64_t>(slot * (kSlot >> 4)), ps = slot ? p1 : p0;
-        // 32 keys (of half h: the kk-th) against a term at pd; `add` to what is there
-        const auto pv = [&](int h, int kk, uint64_t pd, bool add) {
-#pragma unroll
-          for (int tile = 0; tile < 4; ++tile)
-            mma_f8f6f4_ss(tmem + tile * kPN,
-                          vs + static_cast<uint64_t>((tile * kChunk + (h * kHalf + kk * 32) * 128) >> 4), pd, IDESC,
-                          add ? 1u : 0u);
-        };
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_p[i & 1][h]), (i >> 1) & 1, p.err))) { ok = false; break; }
+    } else if (CACHE != kFourBit && warp == kTmaWarp) {
+      // ============================================================= key blocks
+      // A block's keys come in parts of a page, up to 64 keys each: five boxes a
+      // part (four 128-byte columns, one of 64), all issued by one lane with the
+      // part's page handed to it (boxes spread over the lanes are issued one
+      // lane at a time, at 200 cycles a box).  Lane k reads part k's page, one
+      // block ahead.
+      const bool leader = elect_one();
+      const int box = min(1 << p.seqs.page_shift, kBK / 2);
+      const int half_parts = (kBK / 2) / box;
+      const auto parts_of = [&](const Seg& g, int j) {  // parts with keys in them
+        return (min(kBK, max(0, seg_keys(g) - (g.j0 + j) * kBK)) + box - 1) / box;
+      };
+      // the first physical row of the lane's part of block j
+      const auto read_row = [&](const Seg& g, int j) -> int {
+        const int key = (g.j0 + j) * kBK + lane * box;
+        if (lane >= parts_of(g, j)) return 0;
+        const int pg = p.seqs.page_table[static_cast<int64_t>(g.b) * p.seqs.max_pages + (key >> p.seqs.page_shift)];
+        const int64_t row = (static_cast<int64_t>(pg) << p.seqs.page_shift) | (key & ((1 << p.seqs.page_shift) - 1));
+        // (rows past the pool's end, where a page hangs over it, arrive as zeros)
+        if (pg < 0 || row + min(box, seg_keys(g) - key) > p.phys_rows) {
+          atomicOr(p.err, kErrPage);
+          if (pg < 0 || row >= p.phys_rows) return 0;
+        }
+        return static_cast<int>(row);
+      };
+      Cursor cur = start;
+      Seg g, gn;
+      int i = 0;
+      bool ok = true, more = next_seg(p, cur, g);
+      // the first segment's q ahead of the keys (behind the first two blocks of
+      // every CTA it took 3 us); the QK warp requests the others
+      if (leader && more) load_q(g);
+      __syncwarp();
+      int row = more ? read_row(g, 0) : 0, row_n = 0;
+      while (ok && more) {
+        more = next_seg(p, cur, gn);
+        for (int j = 0; ok && j < g.nb; ++j) {
+          if (j + 1 < g.nb)
+            row_n = read_row(g, j + 1);
+          else if (more)
+            row_n = read_row(gn, 0);
+          const int slot = i % kNST, parts = parts_of(g, j);
+          const uint32_t bar = smem_u32(&s.bar_full[slot]);
+          const uint32_t dst = smem_u32(s.kv[slot]);
+          const uint32_t par = ((i / kNST) & 1) ^ 1;
+          const auto load = [&](int k, int y) {  // part k's keys
+            const uint32_t d = dst + k * box * 128;
+            tma_load_2d(d, &tk, 0, y, bar);
+            tma_load_2d(d + kChunk, &tk, 128, y, bar);
+            tma_load_2d(d + 2 * kChunk, &tk, 256, y, bar);
+            tma_load_2d(d + 3 * kChunk, &tk, 384, y, bar);
+            tma_load_2d(dst + kRopeOff + k * box * 64, &tr, 512, y, bar);
+          };
+          const int y0 = __shfl_sync(0xffffffffu, row, 0), y1 = __shfl_sync(0xffffffffu, row, 1);
+          if (parts == 2 && half_parts == 1) {
+            // two pages (the usual case), straight from one thread
+            int done = 0;
+            if (leader) {
+              ok = mbar_wait(smem_u32(&s.bar_empty[slot][0]), par, p.err);
+              if (ok) {
+                done = 1;
+                mbar_arrive_expect_tx(bar, 2 * box * kD);
+                load(0, y0);
+                // the second half of the keys once PV has given it back
+                ok = mbar_wait(smem_u32(&s.bar_empty[slot][1]), par, p.err);
+                if (ok) load(1, y1);
+              }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            i += __any_sync(0xffffffffu, done) ? 1 : 0;
+            row = row_n;
+            continue;
+          }
+          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_empty[slot][0]), par, p.err))) { ok = false; break; }
+          if (leader) {
+            if (parts > 0)
+              mbar_arrive_expect_tx(bar, parts * box * kD);
+            else
+              mbar_arrive(bar);
+          }
+          for (int k = 0; k < parts; ++k) {
+            if (k == half_parts &&
+                !__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_empty[slot][1]), par, p.err))) {
+              ok = false;
+              break;
+            }
+            const int y = __shfl_sync(0xffffffffu, row, k);
+            if (leader) load(k, y);
+            __syncwarp();
+          }
+          ++i;
+          row = row_n;
+        }
+        g = gn;
+      }
+      // nothing is still landing when the CTA ends
+      for (int sl = 0; sl < kNST; ++sl) {
+        const int loads = (i + kNST - 1 - sl) / kNST;
+        if (loads > 0) mbar_wait(smem_u32(&s.bar_full[sl]), (loads - 1) & 1, p.err);
+      }
+    } else if (warp == kQkWarp) {
+      // ============================================================== q and QK
+      Cursor cur = start;
+      Seg g;
+      const bool leader = elect_one();
+      constexpr uint32_t IDESC = idesc_e4m3_f32(kBK, kQN, 0, 0);
+      const uint64_t ka = make_sdesc(smem_u32(s.kv[0]), 16, 1024, kSwizzle128B);
+      const uint64_t kr = make_sdesc(smem_u32(s.kv[0]) + kRopeOff, 16, 512, kSwizzle64B);
+      const uint64_t qa = make_sdesc(smem_u32(s.q), 16, 1024, kSwizzle128B);
+      const uint64_t qr = make_sdesc(smem_u32(s.q) + 4 * kQChunk, 16, 512, kSwizzle64B);
+      int i = 0, nq = 0;
+      bool ok = true;
+      while (ok && next_seg(p, cur, g)) {
+        // the segment's q rows: every QK before has completed (waited for below)
+        if (leader && nq > 0) load_q(g);
+        __syncwarp();
+        ++nq;
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_q), (nq - 1) & 1, p.err));
+        for (int j = 0; ok && j < g.nb; ++j, ++i) {
+          const int slot = i % kNST, buf = i & 1;
+          const bool w = (i < 2 || mbar_wait(smem_u32(&s.bar_s_free[buf]), ((i >> 1) - 1) & 1, p.err)) &&
+                         mbar_wait(smem_u32(&s.bar_full[slot]), (i / kNST) & 1, p.err);
+          if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
           tc_fence_after();
           if (leader) {
+            const uint64_t so = static_cast<uint64_t>(slot * (kSlot >> 4));
+            const uint32_t d = tmem + kS + buf * kQN;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_f8f6f4_ss(d, ka + so + static_cast<uint64_t>((c * kChunk + kk * 32) >> 4),
+                              qa + static_cast<uint64_t>((c * kQChunk + kk * 32) >> 4), IDESC, (c | kk) ? 1u : 0u);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
-              pv(h, kk, ps + static_cast<uint64_t>(((h * kHalf + kk * 32) * 64) >> 4), j > 0 || (h | kk));
+              mma_f8f6f4_ss(d, kr + so + static_cast<uint64_t>((kk * 32) >> 4), qr + static_cast<uint64_t>((kk * 32) >> 4),
+                            IDESC, 1u);
+            mma_commit(smem_u32(&s.bar_s[buf]));
           }
           __syncwarp();
-          if constexpr (NR == 64) {
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_more[h]), i & 1, p.err))) { ok = false; break; }
+        }
+        // q's place is free once the segment's last QK has completed
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_s[(i - 1) & 1]), ((i - 1) >> 1) & 1, p.err));
+      }
+      if (leader) mma_commit(smem_u32(&s.bar_drain[0]));
+      __syncwarp();
+      mbar_wait(smem_u32(&s.bar_drain[0]), 0, p.err);
+      if (nq > 0) mbar_wait(smem_u32(&s.bar_qraw), (nq - 1) & 1, p.err);
+    } else if (warp == kPvWarp) {
+      // ==================================================================== PV
+      Cursor cur = start;
+      Seg g;
+      const bool leader = elect_one();
+      constexpr uint32_t IDESC = idesc_e4m3_e5m2_f32(128, kPN, 1, 1);
+      const uint64_t va = make_sdesc(smem_u32(s.kv[0]), kChunk, 1024, kSwizzle128B);
+      // P^T of each slot.  NR = 32 is 96 columns wide: 64 in the rotary chunk, 32 in
+      // the slot's further place.
+      const auto p_desc = [&](int slot) {
+        const uint32_t a = smem_u32(s.kv[slot]) + kRopeOff;
+        return make_sdesc(a, NR == 32 ? smem_u32(s.pmore) + slot * kPRow - a : kPRow, 512, kSwizzle64B);
+      };
+      const uint64_t p0 = p_desc(0), p1 = p_desc(1);
+      const uint64_t pm = make_sdesc(smem_u32(s.pmore), kPRow, 512, kSwizzle64B);
+      int i = 0;
+      bool ok = true;
+      while (ok && next_seg(p, cur, g)) {
+        for (int j = 0; ok && j < g.nb; ++j, ++i) {
+          const int slot = i % kNST;
+          const uint64_t vs = va + static_cast<uint64_t>(slot * (kSlot >> 4)), ps = slot ? p1 : p0;
+          // 32 keys (of half h: the kk-th) against a term at pd; `add` to what is there
+          const auto pv = [&](int h, int kk, uint64_t pd, bool add) {
+#pragma unroll
+            for (int tile = 0; tile < 4; ++tile)
+              mma_f8f6f4_ss(tmem + tile * kPN,
+                            vs + static_cast<uint64_t>((tile * kChunk + (h * kHalf + kk * 32) * 128) >> 4), pd, IDESC,
+                            add ? 1u : 0u);
+          };
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_p[i & 1][h]), (i >> 1) & 1, p.err))) { ok = false; break; }
             tc_fence_after();
             if (leader) {
 #pragma unroll
-              for (int term = 0; term < 2; ++term)
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk)
-                  pv(h, kk, pm + static_cast<uint64_t>((term * (kPRow / 2) + kk * 32 * 64) >> 4), true);
+              for (int kk = 0; kk < 2; ++kk)
+                pv(h, kk, ps + static_cast<uint64_t>(((h * kHalf + kk * 32) * 64) >> 4), j > 0 || (h | kk));
             }
+            __syncwarp();
+            if constexpr (NR == 64) {
+              if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.bar_more[h]), i & 1, p.err))) { ok = false; break; }
+              tc_fence_after();
+              if (leader) {
+#pragma unroll
+                for (int term = 0; term < 2; ++term)
+#pragma unroll
+                  for (int kk = 0; kk < 2; ++kk)
+                    pv(h, kk, pm + static_cast<uint64_t>((term * (kPRow / 2) + kk * 32 * 64) >> 4), true);
+              }
+            }
+            if (leader) {
+              mma_commit(smem_u32(&s.bar_empty[slot][h]));
+              if (h == 1) mma_commit(smem_u32(&s.bar_pv[i & 1]));
+            }
+            __syncwarp();
           }
-          if (leader) {
-            mma_commit(smem_u32(&s.bar_empty[slot][h]));
-            if (h == 1) mma_commit(smem_u32(&s.bar_pv[i & 1]));
-          }
-          __syncwarp();
         }
       }
+      if (leader) mma_commit(smem_u32(&s.bar_drain[1]));
+      __syncwarp();
+      mbar_wait(smem_u32(&s.bar_drain[1]), 0, p.err);
     }
-    if (leader) mma_commit(smem_u32(&s.bar_drain[1]));
-    __syncwarp();
-    mbar_wait(smem_u32(&s.bar_drain[1]), 0, p.err);
-  }
   }
   tc_fence_before();
   __syncthreads();

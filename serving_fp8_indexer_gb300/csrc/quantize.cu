@@ -6,6 +6,8 @@
 // blocks are independent: eight lanes hold a block's 128 columns (32 bytes a
 // lane), find its largest magnitude with three shuffles and store 16 bytes a lane.
 // With it a row is read once, kept in registers as bf16 and summed first.
+// Measured: 4096 x 16384 33.4 us (6.1 TB/s, 0.91 of the copy rate; by 8 columns a lane 43.4,
+// two loads a lane in flight 35.6), 16 x 2048 with the norm 2.0 us (a launch).
 #include <algorithm>
 
 #include "quantize.cuh"
