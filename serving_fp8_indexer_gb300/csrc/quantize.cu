@@ -81,15 +81,39 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const Params p, int 
   }
 }
 
+// Rows of a few whole blocks, side by side: a thread's chunks are 256 apart in the
+// run of all rows' chunks.
+template <int kLoads>
+__global__ void __launch_bounds__(kThreads) quantize_flat_kernel(const Params p, uint32_t magic) {
+  const int lane = threadIdx.x & 31;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * (kThreads * kLoads), row0 = base / p.chunks;
+  const int rem = static_cast<int>(base - row0 * p.chunks);  // (a multiple of 8: blocks stay with their eight lanes)
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  Raw raw[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int at = rem + threadIdx.x + kThreads * i, r = __umulhi(at, magic), c = at - r * p.chunks;
+    const uint4* x = reinterpret_cast<const uint4*>(p.x + (row0 + r) * p.x_stride);
+    raw[i] = row0 + r < p.M ? Raw{__ldcs(x + 2 * c), __ldcs(x + 2 * c + 1)} : Raw{none, none};
+  }
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int at = rem + threadIdx.x + kThreads * i, r = __umulhi(at, magic), c = at - r * p.chunks;
+    float v[2][8];
+    unpack(raw[i], v);
+    quantize_chunk(p, row0 + r, c, row0 + r < p.M, v, lane);
+  }
+}
+
 // kRowThreads threads take a row: its chunks stay in registers between the sum
 // and the rounding.
 template <int kRowThreads, int kLoads>
 __global__ void __launch_bounds__(kThreads) quantize_norm_kernel(const Params p) {
-  constexpr int kWarps = kRowThreads / 32;
+  constexpr int kWarps = kRowThreads <= 32 ? 1 : kRowThreads / 32;
   __shared__ float s_sum[kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rt = threadIdx.x % kRowThreads;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / kRowThreads) + threadIdx.x / kRowThreads;
-  const bool live = row < p.M;  // (whole warps; the others only keep the barrier)
+  const bool live = row < p.M;  // (the others keep the barrier and the shuffles)
   const uint4* x = reinterpret_cast<const uint4*>(p.x + (live ? row : 0) * p.x_stride);
   const uint4* weight = reinterpret_cast<const uint4*>(p.w);
   const uint4 none = make_uint4(0, 0, 0, 0);
@@ -109,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) quantize_norm_kernel(const Params p)
     for (int k = 0; k < 8; ++k) ss = fmaf(v[1][k], v[1][k], fmaf(v[0][k], v[0][k], ss));
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  for (int o = (kRowThreads < 32 ? kRowThreads : 32) / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   if constexpr (kWarps > 1) {
     if (lane == 0) s_sum[warp] = ss;
     __syncthreads();
@@ -117,12 +141,11 @@ __global__ void __launch_bounds__(kThreads) quantize_norm_kernel(const Params p)
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) ss += s_sum[warp / kWarps * kWarps + w];
   }
-  if (!live) return;
   const float rstd = 1.f / sqrtf(ss / static_cast<float>(p.K) + p.eps);
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const int c = rt + kRowThreads * i;
-    const bool in = c < p.chunks;
+    const bool in = live && c < p.chunks;
     if (i > 0) w0 = in ? Raw{weight[2 * c], weight[2 * c + 1]} : Raw{none, none};
     float v[2][8], w[2][8];
     unpack(raw[i], v);
@@ -150,23 +173,53 @@ smla_status_t launch_quantize(const QuantizeArgs& a, cudaStream_t stream) {
   p.eps = a.norm_eps;
   p.out = a.out;
   p.scales = a.scales;
+  const auto grid = [](int64_t n, int64_t per) { return static_cast<unsigned>((n + per - 1) / per); };
   if (p.w) {
-    if (a.K <= 1024)
-      quantize_norm_kernel<32, 2><<<(a.M + 7) / 8, kThreads, 0, stream>>>(p);
-    else if (a.K <= 4096)
-      quantize_norm_kernel<256, 1><<<a.M, kThreads, 0, stream>>>(p);
-    else
+    // where rows are many, as few threads a row as hold it in one or two loads (30 000 x
+    // 2048 45.0 us; 50.5 in four loads, 70 by a CTA a row); where they are few, a CTA
+    if (a.K > 1024 && a.M < 8 * device_sm_count()) {
+      if (a.K <= 4096)
+        quantize_norm_kernel<256, 1><<<a.M, kThreads, 0, stream>>>(p);
+      else
+        quantize_norm_kernel<256, 4><<<a.M, kThreads, 0, stream>>>(p);
+    } else if (a.K <= 128) {
+      quantize_norm_kernel<8, 1><<<grid(a.M, 32), kThreads, 0, stream>>>(p);
+    } else if (a.K <= 256) {
+      quantize_norm_kernel<16, 1><<<grid(a.M, 16), kThreads, 0, stream>>>(p);
+    } else if (a.K <= 512) {
+      quantize_norm_kernel<32, 1><<<grid(a.M, 8), kThreads, 0, stream>>>(p);
+    } else if (a.K <= 1024) {
+      quantize_norm_kernel<32, 2><<<grid(a.M, 8), kThreads, 0, stream>>>(p);
+    } else if (a.K <= 2048) {
+      quantize_norm_kernel<64, 2><<<grid(a.M, 4), kThreads, 0, stream>>>(p);
+    } else if (a.K <= 4096) {
+      quantize_norm_kernel<128, 2><<<grid(a.M, 2), kThreads, 0, stream>>>(p);
+    } else if (a.K <= 8192) {
+      quantize_norm_kernel<256, 2><<<a.M, kThreads, 0, stream>>>(p);
+    } else {
       quantize_norm_kernel<256, 4><<<a.M, kThreads, 0, stream>>>(p);
+    }
+  } else if (a.K <= 512 && a.K % kBlock == 0) {
+    const uint32_t magic = static_cast<uint32_t>(((uint64_t(1) << 32) + p.chunks - 1) / p.chunks);
+    const int64_t chunks = static_cast<int64_t>(a.M) * p.chunks;
+    if (chunks >= (1 << 18))
+      quantize_flat_kernel<4><<<grid(chunks, kThreads * 4), kThreads, 0, stream>>>(p, magic);
+    else
+      quantize_flat_kernel<1><<<grid(chunks, kThreads), kThreads, 0, stream>>>(p, magic);
   } else {
     const auto go = [&](auto kernel, int loads) {
       const int per_row = (p.chunks + 32 * loads - 1) / (32 * loads);
       const int64_t units = static_cast<int64_t>(a.M) * per_row;
-      kernel<<<static_cast<unsigned>((units + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, stream>>>(p, per_row, units);
+      kernel<<<grid(units, kThreads / 32), kThreads, 0, stream>>>(p, per_row, units);
     };
-    if (a.K >= 1024 && static_cast<int64_t>(a.M) * a.K >= (1 << 22))
-      go(quantize_kernel<4>, 4);
-    else
+    // four loads a lane, unless their 2048 columns leave half a warp's work or more
+    // idle at a row's end (60 000 x 1024 33.5 us in two, 44.0 in four)
+    if (a.K < 1024 || static_cast<int64_t>(a.M) * a.K < (1 << 22))
       go(quantize_kernel<1>, 1);
+    else if ((a.K - 1) % 2048 < 1024)
+      go(quantize_kernel<2>, 2);
+    else
+      go(quantize_kernel<4>, 4);
   }
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SMLA_OK : fail_cuda(e, "quantize launch");

@@ -225,7 +225,9 @@ def _quantized(x, weight=None, eps=1e-6):
     return out, s
 
 
-@pytest.mark.parametrize("M,K", [(1, 16), (3, 128), (5, 144), (16, 2048), (257, 1552), (1000, 576), (4100, 1168), (2, 16384)])
+@pytest.mark.parametrize("M,K", [(1, 16), (3, 128), (5, 144), (16, 2048), (257, 1552), (1000, 576), (4100, 1168), (2, 16384),
+                                 (1, 128), (2047, 128), (70001, 128), (3001, 256), (11003, 384), (9001, 512), (4097, 1024),
+                                 (3000, 4112), (2500, 2048)])
 def test_bytes_and_scales_are_the_quotients(M, K):
     g = _gen(M + K)
     wide = torch.randn((M, K + 64), generator=g, device="cuda").bfloat16() * torch.exp(2 * torch.randn((M, 1), generator=g, device="cuda")).bfloat16()
@@ -252,7 +254,9 @@ def test_zeros_infinities_nan_and_tiny_blocks():
     assert int(nan.sum()) == 1 and float(s[0, 0]) == 1.0 and int(out[2, 3]) == 0x7E and int(out[2, 130]) == 0xFE
 
 
-@pytest.mark.parametrize("M,K", [(1, 16), (7, 128), (9, 1024), (16, 2048), (3, 4096), (130, 1040), (5, 16384), (2, 4112)])
+@pytest.mark.parametrize("M,K", [(1, 16), (7, 128), (9, 1024), (16, 2048), (3, 4096), (130, 1040), (5, 16384), (2, 4112),
+                                 (1, 48), (33, 96), (1001, 208), (17, 256), (1003, 512), (2001, 640), (1301, 1552), (1300, 2048),
+                                 (1501, 4096), (1219, 4112), (1217, 8192), (1218, 16384)])
 def test_normalised_rows(M, K):
     g = _gen(M * K)
     wide = (torch.randn((M, K + 8), generator=g, device="cuda") * torch.exp(3 * torch.randn((M, 1), generator=g, device="cuda"))).bfloat16()
