@@ -121,9 +121,8 @@ class Rope:
         self.inv_freq, self.offset, self.layout, self.amplitude = inv_freq, int(offset), int(layout), float(amplitude)
 
     def as_c(self, dev: Optional[int] = None) -> RopeT:
-        dev = _device() if dev is None else dev
-        return RopeT(_flat(self.inv_freq, "inv_freq", torch.float64, dev, 1), self.offset, 2 * self.inv_freq.shape[0],
-                     self.layout, self.amplitude)
+        dev, f = _device() if dev is None else dev, self.inv_freq
+        return RopeT(_flat(f, "inv_freq", torch.float64, dev, 1), self.offset, 2 * f.shape[0], self.layout, self.amplitude)
 
 
 def rope_frequencies(dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
@@ -278,12 +277,18 @@ def dense_decode(q: torch.Tensor, latent: torch.Tensor, scales: Optional[torch.T
 FP4_ROW = 320  # bytes of a 4-bit cache row
 
 
-def _fp4_pool(pool, dev: int):
-    """(pointer, rows) of a 4-bit cache."""
-    ptr = _flat(pool, "pool", torch.uint8, dev, 2)
+# The calls below make all their checks in one condition, with the cheapest queries
+# of a tensor; which check failed is found out behind it.  (A 16-row quantisation
+# takes 2 us on the GPU, and a helper call for each tensor 4 us on the host.)
+def _refuse_fp4_pool(pool, dev: int):
+    _flat(pool, "pool", _U8, dev, 2)
     if pool.shape[1] != FP4_ROW:
         raise ValueError(f"a 4-bit pool must be [phys_rows, {FP4_ROW}], got {tuple(pool.shape)}")
-    return ptr, pool.shape[0]
+
+
+def _on_device(t, dtype, dev: int) -> bool:
+    """A contiguous tensor of this type on the device."""
+    return t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
 
 
 def cache_append_fp4(x: torch.Tensor, seqs: Seqs, pool: torch.Tensor, rope: Optional[Rope] = None,
@@ -292,19 +297,24 @@ def cache_append_fp4(x: torch.Tensor, seqs: Seqs, pool: torch.Tensor, rope: Opti
     """cache_append into a 4-bit latent cache: x bf16 [T, 576], pool uint8
     [phys_rows, 320] (codes, block shifts and the row's scale; include/smla.h)."""
     lib, dev = _lib._lib or _lib.load(), _device()
-    xp, (T, D), xs = _rows(x, "x", (torch.bfloat16,), dev, 2)
-    rp, rs = None, D
+    T, shape, p_shape, n = seqs.T, x.shape, pool.shape, 0
+    if not (shape == (T, 576) and len(p_shape) == 2 and p_shape[1] == FP4_ROW and x.dtype is _BF16 and
+            x.get_device() == dev and x.stride(1) == 1 and _on_device(pool, _U8, dev)):
+        _rows(x, "x", (_BF16,), dev, 2)
+        _refuse_fp4_pool(pool, dev)
+        raise ValueError(f"x {tuple(shape)} must be [T={T}, 576]")
+    w = r = None
+    r_stride = 576
+    if norm_weight is not None:
+        w, n = _flat(norm_weight, "norm_weight", _BF16, dev, 1), norm_weight.shape[0]
     if rows_out is not None:
-        rp, rows_shape, rs = _rows(rows_out, "rows_out", (torch.bfloat16,), dev, 2)
-        rs = rs[0]
-        if rows_shape != x.shape:
+        r, r_shape, r_stride = _rows(rows_out, "rows_out", (_BF16,), dev, 2)
+        r_stride = r_stride[0]
+        if r_shape != shape:
             raise ValueError("rows_out must have x's shape")
-    pp, phys_rows = _fp4_pool(pool, dev)
-    if T != seqs.T or D != 576:
-        raise ValueError(f"x {tuple(x.shape)} must be [T={seqs.T}, 576]")
-    st = lib.smla_cache_append_fp4(xp, xs[0], _seqs(seqs, dev), _flat(norm_weight, "norm_weight", torch.bfloat16, dev, 1),
-                                   0 if norm_weight is None else norm_weight.shape[0], norm_eps,
-                                   rope.as_c(dev) if rope is not None else RopeT(), pp, phys_rows, rp, rs, _on(stream, dev))
+    st = lib.smla_cache_append_fp4(x.data_ptr(), x.stride(0) if T > 1 else 576, _seqs(seqs, dev), w, n, norm_eps,
+                                   rope.as_c(dev) if rope is not None else RopeT(), pool.data_ptr(), p_shape[0], r,
+                                   r_stride, _on(stream, dev))
     if st:
         _check(lib, st)
 
@@ -316,13 +326,18 @@ def cache_gather_fp4(pool: torch.Tensor, seqs: Seqs, rows: torch.Tensor, row_sca
     values exactly and serve as a pool of the calls over e4m3 caches
     (scale_block_size 576)."""
     lib, dev = _lib._lib or _lib.load(), _device()
-    dtype = torch.bfloat16 if row_scales is None else torch.uint8
-    rp, (T, D), rs = _rows(rows, "rows", (dtype,), dev, 2)
-    pp, phys_rows = _fp4_pool(pool, dev)
-    if T != seqs.T or D != 576 or (row_scales is not None and row_scales.shape != (T, 1)):
-        raise ValueError(f"rows {tuple(rows.shape)} must be [T={seqs.T}, 576], row_scales [T, 1]")
-    st = lib.smla_cache_gather_fp4(pp, phys_rows, _seqs(seqs, dev), rp, SMLA_BF16 if row_scales is None else SMLA_E4M3, rs[0],
-                                   _flat(row_scales, "row_scales", torch.float32, dev, 2), _on(stream, dev))
+    T, shape, p_shape = seqs.T, rows.shape, pool.shape
+    bf16 = row_scales is None
+    if not (shape == (T, 576) and len(p_shape) == 2 and p_shape[1] == FP4_ROW and rows.dtype is (_BF16 if bf16 else _U8) and
+            rows.get_device() == dev and rows.stride(1) == 1 and _on_device(pool, _U8, dev) and
+            (bf16 or row_scales.shape == (T, 1) and _on_device(row_scales, _F32, dev))):
+        _rows(rows, "rows", (_BF16 if bf16 else _U8,), dev, 2)
+        _refuse_fp4_pool(pool, dev)
+        _flat(row_scales, "row_scales", _F32, dev, 2)
+        raise ValueError(f"rows {tuple(shape)} must be [T={T}, 576], row_scales [T, 1]")
+    st = lib.smla_cache_gather_fp4(pool.data_ptr(), p_shape[0], _seqs(seqs, dev), rows.data_ptr(),
+                                   SMLA_BF16 if bf16 else SMLA_E4M3, rows.stride(0) if T > 1 else 576,
+                                   None if bf16 else row_scales.data_ptr(), _on(stream, dev))
     if st:
         _check(lib, st)
     return rows
@@ -334,17 +349,23 @@ def dense_decode_fp4(q: torch.Tensor, pool: torch.Tensor, seqs: Seqs, max_kv_len
     """dense_decode over a 4-bit latent cache, pool uint8 [phys_rows, 320];
     workspace of dense_decode_workspace_size() bytes."""
     lib, dev = _lib._lib or _lib.load(), _device()
-    bf16 = q.dtype is torch.bfloat16
-    qp = _flat(q, "q", torch.bfloat16 if bf16 else torch.uint8, dev, 3)
-    pp, phys_rows = _fp4_pool(pool, dev)
-    T, H, D = q.shape
-    if T != seqs.T or D != 576 or out.shape[:2] != (T, H) or (attn_sink is not None and attn_sink.shape != (H,)):
-        raise ValueError(f"q must be [T={seqs.T}, H, 576], out [T, H, 512], attn_sink [H]")
-    st = lib.smla_dense_decode_fp4(qp, SMLA_BF16 if bf16 else SMLA_E4M3, pp, phys_rows, _seqs(seqs, dev), max_kv_len, H,
-                                   out.shape[2], softmax_scale, _flat(attn_sink, "attn_sink", torch.float32, dev, 1),
-                                   _flat(out, "out", torch.bfloat16, dev, 3),
-                                   _flat(workspace, "workspace", torch.uint8, dev, 1),
-                                   0 if workspace is None else workspace.numel(), _on(stream, dev))
+    T, shape, p_shape, o_shape = seqs.T, q.shape, pool.shape, out.shape
+    bf16 = q.dtype is _BF16
+    if not (len(shape) == 3 and shape[0] == T and shape[2] == 576 and len(p_shape) == 2 and p_shape[1] == FP4_ROW and
+            len(o_shape) == 3 and o_shape[:2] == shape[:2] and _on_device(q, _BF16 if bf16 else _U8, dev) and
+            _on_device(pool, _U8, dev) and _on_device(out, _BF16, dev)):
+        _flat(q, "q", _BF16 if bf16 else _U8, dev, 3)
+        _refuse_fp4_pool(pool, dev)
+        _flat(out, "out", _BF16, dev, 3)
+        raise ValueError(f"q must be [T={T}, H, 576], out [T, H, 512]")
+    H = shape[1]
+    if attn_sink is not None and attn_sink.shape != (H,):
+        raise ValueError(f"attn_sink must be [H={H}]")
+    st = lib.smla_dense_decode_fp4(q.data_ptr(), SMLA_BF16 if bf16 else SMLA_E4M3, pool.data_ptr(), p_shape[0],
+                                   _seqs(seqs, dev), max_kv_len, H, o_shape[2], softmax_scale,
+                                   _flat(attn_sink, "attn_sink", _F32, dev, 1), out.data_ptr(),
+                                   _flat(workspace, "workspace", _U8, dev, 1), 0 if workspace is None else workspace.numel(),
+                                   _on(stream, dev))
     if st:
         _check(lib, st)
     return out
@@ -356,12 +377,18 @@ def quantize_blocks(x: torch.Tensor, out: torch.Tensor, scales: torch.Tensor, no
     [M, K] (rows may be strided): a scale for each 128 columns, after an RMS norm
     over the row when its weight bf16 [K] is given."""
     lib, dev = _lib._lib or _lib.load(), _device()
-    xp, shape, xs = _rows(x, "x", (_BF16,), dev, 2)
-    M, K = shape
-    if out.shape != shape or scales.shape != (M, (K + 127) >> 7) or (norm_weight is not None and norm_weight.shape != (K,)):
+    shape = x.shape
+    M, K = shape if len(shape) == 2 else (0, 0)
+    if not (len(shape) == 2 and out.shape == shape and scales.shape == (M, (K + 127) >> 7) and x.dtype is _BF16 and
+            x.get_device() == dev and (x.stride(1) == 1 or K <= 1) and _on_device(out, _U8, dev) and
+            _on_device(scales, _F32, dev) and (norm_weight is None or norm_weight.shape == (K,))):
+        _rows(x, "x", (_BF16,), dev, 2)
+        _flat(out, "out", _U8, dev, 2)
+        _flat(scales, "scales", _F32, dev, 2)
         raise ValueError(f"out must be [M={M}, K={K}], scales [M, {-(-K // 128)}], norm_weight [K]")
-    st = lib.smla_quantize_blocks(xp, xs[0], M, K, _flat(norm_weight, "norm_weight", _BF16, dev, 1), norm_eps,
-                                  _flat(out, "out", _U8, dev, 2), _flat(scales, "scales", _F32, dev, 2), _on(stream, dev))
+    st = lib.smla_quantize_blocks(x.data_ptr(), x.stride(0) if M > 1 else K, M, K,
+                                  _flat(norm_weight, "norm_weight", _BF16, dev, 1), norm_eps, out.data_ptr(),
+                                  scales.data_ptr(), _on(stream, dev))
     if st:
         _check(lib, st)
 
