@@ -11,18 +11,20 @@
 // Two forms.
 // * wide: rows of a are the MMA's M, rows of b its N, a pair of CTAs a tile of 256 x
 //   256.  A thread of the epilogue owns half a tile's row, so a block's scale is one
-//   number for it.  Persistent pairs walk the tiles in groups of eight row tiles.
+//   number for it.  Persistent pairs walk the tiles in groups of eight row tiles.  A
+//   last wave that would leave half of the pairs idle goes as halves of 256 x 128, with
+//   four accumulators (4096 x 4096 x 16384 218 -> 202 us, 512 rows of it 60 -> 42.7).
 // * narrow, for calls whose few rows leave the wide form's tiles too few to fill
 //   the GPU: rows of b (the weights, which are what such a call reads) are the M,
 //   rows of a the N (16, 32 or 64).  The CTAs of a cluster divide the columns k of a
 //   tile and add their sums through distributed shared memory in a fixed order, so
 //   that a result does not depend on the run.
 //
-// Bound and measured.  Wide: an accumulator's way round (MMAs 512 cycles, the word to the
-// epilogue, its loads and multiply-adds, the word back from the other CTA), about 890
-// cycles a block of two accumulators, which are all of TMEM: 4096 x 4096 x 16384 215 us
-// (2550 TFLOP/s; 168-184 without the multiply-adds), 8192^3 378 us (2910); with four
-// blocks a tile and 269 MB to store, 4101 x 32768 x 512 97 us (a fill of as much 72).
+// Bound and measured.  Wide: the epilogue's warps, whose waits, TMEM loads and
+// multiply-adds follow one another, 870 cycles a block of 256 x 256 (MMAs 512): 4096 x
+// 4096 x 16384 202 us (2720 TFLOP/s), 8192^3 378 us (2910); with four blocks a tile and 269 MB to store, 4101 x 32768 x 512 97 us (a fill of as much 72).
+// (Slower or the same: one CTA's MMAs with b by multicast 216 us for 217; 16 epilogue
+// warps of 64 columns 228; each load one piece ahead, over the end of a block, 237.)
 // Narrow: HBM behind 4 us of start and end, 16 x 4096 x 16384 14.5 us (4.6 TB/s),
 // 128 x (16 x 512 x 128) 5.1 us.
 #include <algorithm>
@@ -48,6 +50,7 @@ struct Params {
   int G, M, N;
   int m_tiles, n_tiles;
   int64_t tiles;
+  unsigned whole;  // (wide: tiles from this one on are halves)
   unsigned* err;
 };
 
@@ -73,15 +76,19 @@ constexpr int kScaleRow = 132;   // padded: the fetching warps' transposed store
 constexpr int BN = 256;
 
 struct WideSmem {
-  static constexpr int kStages = 4;  // a stage's way round takes 1.5 us: what is in flight sets the rate
-  // places for 64 bytes of an epilogue warp's 32 rows on their way out
-  static constexpr int kPlaces = 4;
+  // a stage's way round takes 1.5 us: what is in flight sets a half tile's rate (512 x
+  // 4096 x 16384: 50 us with four, 42.7)
+  static constexpr int kStages = 5;
+  // places for 64 bytes of an epilogue warp's 32 rows on their way out (4101 x 32768 x
+  // 512 with one, and a stage more: 106 us for 101)
+  static constexpr int kPlaces = 2;
   uint8_t a[kStages][128 * kBK];
   uint8_t b[kStages][BN / 2 * kBK];
   uint8_t out[kWideSoft][kPlaces][32 * 64];
   float as[2][kScaleBlocks][kScaleRow], bs[2][2][kScaleBlocks];
   unsigned long long full[kStages], empty[kStages];
-  unsigned long long sum_full[2], sum_empty[2], scale_full[2], scale_empty[2], drain;
+  // of the two accumulators of BN columns, then of the four of BN / 2
+  unsigned long long sum_full[6], sum_empty[6], scale_full[2], scale_empty[2], drain;
   uint32_t tmem_base;
 };
 
@@ -141,9 +148,9 @@ __device__ __forceinline__ Tile tile_at(const Params& p, unsigned t) {
 
 __global__ void __launch_bounds__(kWideThreads, 1)
     wide_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-                const __grid_constant__ CUtensorMap to, const Params p) {
+                const __grid_constant__ CUtensorMap tb_half, const __grid_constant__ CUtensorMap to, const Params p) {
   using S = WideSmem;
-  constexpr int kStages = S::kStages, kCols = BN / 2;  // columns of a thread
+  constexpr int kStages = S::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (smem_u32(smem_raw) & 1023u) {  // (the same for every CTA)
     if (threadIdx.x == 0) atomicOr(p.err, kErrShape);
@@ -153,14 +160,29 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(blockIdx.x & 1), m_of = rank * 128;  // this CTA's rows of a tile
   const unsigned tiles = static_cast<unsigned>(p.tiles), pairs = gridDim.x >> 1;
+  // The pair's tiles: role(columns, tile) of each whole one, then of the half that may
+  // follow.  (The half's code is its own: with its size a variable, the whole tiles'
+  // loop took 5 to 8 % longer.)
+  const auto walk = [&](auto&& role) {
+    unsigned t = blockIdx.x >> 1;
+    bool ok = true;
+    for (; ok && t < p.whole; t += pairs) ok = role(std::integral_constant<int, BN>{}, tile_at(p, t));
+    if (!ok || t >= tiles) return;
+    const unsigned in = t - p.whole;
+    Tile tile = tile_at(p, p.whole + (in >> 1));
+    tile.n0 += static_cast<int>(in & 1) * (BN / 2);
+    role(std::integral_constant<int, BN / 2>{}, tile);
+  };
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&s.full[i]), 2 - rank);  // the first CTA's counts the second's landing too
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 6; ++i) {
       mbar_init(smem_u32(&s.sum_full[i]), 1);
       mbar_init(smem_u32(&s.sum_empty[i]), 2 * kWideSoft);  // (the first CTA's counts)
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s.scale_full[i]), 2);
       mbar_init(smem_u32(&s.scale_empty[i]), kWideSoft);
     }
@@ -172,7 +194,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   }
   if (threadIdx.x == 8 * 32) {
     tma_prefetch_desc(&ta);
-    tma_prefetch_desc(&tb);
+    tma_prefetch_desc(p.whole ? &tb : &tb_half);
     tma_prefetch_desc(&to);
   }
   tc_fence_before();
@@ -186,26 +208,29 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     setmaxnreg_inc<216>();
     const int half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t from = tmem + lanes + half * kCols;
     const uint32_t full0 = smem_u32(s.sum_full), empty0 = cluster_addr(smem_u32(s.sum_empty), 0);
     int buf = 0, q = 0;            // accumulator, group of scales
     uint32_t phase = 0, q_phase = 0;
-    bool ok = true;
-    for (unsigned t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
-      const Tile tile = tile_at(p, t);
+    walk([&](auto c, const Tile& tile) {
+      constexpr int cols = decltype(c)::value;
+      constexpr int kCols = cols / 2, kSums = 2 * BN / cols;  // columns of a thread, accumulators
+      constexpr int kFirst = cols == BN ? 0 : 2;
+      if (cols != BN) buf = phase = 0;
+      const uint32_t from = tmem + lanes + half * kCols;
+      bool ok = true;
       float acc[kCols];
 #pragma unroll
       for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
       for (int kb0 = 0; ok && kb0 < p.kb; kb0 += kScaleBlocks) {
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.scale_full[q]), q_phase, p.err));
         const float* sa = &s.as[q][0][(warp & 3) * 32 + lane];
-        const float* sb = s.bs[q][half];
+        const float* sb = s.bs[q][cols == BN ? half : 0];
 #pragma unroll 1
         for (int left = min(kScaleBlocks, p.kb - kb0); ok && left > 0; --left, sa += kScaleRow, ++sb) {
           const float scale = *sa * *sb;
-          ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * buf, phase, p.err));
+          ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * (kFirst + buf), phase, p.err));
           tc_fence_after();
-          const uint32_t a = from + buf * BN;
+          const uint32_t a = from + buf * cols;
           // 32 columns at a time, two loads in flight.  (Paired multiply-adds had a move
           // beside each, for their register pairs: 252 us for 213 at 4096^2 x 16384.)
           const auto add = [&](const uint32_t (&v)[32], int c) {
@@ -217,19 +242,21 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           tmem_ld32(a + 32, v1);
           tmem_wait_ld_regs(v0);
           tmem_wait_ld_regs(v1);
-          add(v0, 0);
-          tmem_ld32(a + 64, v0);
-          add(v1, 32);
-          tmem_ld32(a + 96, v1);
-          tmem_wait_ld_regs(v0);
-          tmem_wait_ld_regs(v1);
+          if constexpr (cols == BN) {
+            add(v0, 0);
+            tmem_ld32(a + 64, v0);
+            add(v1, 32);
+            tmem_ld32(a + 96, v1);
+            tmem_wait_ld_regs(v0);
+            tmem_wait_ld_regs(v1);
+          }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) cluster_arrive(empty0 + 8 * buf);
-          add(v0, 64);
-          add(v1, 96);
-          buf ^= 1;
-          phase ^= buf ^ 1;
+          if (lane == 0) cluster_arrive(empty0 + 8 * (kFirst + buf));
+          add(v0, kCols - 64);
+          add(v1, kCols - 32);
+          buf = (buf + 1) % kSums;
+          phase ^= buf == 0;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.scale_empty[q]));
@@ -277,7 +304,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             });
         }
       }
-    }
+      return ok;
+    });
     if (lane == 0) tma_store_wait_all();
     __syncwarp();
   } else {
@@ -287,25 +315,25 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (elect_one()) {
         int st = 0;
         uint32_t phase = 0, used = 0;
-        bool ok = true;
-        for (unsigned t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
-          const Tile tile = tile_at(p, t);
-          const int m = tile.m0 + m_of, n = tile.n0 + rank * (BN / 2);
+        walk([&](auto c, const Tile& tile) {
+          constexpr int cols = decltype(c)::value;
+          const CUtensorMap* const map = cols == BN ? &tb : &tb_half;
+          const int m = tile.m0 + m_of, n = tile.n0 + rank * (cols / 2);
           const int y = p.a_flip ? tile.g : m, z = p.a_flip ? m : tile.g;
           for (int kb = 0; kb < p.kb; ++kb) {
-            ok = mbar_wait(smem_u32(&s.empty[st]), phase ^ 1, p.err);
-            if (!ok) break;
+            if (!mbar_wait(smem_u32(&s.empty[st]), phase ^ 1, p.err)) return false;
             const uint32_t bar = smem_u32(&s.full[st]);
-            mbar_arrive_expect_tx(bar, (128 + BN / 2) * kBK);
+            mbar_arrive_expect_tx(bar, (128 + cols / 2) * kBK);
             tma_load_3d(smem_u32(s.a[st]), &ta, kb * kBK, y, z, bar);
-            tma_load_3d(smem_u32(s.b[st]), &tb, kb * kBK, n, tile.g, bar);
+            tma_load_3d(smem_u32(s.b[st]), map, kb * kBK, n, tile.g, bar);
             used |= 1u << st;
             if (++st == kStages) {
               st = 0;
               phase ^= 1;
             }
           }
-        }
+          return true;
+        });
         // nothing is still landing when the CTA ends: the last load of each stage
         for (int k = 0; k < kStages; ++k)
           if (used >> k & 1) mbar_wait(smem_u32(&s.full[k]), k < st ? phase : phase ^ 1, p.err);
@@ -314,7 +342,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     } else if (warp == 9) {
       // =================================================================== MMAs
       if (elect_one()) {
-        constexpr uint32_t IDESC = idesc_e4m3_f32(256, BN, 0, 0);
         const uint64_t da = make_sdesc(smem_u32(s.a[0]), 16, 1024, kSwizzle128B);
         const uint64_t db = make_sdesc(smem_u32(s.b[0]), 16, 1024, kSwizzle128B);
         // (One thread, whose every instruction the MMAs wait for: nothing is computed
@@ -323,34 +350,44 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const uint32_t sum_full0 = smem_u32(s.sum_full), sum_empty0 = smem_u32(s.sum_empty);
         int st = 0, buf = 0;
         uint32_t phase = 0, buf_phase = 1;
-        bool ok = true;
-        for (unsigned t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
+        walk([&](auto c, const Tile&) {
+          constexpr int cols = decltype(c)::value;
+          constexpr uint32_t IDESC = idesc_e4m3_f32(256, cols, 0, 0);
+          constexpr int kSums = 2 * BN / cols, kFirst = cols == BN ? 0 : 2;
+          if (cols != BN) {
+            for (int i = 0; rank == 0 && i < 2; ++i) {  // the wider accumulators have been read
+              if (!mbar_wait(sum_empty0 + 8 * buf, buf_phase, p.err)) return false;
+              buf ^= 1;
+              buf_phase ^= buf ^ 1;
+            }
+            buf = 0;
+            buf_phase = 1;
+          }
           for (int kb = 0; kb < p.kb; ++kb) {
-            ok = mbar_wait(full0 + 8 * st, phase, p.err);
-            if (!ok) break;
+            if (!mbar_wait(full0 + 8 * st, phase, p.err)) return false;
             if (rank == 1) {
               cluster_arrive(peer0 + 8 * st);
             } else {
-              ok = mbar_wait(sum_empty0 + 8 * buf, buf_phase, p.err);
-              if (!ok) break;
+              if (!mbar_wait(sum_empty0 + 8 * (kFirst + buf), buf_phase, p.err)) return false;
               tc_fence_after();
               const uint64_t a = da + static_cast<uint64_t>(st * (128 * kBK >> 4));
               const uint64_t b = db + static_cast<uint64_t>(st * (BN / 2 * kBK >> 4));
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                pair_mma_f8f6f4(tmem + buf * BN, a + static_cast<uint64_t>(2 * k), b + static_cast<uint64_t>(2 * k), IDESC,
+                pair_mma_f8f6f4(tmem + buf * cols, a + static_cast<uint64_t>(2 * k), b + static_cast<uint64_t>(2 * k), IDESC,
                                 k ? 1u : 0u);
-              pair_commit(sum_full0 + 8 * buf);
+              pair_commit(sum_full0 + 8 * (kFirst + buf));
               pair_commit(empty0 + 8 * st);
-              buf ^= 1;
-              buf_phase ^= buf ^ 1;
+              buf = (buf + 1) % kSums;
+              buf_phase ^= buf == 0;
             }
             if (++st == kStages) {
               st = 0;
               phase ^= 1;
             }
           }
-        }
+          return true;
+        });
         if (rank == 0) {
           pair_commit(smem_u32(&s.drain));
           mbar_wait(smem_u32(&s.drain), 0, p.err);
@@ -365,9 +402,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // x 16384.)
       const int rows0 = (warp - 10) * 64 + (lane >> 3), b = lane & 7;
       int q = 0;
-      bool ok = true;
-      for (unsigned t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
-        const Tile tile = tile_at(p, t);
+      const auto tile_scales = [&](const Tile& tile) {
         const float* as = p.as + tile.g * p.as_gs;
         const float* bs = p.bs + static_cast<int64_t>(tile.g) * p.nb * p.kb;
         for (int kb0 = 0; kb0 < p.kb; kb0 += kScaleBlocks, ++q) {
@@ -376,16 +411,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
           for (int k = 0; k < 16; ++k) v[k] = as[min(tile.m0 + m_of + rows0 + 4 * k, p.M - 1) * p.as_ms + kb];
           const int n = lane >> 3;  // half of the tile's columns
-          if (n < 2) w = bs[static_cast<int64_t>(min((tile.n0 + n * kCols) / 128, p.nb - 1)) * p.kb + kb];
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.scale_empty[q & 1]), ((q >> 1) & 1) ^ 1, p.err));
-          if (!ok) break;
+          if (n < 2) w = bs[static_cast<int64_t>(min((tile.n0 + n * 128) / 128, p.nb - 1)) * p.kb + kb];
+          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s.scale_empty[q & 1]), ((q >> 1) & 1) ^ 1, p.err))) return false;
 #pragma unroll
           for (int k = 0; k < 16; ++k) s.as[q & 1][b][rows0 + 4 * k] = v[k];
           if (warp == 10 && n < 2) s.bs[q & 1][n][b] = w;
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&s.scale_full[q & 1]));
         }
-      }
+        return true;
+      };
+      walk([&](auto, const Tile& tile) { return tile_scales(tile); });
     }
   }
   tc_fence_before();
@@ -699,9 +735,16 @@ static smla_status_t launch_cluster(void (*kernel)(Args...), unsigned grid, int 
   return e == cudaSuccess ? SMLA_OK : fail_cuda(e, "block matmul launch");
 }
 
+// How many of the wide form's tiles go as halves: a last wave that leaves half of
+// the pairs idle.
+static int64_t tail(int64_t tiles) {
+  const int64_t pairs = device_sm_count() / 2, last = tiles % pairs;
+  return 2 * last <= pairs ? last : 0;
+}
+
 static smla_status_t launch_wide(const MatmulArgs& a, unsigned* err, cudaStream_t stream) {
   Params p = params(a, 256, BN, err);
-  CUtensorMap ta, tb, to;
+  CUtensorMap ta, tb, tb_half, to;
   smla_status_t st = maps(a, 128, BN / 2, &ta, &tb, &p);
   if (st != SMLA_OK) return st;
   const int es = p.out_f32 ? 4 : 2;
@@ -712,8 +755,15 @@ static smla_status_t launch_wide(const MatmulArgs& a, unsigned* err, cudaStream_
   static std::atomic<unsigned long long> ready{0};
   st = prepare_kernel(reinterpret_cast<const void*>(wide_kernel), smem, kWideRegs, ready, "block matmul kernel");
   if (st != SMLA_OK) return st;
+  const int64_t last = tail(p.tiles);
+  p.whole = static_cast<unsigned>(p.tiles - last);
+  p.tiles += last;
+  tb_half = tb;
+  bool flip;
+  if (last && !byte_map(&tb_half, a.b, static_cast<int64_t>(a.N) * a.K, a.K, a.G, a.N, a.K, BN / 4, &flip))
+    return fail(SMLA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the block matmul's half tiles");
   const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(p.tiles, device_sm_count() / 2));
-  return launch_cluster(wide_kernel, 2 * pairs, kWideThreads, smem, 2, stream, ta, tb, to, p);
+  return launch_cluster(wide_kernel, 2 * pairs, kWideThreads, smem, 2, stream, ta, tb, tb_half, to, p);
 }
 
 template <int MT, int CS>
@@ -745,12 +795,14 @@ smla_status_t launch_block_matmul(const MatmulArgs& a, unsigned* err, cudaStream
   };
   const int kb = (a.K + kBK - 1) / kBK;
   // The wide form where it is the faster one: a wave of its tiles takes about 1.5 us
-  // and 0.42 a block, a 64-row tile of the narrow form an SM 1.5 us and 0.27 a block
-  // (narrow / wide: 256 x 4096 x 4096 13.6 / 17.5 us, 512 rows 19.5 / 18.4; 512 x 4096 x
-  // 16384 62 / 58; 128 x 24576 x 2048 21.2 / 23.0, 256 rows 31.7 / 23.6; 128 heads x 64 x
-  // 512 x 128 9.1 / 11.2, 128 rows 16.1 / 11.9).
-  const int64_t waves = (tiles(256, BN) + sms / 2 - 1) / (sms / 2);
-  if (a.M > 32 && waves * (72 + 20 * kb) * sms < tiles(64, 128) * (72 + 13 * kb)) return launch_wide(a, err, stream);
+  // and 0.42 a block (0.27 of halves), a 64-row tile of the narrow form an SM 1.5 us
+  // and 0.27 a block (narrow / wide: 256 x 4096 x 4096 14.1 / 13.5 us, 512 rows 19.1 /
+  // 13.9; 256 x 4096 x 16384 35.6 / 40.4, 512 rows 62 / 40.5; 64 x 24576 x 2048 13.5 /
+  // 18.4, 128 rows 20.7 / 19.5, 256 rows 31.2 / 19.7; 128 heads x 64 x 512 x 128 9.0 /
+  // 11.0, 128 rows 15.1 / 11.4).
+  const int64_t wide = tiles(256, BN), last = tail(wide), waves = (wide - last + sms / 2 - 1) / (sms / 2);
+  const int64_t wide_cost = (waves * (72 + 20 * kb) + (last ? 72 + 13 * kb : 0)) * sms;
+  if (a.M > 32 && wide_cost < tiles(64, 128) * (72 + 13 * kb)) return launch_wide(a, err, stream);
   const auto go = [&](auto mt) {
     constexpr int MT = decltype(mt)::value;
     const int64_t n = tiles(MT, 128);

@@ -73,6 +73,16 @@ def test_product(G, M, N, K, dtype):
     _close(out, av, bv)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("G,M,N,K", [(1, 2050, 2056, 16), (1, 2600, 1800, 272), (1, 2100, 2296, 1296), (3, 700, 2200, 640),
+                                     (1, 4000, 3904, 400), (1, 512, 4104, 2064), (2, 300, 1168, 8192), (1, 257, 8200, 144)])
+def test_whole_and_half_tiles(G, M, N, K, dtype):
+    """Tiles beyond whole waves of the GPU's pairs of CTAs, few of them: the last
+    ones are divided, behind whole ones of one block of columns and of many, and with
+    their second half past N; or all of a call's are."""
+    test_product(G, M, N, K, dtype)
+
+
 @pytest.mark.parametrize("G,M,N,K", [(16, 3, 64, 256), (8, 130, 136, 384), (128, 300, 128, 144)])
 def test_heads_of_a_token_major_tensor(G, M, N, K):
     """Every operand strided as the heads of a [T, H, wider] tensor are; what lies
