@@ -315,13 +315,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (elect_one()) {
         int st = 0;
         uint32_t phase = 0, used = 0;
+        bool ok = true;
         walk([&](auto c, const Tile& tile) {
           constexpr int cols = decltype(c)::value;
           const CUtensorMap* const map = cols == BN ? &tb : &tb_half;
           const int m = tile.m0 + m_of, n = tile.n0 + rank * (cols / 2);
           const int y = p.a_flip ? tile.g : m, z = p.a_flip ? m : tile.g;
           for (int kb = 0; kb < p.kb; ++kb) {
-            if (!mbar_wait(smem_u32(&s.empty[st]), phase ^ 1, p.err)) return false;
+            ok = mbar_wait(smem_u32(&s.empty[st]), phase ^ 1, p.err);
+            if (!ok) return false;
             const uint32_t bar = smem_u32(&s.full[st]);
             mbar_arrive_expect_tx(bar, (128 + cols / 2) * kBK);
             tma_load_3d(smem_u32(s.a[st]), &ta, kb * kBK, y, z, bar);
@@ -334,9 +336,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
           return true;
         });
-        // nothing is still landing when the CTA ends: the last load of each stage
-        for (int k = 0; k < kStages; ++k)
-          if (used >> k & 1) mbar_wait(smem_u32(&s.full[k]), k < st ? phase : phase ^ 1, p.err);
+        // nothing is on its way into this CTA's memory when it ends: each stage's last
+        // load, and the word that the MMAs have read it (which the first CTA's send to
+        // both; its parity is the load's)
+        for (int k = 0; k < kStages; ++k) {
+          if (!(used >> k & 1)) continue;
+          const uint32_t last = k < st ? phase : phase ^ 1;
+          ok = mbar_wait(smem_u32(&s.full[k]), last, p.err) && ok;
+          ok = ok && mbar_wait(smem_u32(&s.empty[k]), last, p.err);
+        }
       }
       __syncwarp();
     } else if (warp == 9) {
@@ -388,10 +396,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
           return true;
         });
-        if (rank == 0) {
-          pair_commit(smem_u32(&s.drain));
-          mbar_wait(smem_u32(&s.drain), 0, p.err);
-        }
+        // (both CTAs wait: the MMAs read the second one's memory too, and tell it so)
+        if (rank == 0) pair_commit(smem_u32(&s.drain));
+        mbar_wait(smem_u32(&s.drain), 0, p.err);
       }
       __syncwarp();
     } else {
