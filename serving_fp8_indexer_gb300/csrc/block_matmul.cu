@@ -65,8 +65,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // where a CTA by itself, which stages all of b, is bound by them (48 KB in and 48
 // KB out a block of 512 MMA cycles: 712 cycles).  Each CTA's TMEM holds its own
 // 128 rows' sums.
-// Warps: 0-7 epilogue (32 rows x BN / 2 columns each), 8 TMA loads, 9 MMAs (in the
-// second CTA: tells the first that a stage has landed), 10-11 a's and b's scales.
+// Warps: 0-7 epilogue (32 rows x BN / 2 columns each), 8 TMA loads (the second CTA's
+// count on the first one's barrier too, which its MMAs wait for), 9 MMAs (in the first
+// CTA), 10-11 a's and b's scales.
 // (The launch's 384 x 168 registers are 128 x (2 x 216 + 72).)
 constexpr int kWideThreads = 384, kWideRegs = 168, kWideSoft = 8, kGroupM = 8;
 static_assert(128 * (2 * 216 + 72) <= kWideThreads * kWideRegs, "the split draws on the launch's registers");
@@ -101,11 +102,20 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// (No release beyond the CTA's: what it tells of are finished TMEM reads and TMA
-// writes, and a cluster-wide one waits for the warp's every store: 765 us at 4096^2 x
-// 16384.)
+// Word to the first CTA of finished TMEM reads, which are over before it is given
+// and leave nothing in memory to be seen.  (No release beyond the CTA's: a
+// cluster-wide one waits for the warp's every store, 765 us at 4096^2 x 16384.)
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A 3-D tiled load into this CTA's shared memory whose bytes count on a barrier of
+// either CTA of the pair (`bar`: an address in the cluster).
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, "
+      "%5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
 }
 // The tcgen05 operations of a pair of CTAs.
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
@@ -123,10 +133,11 @@ __device__ __forceinline__ void pair_mma_f8f6f4(uint32_t d_tmem, uint64_t a_desc
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Arrives on the barrier at this address in both CTAs when the MMAs so far complete.
-__device__ __forceinline__ void pair_commit(uint32_t bar) {
+// Arrives on the barrier at this address in the CTAs of the mask (both) when the MMAs
+// so far complete.
+__device__ __forceinline__ void pair_commit(uint32_t bar, uint16_t ctas = 3) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-               "h"(static_cast<uint16_t>(3))
+               "h"(ctas)
                : "memory");
 }
 
@@ -175,7 +186,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   };
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&s.full[i]), 2 - rank);  // the first CTA's counts the second's landing too
+      mbar_init(smem_u32(&s.full[i]), 1);  // (the first CTA's counts)
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
     for (int i = 0; i < 6; ++i) {
@@ -316,6 +327,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         int st = 0;
         uint32_t phase = 0, used = 0;
         bool ok = true;
+        const uint32_t full0 = cluster_addr(smem_u32(s.full), 0);
         walk([&](auto c, const Tile& tile) {
           constexpr int cols = decltype(c)::value;
           const CUtensorMap* const map = cols == BN ? &tb : &tb_half;
@@ -324,10 +336,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           for (int kb = 0; kb < p.kb; ++kb) {
             ok = mbar_wait(smem_u32(&s.empty[st]), phase ^ 1, p.err);
             if (!ok) return false;
-            const uint32_t bar = smem_u32(&s.full[st]);
-            mbar_arrive_expect_tx(bar, (128 + cols / 2) * kBK);
-            tma_load_3d(smem_u32(s.a[st]), &ta, kb * kBK, y, z, bar);
-            tma_load_3d(smem_u32(s.b[st]), map, kb * kBK, n, tile.g, bar);
+            // (the second CTA's bytes may land ahead of this: the phase is not over
+            // without the arrival)
+            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&s.full[st]), 2 * (128 + cols / 2) * kBK);
+            pair_load_3d(smem_u32(s.a[st]), &ta, kb * kBK, y, z, full0 + 8 * st);
+            pair_load_3d(smem_u32(s.b[st]), map, kb * kBK, n, tile.g, full0 + 8 * st);
             used |= 1u << st;
             if (++st == kStages) {
               st = 0;
@@ -337,24 +350,25 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           return true;
         });
         // nothing is on its way into this CTA's memory when it ends: each stage's last
-        // load, and the word that the MMAs have read it (which the first CTA's send to
-        // both; its parity is the load's)
+        // load, and the word that the MMAs have read it (which comes to both CTAs; its
+        // parity is the load's).  Where a wait has given up, the second CTA's own loads
+        // were issued before that wait began, and are waited for by the first.
         for (int k = 0; k < kStages; ++k) {
           if (!(used >> k & 1)) continue;
           const uint32_t last = k < st ? phase : phase ^ 1;
-          ok = mbar_wait(smem_u32(&s.full[k]), last, p.err) && ok;
+          if (rank == 0) ok = mbar_wait(smem_u32(&s.full[k]), last, p.err) && ok;
           ok = ok && mbar_wait(smem_u32(&s.empty[k]), last, p.err);
         }
       }
       __syncwarp();
     } else if (warp == 9) {
       // =================================================================== MMAs
-      if (elect_one()) {
+      if (rank == 0 && elect_one()) {
         const uint64_t da = make_sdesc(smem_u32(s.a[0]), 16, 1024, kSwizzle128B);
         const uint64_t db = make_sdesc(smem_u32(s.b[0]), 16, 1024, kSwizzle128B);
         // (One thread, whose every instruction the MMAs wait for: nothing is computed
         // that can be carried along.)
-        const uint32_t full0 = smem_u32(s.full), empty0 = smem_u32(s.empty), peer0 = cluster_addr(full0, 0);
+        const uint32_t full0 = smem_u32(s.full), empty0 = smem_u32(s.empty);
         const uint32_t sum_full0 = smem_u32(s.sum_full), sum_empty0 = smem_u32(s.sum_empty);
         int st = 0, buf = 0;
         uint32_t phase = 0, buf_phase = 1;
@@ -363,7 +377,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           constexpr uint32_t IDESC = idesc_e4m3_f32(256, cols, 0, 0);
           constexpr int kSums = 2 * BN / cols, kFirst = cols == BN ? 0 : 2;
           if (cols != BN) {
-            for (int i = 0; rank == 0 && i < 2; ++i) {  // the wider accumulators have been read
+            for (int i = 0; i < 2; ++i) {  // the wider accumulators have been read
               if (!mbar_wait(sum_empty0 + 8 * buf, buf_phase, p.err)) return false;
               buf ^= 1;
               buf_phase ^= buf ^ 1;
@@ -373,22 +387,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
           for (int kb = 0; kb < p.kb; ++kb) {
             if (!mbar_wait(full0 + 8 * st, phase, p.err)) return false;
-            if (rank == 1) {
-              cluster_arrive(peer0 + 8 * st);
-            } else {
-              if (!mbar_wait(sum_empty0 + 8 * (kFirst + buf), buf_phase, p.err)) return false;
-              tc_fence_after();
-              const uint64_t a = da + static_cast<uint64_t>(st * (128 * kBK >> 4));
-              const uint64_t b = db + static_cast<uint64_t>(st * (BN / 2 * kBK >> 4));
+            if (!mbar_wait(sum_empty0 + 8 * (kFirst + buf), buf_phase, p.err)) return false;
+            tc_fence_after();
+            const uint64_t a = da + static_cast<uint64_t>(st * (128 * kBK >> 4));
+            const uint64_t b = db + static_cast<uint64_t>(st * (BN / 2 * kBK >> 4));
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                pair_mma_f8f6f4(tmem + buf * cols, a + static_cast<uint64_t>(2 * k), b + static_cast<uint64_t>(2 * k), IDESC,
-                                k ? 1u : 0u);
-              pair_commit(sum_full0 + 8 * (kFirst + buf));
-              pair_commit(empty0 + 8 * st);
-              buf = (buf + 1) % kSums;
-              buf_phase ^= buf == 0;
-            }
+            for (int k = 0; k < 4; ++k)
+              pair_mma_f8f6f4(tmem + buf * cols, a + static_cast<uint64_t>(2 * k), b + static_cast<uint64_t>(2 * k), IDESC,
+                              k ? 1u : 0u);
+            pair_commit(sum_full0 + 8 * (kFirst + buf));
+            pair_commit(empty0 + 8 * st);
+            buf = (buf + 1) % kSums;
+            buf_phase ^= buf == 0;
             if (++st == kStages) {
               st = 0;
               phase ^= 1;
@@ -396,8 +406,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
           return true;
         });
-        // (both CTAs wait: the MMAs read the second one's memory too, and tell it so)
-        if (rank == 0) pair_commit(smem_u32(&s.drain));
+        pair_commit(smem_u32(&s.drain), 1);  // (the second CTA's loads have waited for theirs)
         mbar_wait(smem_u32(&s.drain), 0, p.err);
       }
       __syncwarp();

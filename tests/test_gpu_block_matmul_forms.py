@@ -55,3 +55,20 @@ def test_calls_on_end_of_pairs_that_end_early(G, M, N, K):
     _close(outs[0], av, bv)
     assert all(torch.equal(outs[0], o) for o in outs)
     assert all(torch.equal(xb[0], q) for q in xb) and all(torch.equal(xs[0], s) for s in xs)
+
+
+@pytest.mark.parametrize("M,N,K", [(2300, 4096, 1040), (600, 2600, 2064)])
+def test_new_operands_in_the_same_stages(M, N, K):
+    """Products of new operands call after call: bytes that the second CTA of a pair has
+    loaded are the ones that the first one's MMAs read, not those of the block or
+    call before."""
+    assert _wide(1, M, N, K)
+    g = _gen(M)
+    b, sb, bv = _operand(g, 1, N, K, False)
+    calls = [_operand(g, 1, M, K, True) for _ in range(6)]
+    outs = [torch.full((M, N), float("nan"), device="cuda") for _ in calls]
+    for (a, sa, _), o in zip(calls, outs):
+        smla.block_matmul(a[0], sa[0], b[0], sb[0], o)
+    smla.check_device_errors()
+    for (_, _, av), o in zip(calls, outs):
+        _close(o[None], av, bv)
