@@ -522,7 +522,8 @@ smla_status_t smla_quantize_blocks(const uint16_t* x, int64_t x_stride, int32_t 
  * K: a multiple of 16, 16 .. 2^20; N a multiple of 8, up to 2^28.  Strides: a's
  * multiples of 16, out's of 8, at least the row's width; out's rows may not share
  * memory (its larger stride spans the other dimension), nor may out and an operand.
- * A stride of a dimension of one element does not matter.  Alignment: a, b, out 16
+ * A stride of a dimension of one element does not matter, nor does any where G, M
+ * or N is 0 (nothing is done then).  Alignment: a, b, out 16
  * bytes; the scales 4.  A result does not depend on the run, nor on the other rows of a
  * or b, but may differ in its last bits with the numbers of rows (G, M, N), by which
  * the order of its sum over k is chosen. */

@@ -292,6 +292,7 @@ smla_status_t smla_block_matmul(const uint8_t* a, int64_t a_group_stride, int64_
   }
   if (out_dtype != SMLA_BF16 && out_dtype != SMLA_F32)
     return fail(SMLA_ERR_INVALID_ARG, "out_dtype=%d must be bf16 or f32", out_dtype);
+  if (G == 0 || M == 0 || N == 0) return SMLA_OK;  // (nor have empty tensors)
   const auto wide_enough = [](int64_t n, int64_t s, int64_t width) { return n <= 1 || s >= width; };
   constexpr int64_t kFar = int64_t(1) << 38;
   if (!wide_enough(M, a_row_stride, K) || !wide_enough(G, a_group_stride, K) || a_row_stride % 16 || a_group_stride % 16 ||
@@ -301,7 +302,6 @@ smla_status_t smla_block_matmul(const uint8_t* a, int64_t a_group_stride, int64_
   if (!wide_enough(M, out_row_stride, N) || !wide_enough(G, out_group_stride, N) || !stride8(out_row_stride) ||
       !stride8(out_group_stride) || out_row_stride >= kFar || out_group_stride >= kFar)
     return fail(SMLA_ERR_INVALID_ARG, "out's strides must be multiples of 8 below 2^38, at least N");
-  if (G == 0 || M == 0 || N == 0) return SMLA_OK;
   // rows of different batches share no memory: one of the two strides spans the other's range
   const __int128 rows_span = static_cast<__int128>(M - 1) * out_row_stride + N;
   const __int128 groups_span = static_cast<__int128>(G - 1) * out_group_stride + N;
