@@ -445,7 +445,8 @@ smla_status_t smla_dense_decode(const void* q, int32_t q_dtype, const void* late
  *   bytes   0..287  e2m1 codes (sign, two exponent bits, one mantissa bit: 0, 0.5,
  *                   1, 1.5, 2, 3, 4, 6), the even column in the low four bits
  *   bytes 288..305  shifts, four bits for each block of 16 columns, the even
- *                   block in the low four; 0..14, and 15 for a block of zeros
+ *                   block in the low four: 0..14; 15 is read as a block of zeros
+ *                   whatever its codes
  *   bytes 306..307  0
  *   bytes 308..311  scale, f32
  *   bytes 312..319  0
@@ -458,8 +459,10 @@ smla_status_t smla_dense_decode(const void* q, int32_t q_dtype, const void* late
  *   scale = largest finite magnitude of r / 384 (1 when that is 0; at least the
  *           smallest normal f32)
  *   shift = the largest k in 0..14 for which the block's largest finite magnitude
- *           times 2^k is at most the row's
+ *           times 2^k is at most the row's (14 for a block whose finite values are all
+ *           0; 15 is never written)
  *   code  = e2m1(r / scale * 2^(shift - 6)), to nearest even, of the f32 quotient
+ *           (below a scale of 2^-100, of one that may be off in its last place)
  * Infinities become the block's +-6; a row with a NaN gets the scale NaN.
  *   pool  [phys_rows, 320] (output), 16-byte aligned
  * The other arguments, the order of the steps and the rules as for smla_cache_append. */

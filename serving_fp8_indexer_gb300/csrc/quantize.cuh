@@ -36,8 +36,9 @@ SMLA_DEVICE_INLINE float quotient(float v, float scale, float inv) {
 // low half), two zero bytes, the row's scale in f32, eight zero bytes.
 //   value = e2m1 * 2^(6 - shift) * scale
 // scale = largest magnitude / 384, so the row's largest value is 6 * 2^6 units, and
-// shift (0..14; 15 stands for a block of zeros) is the largest that keeps the
-// block's within 6 code units.  e2m1 * 2^(6 - shift) is an e4m3 number for every
+// shift (0..14) is the largest that keeps the block's within 6 code units: 14 for a
+// block of zeros.  15 is never written; readers take such a block as zeros whatever
+// its codes.  e2m1 * 2^(6 - shift) is an e4m3 number for every
 // code and shift (0.5 * 2^-8 is e4m3's smallest): attention reads the row on the
 // FP8 pipe as it is held, with the scale by the row.
 constexpr int kFp4Row = 320, kFp4Shifts = 288, kFp4Scale = 308, kFp4Blocks = 36;
