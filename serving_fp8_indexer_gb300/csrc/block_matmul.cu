@@ -13,7 +13,8 @@
 //   256.  A thread of the epilogue owns half a tile's row, so a block's scale is one
 //   number for it.  Persistent pairs walk the tiles in groups of eight row tiles.  A
 //   last wave that would leave half of the pairs idle goes as halves of 256 x 128, with
-//   four accumulators (4096 x 4096 x 16384 218 -> 202 us, 512 rows of it 60 -> 42.7).
+//   four accumulators (4096 x 4096 x 16384 218 -> 202 us when they came, 512 rows of it
+//   60 -> 42.7).
 // * narrow, for calls whose few rows leave the wide form's tiles too few to fill
 //   the GPU: rows of b (the weights, which are what such a call reads) are the M,
 //   rows of a the N (16, 32 or 64).  The CTAs of a cluster divide the columns k of a
@@ -22,7 +23,9 @@
 //
 // Bound and measured.  Wide: the epilogue's warps, whose waits, TMEM loads and
 // multiply-adds follow one another, 870 cycles a block of 256 x 256 (MMAs 512): 4096 x
-// 4096 x 16384 202 us (2720 TFLOP/s), 8192^3 378 us (2910); with four blocks a tile and 269 MB to store, 4101 x 32768 x 512 97 us (a fill of as much 72).
+// 4096 x 16384 196-198 us (2790 TFLOP/s), 512 rows of it 38.4, 8192^3 376 (2920); with
+// four blocks a tile and 269 MB to store, 4101 x 32768 x 512 97 us (a fill of as much 72).
+// The heads of 4096 tokens, 128 x (4096 x 512 x 128): 108 us, of which HBM takes 92.
 // (Slower or the same: one CTA's MMAs with b by multicast 216 us for 217; 16 epilogue
 // warps of 64 columns 228; each load one piece ahead, over the end of a block, 237.)
 // Narrow: HBM behind 4 us of start and end, 16 x 4096 x 16384 14.5 us (4.6 TB/s),
@@ -78,7 +81,8 @@ constexpr int BN = 256;
 
 struct WideSmem {
   // a stage's way round takes 1.5 us: what is in flight sets a half tile's rate (512 x
-  // 4096 x 16384: 50 us with four, 42.7)
+  // 4096 x 16384: 50 us with four for 42.7, before the loads of the second CTA counted
+  // on the first one's barrier; 38.4 since)
   static constexpr int kStages = 5;
   // places for 64 bytes of an epilogue warp's 32 rows on their way out (4101 x 32768 x
   // 512 with one, and a stage more: 106 us for 101)
@@ -109,7 +113,9 @@ __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // A 3-D tiled load into this CTA's shared memory whose bytes count on a barrier of
-// either CTA of the pair (`bar`: an address in the cluster).
+// either CTA of the pair (`bar`: an address in the cluster).  (Told of by a thread of
+// the second CTA instead they took 199 us for 196 at 4096^2 x 16384, with a release of
+// CTA scope, which promises nothing to another CTA, and 453 with one of the cluster's.)
 __device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, "
@@ -812,10 +818,11 @@ smla_status_t launch_block_matmul(const MatmulArgs& a, unsigned* err, cudaStream
   const int kb = (a.K + kBK - 1) / kBK;
   // The wide form where it is the faster one: a wave of its tiles takes about 1.5 us
   // and 0.42 a block (0.27 of halves), a 64-row tile of the narrow form an SM 1.5 us
-  // and 0.27 a block (narrow / wide: 256 x 4096 x 4096 14.1 / 13.5 us, 512 rows 19.1 /
-  // 13.9; 256 x 4096 x 16384 35.6 / 40.4, 512 rows 62 / 40.5; 64 x 24576 x 2048 13.5 /
-  // 18.4, 128 rows 20.7 / 19.5, 256 rows 31.2 / 19.7; 128 heads x 64 x 512 x 128 9.0 /
-  // 11.0, 128 rows 15.1 / 11.4).
+  // and 0.27 a block (narrow / wide: 256 x 4096 x 4096 14.2 / 13.7 us, 512 rows 19.2 /
+  // 14.0; 256 x 4096 x 16384 35.6 / 38.1, 512 rows 62 / 38.1; 64 x 24576 x 2048 14.0 /
+  // 18.2, 128 rows 20.5 / 19.2, 256 rows 31.7 / 19.8; 128 heads x 64 x 512 x 128 10.2 /
+  // 12.1, 128 rows 16.9 / 12.4; where the choice costs most, of 33 sizes: 1000 x 1000 x
+  // 992, narrow, 8.5 / 6.7).
   const int64_t wide = tiles(256, BN), last = tail(wide), waves = (wide - last + sms / 2 - 1) / (sms / 2);
   const int64_t wide_cost = (waves * (72 + 20 * kb) + (last ? 72 + 13 * kb : 0)) * sms;
   if (a.M > 32 && wide_cost < tiles(64, 128) * (72 + 13 * kb)) return launch_wide(a, err, stream);
