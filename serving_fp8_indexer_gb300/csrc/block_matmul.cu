@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
           return true;
         });
-        pair_commit(smem_u32(&s.drain), 1);  // (the second CTA's loads have waited for theirs)
+        pair_commit(smem_u32(&s.drain), 1);  // (the second CTA ends by its loads' waits)
         mbar_wait(smem_u32(&s.drain), 0, p.err);
       }
       __syncwarp();
